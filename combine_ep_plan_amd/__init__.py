@@ -25,10 +25,15 @@ EP_ERR_HIP = -4
 EP_STATUS_BAD_EXPERT = 1
 EP_STATUS_CAPACITY = 2
 EP_STATUS_BAD_REGION = 4
+EP_STATUS_BAD_PAGE = 8
 EP_PAYLOAD_BF16 = 0
 EP_PAYLOAD_FP8_B128 = 1
 EP_KV_STATIC_SLOTS = 64
 EP_PROBE_COPY, EP_PROBE_FILL, EP_PROBE_READ, EP_PROBE_SCATTER, EP_PROBE_SCATTER_WIDE = range(5)
+EP_KV_MAX_REQUESTS = 16384
+EP_DTYPE_BF16, EP_DTYPE_F16, EP_DTYPE_E4M3 = range(3)
+EP_ROPE_HALF, EP_ROPE_INTERLEAVED = range(2)
+EP_ROPE_NONE, EP_ROPE_LINEAR, EP_ROPE_NTK, EP_ROPE_YARN = range(4)
 EP_PROBE_NT_LOADS, EP_PROBE_XCD, EP_PROBE_ONE_WAVE = 1, 2, 4
 
 # Every entry point the C header declares (checked by the tests).
@@ -43,6 +48,8 @@ EXPORTS = (
     "ep_expert_stub", "ep_combine",
     "ep_combine_presum", "ep_kv_plan", "ep_kv_push", "ep_kv_push_staged",
     "ep_kv_push_staged_static",
+    "ep_kv_pages_bytes", "ep_kv_extend", "ep_kv_fork", "ep_kv_free", "ep_kv_compact",
+    "ep_kv_copy_pages", "ep_rope_freqs", "ep_kv_append", "ep_kv_attend_bytes", "ep_kv_attend",
     "ep_probe_copy", "ep_probe_pattern", "ep_status_string",
     "ep_last_error",
 )
@@ -68,6 +75,57 @@ class PlanView(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "cnt", "send_off", "send_pos", "recv_off", "grp_off", "grp_pos",
         "src_off", "comb_row", "grp_slot", "send_slot", "recv_rows", "send_seg", "win_list")]
+
+
+class KvPages(ctypes.Structure):
+    """ep_kv_pages: tables, lens, refs and pool of a paged cache (see make_kv_pages)."""
+    _fields_ = [
+        ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("refs", ctypes.c_void_p),
+        ("pool", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_pages", ctypes.c_int32),
+        ("page_tokens", ctypes.c_int32), ("ranks", ctypes.c_int32), ("reserved", ctypes.c_int32),
+        ("page_bytes", ctypes.c_int64), ("rank_bytes", ctypes.c_int64),
+    ]
+
+
+class KvCache(ctypes.Structure):
+    """ep_kv_cache: K and V of one layer in the pages of a pool (see make_kv_cache)."""
+    _fields_ = [
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("page_stride", ctypes.c_int64), ("token_stride", ctypes.c_int64),
+        ("head_stride", ctypes.c_int64),
+        ("n_pages", ctypes.c_int32), ("page_tokens", ctypes.c_int32), ("n_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32), ("dtype", ctypes.c_int32), ("reserved", ctypes.c_int32),
+    ]
+
+
+class KvBatch(ctypes.Structure):
+    """ep_kv_batch: tables, lengths and row offsets of the sequences of one step."""
+    _fields_ = [
+        ("tables", ctypes.c_void_p), ("lens", ctypes.c_void_p), ("q_off", ctypes.c_void_p),
+        ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32), ("n_tokens", ctypes.c_int32),
+        ("dtype", ctypes.c_int32),
+    ]
+
+
+class Rows(ctypes.Structure):
+    """ep_rows: [tokens][heads][head_dim] rows by their byte strides."""
+    _fields_ = [("p", ctypes.c_void_p), ("token_stride", ctypes.c_int64),
+                ("head_stride", ctypes.c_int64)]
+
+
+class Rope(ctypes.Structure):
+    """ep_rope: pair frequencies and layout of rotary positions (see make_rope)."""
+    _fields_ = [("inv_freq", ctypes.c_void_p), ("rot_dim", ctypes.c_int32),
+                ("layout", ctypes.c_int32), ("mscale", ctypes.c_float),
+                ("reserved", ctypes.c_int32)]
+
+
+class KvGroups(ctypes.Structure):
+    """ep_kv_groups: ranges of sequences that share their leading tokens."""
+    _fields_ = [("group_off", ctypes.c_void_p), ("shared", ctypes.c_void_p),
+                ("n_groups", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 def _load() -> ctypes.CDLL:
@@ -111,6 +169,24 @@ def _load() -> ctypes.CDLL:
                                              ctypes.c_int32, P, P, P]),
         "ep_kv_push_staged_static": (ctypes.c_int, [ctypes.c_int32, P, I64, I64, P, I64, P, I64,
                                                     ctypes.c_int32, P, P, P]),
+        "ep_kv_pages_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvPages), I64]),
+        "ep_kv_extend": (ctypes.c_int, [ctypes.POINTER(KvPages), P, P, I64, P, P, P]),
+        "ep_kv_fork": (ctypes.c_int, [ctypes.POINTER(KvPages), P, P, I64, P, P, P]),
+        "ep_kv_free": (ctypes.c_int, [ctypes.POINTER(KvPages), P, I64, P, P, P]),
+        "ep_kv_compact": (ctypes.c_int, [ctypes.POINTER(KvPages), P, P, P, P]),
+        "ep_kv_copy_pages": (ctypes.c_int, [ctypes.POINTER(KvPages), P, P, I64, P, P, P]),
+        "ep_rope_freqs": (ctypes.c_int, [ctypes.c_int32, ctypes.c_double, ctypes.c_int32,
+                                         ctypes.c_double, ctypes.c_double, ctypes.c_double,
+                                         ctypes.c_double, P, ctypes.POINTER(ctypes.c_float)]),
+        "ep_kv_append": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
+                                        ctypes.POINTER(Rows), ctypes.c_int32,
+                                        ctypes.POINTER(Rows), ctypes.POINTER(Rows),
+                                        ctypes.POINTER(Rows), ctypes.POINTER(Rope), P, P]),
+        "ep_kv_attend_bytes": (ctypes.c_size_t, [ctypes.POINTER(KvCache)] + [ctypes.c_int32] * 5),
+        "ep_kv_attend": (ctypes.c_int, [ctypes.POINTER(KvCache), ctypes.POINTER(KvBatch),
+                                        ctypes.POINTER(KvGroups), ctypes.c_int32,
+                                        ctypes.POINTER(Rows), ctypes.c_int32,
+                                        ctypes.POINTER(Rows), P, ctypes.c_float, P, P, P]),
         "ep_probe_copy": (ctypes.c_int, [P, P, ctypes.c_size_t, P]),
         "ep_probe_pattern": (ctypes.c_int, [P, P, P, I64, I64, I64, I64, ctypes.c_int,
                                             ctypes.c_int, ctypes.c_int, ctypes.c_int, I64, P]),
@@ -367,6 +443,190 @@ def kv_push_staged_static(ranks: int, regions, n_regions: int, total_bytes: int,
                                          _addr(dst_pool), int(dst_rank_bytes), int(bounce_slots),
                                          _addr(notify), _addr(status), _stream(stream)),
            "ep_kv_push_staged_static")
+
+
+# ---------------------------------------------------------------------------
+# Paged KV cache: page state, rotary append, attention
+# ---------------------------------------------------------------------------
+
+def _ints(t, shape, name: str):
+    """Address of a contiguous int32 tensor of the given shape (None: any size)."""
+    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
+    if str(t.dtype) != "torch.int32":
+        raise ValueError(f"{name} must be int32, not {t.dtype}")
+    return _addr(t)
+
+
+def make_kv_pages(tables, lens, refs, pool, page_tokens: int) -> KvPages:
+    """Page state from tables [n_seqs, max_pages], lens [n_seqs], refs [n_pages] (int32) and a
+    contiguous pool [ranks, n_pages, ...]; all of them are read and changed in place."""
+    seqs, n_pages = tables.shape[0], refs.shape[0]
+    if pool.dim() < 3 or pool.shape[1] != n_pages:
+        raise ValueError(f"pool has shape {tuple(pool.shape)}, not [ranks, {n_pages}, ...]")
+    page_bytes = pool[0, 0].numel() * pool.element_size()
+    g = KvPages(_ints(tables, (None, None), "tables"), _ints(lens, (seqs,), "lens"),
+                _ints(refs, (None,), "refs"), _addr(pool), seqs, tables.shape[1], n_pages,
+                int(page_tokens), pool.shape[0], 0, page_bytes, n_pages * page_bytes)
+    g.tensors = (tables, lens, refs, pool)   # they live as long as the addresses are used
+    return g
+
+
+def kv_pages_bytes(g: KvPages, m: int) -> int:
+    return int(_lib.ep_kv_pages_bytes(ctypes.byref(g), int(m)))
+
+
+def kv_extend(g: KvPages, seqs, add, ws, status, stream=None) -> None:
+    m = seqs.numel()
+    _check(_lib.ep_kv_extend(ctypes.byref(g), _ints(seqs, (m,), "seqs"), _ints(add, (m,), "add"),
+                             m, _addr(ws), _addr(status), _stream(stream)), "ep_kv_extend")
+
+
+def kv_fork(g: KvPages, parents, children, ws, status, stream=None) -> None:
+    m = parents.numel()
+    _check(_lib.ep_kv_fork(ctypes.byref(g), _ints(parents, (m,), "parents"),
+                           _ints(children, (m,), "children"), m, _addr(ws), _addr(status),
+                           _stream(stream)), "ep_kv_fork")
+
+
+def kv_free(g: KvPages, seqs, ws, status, stream=None) -> None:
+    m = seqs.numel()
+    _check(_lib.ep_kv_free(ctypes.byref(g), _ints(seqs, (m,), "seqs"), m, _addr(ws),
+                           _addr(status), _stream(stream)), "ep_kv_free")
+
+
+def kv_compact(g: KvPages, ws, status, n_live=None, stream=None) -> None:
+    _check(_lib.ep_kv_compact(ctypes.byref(g), _addr(n_live), _addr(ws), _addr(status),
+                              _stream(stream)), "ep_kv_compact")
+
+
+def kv_copy_pages(g: KvPages, src, dst, ws, status, stream=None) -> None:
+    m = src.numel()
+    _check(_lib.ep_kv_copy_pages(ctypes.byref(g), _ints(src, (m,), "src"), _ints(dst, (m,), "dst"),
+                                 m, _addr(ws), _addr(status), _stream(stream)),
+           "ep_kv_copy_pages")
+
+
+def _dtype(t, name: str) -> int:
+    import torch
+    codes = {torch.bfloat16: EP_DTYPE_BF16, torch.float16: EP_DTYPE_F16,
+             torch.float8_e4m3fn: EP_DTYPE_E4M3}
+    if t.dtype not in codes:
+        raise ValueError(f"{name} has dtype {t.dtype}: bfloat16, float16 or float8_e4m3fn are taken")
+    return codes[t.dtype]
+
+
+def _dense_rows(t, dims: int, name: str) -> None:
+    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} and strides {t.stride()}: {dims} axes, "
+                         "the last one dense, are taken")
+
+
+def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
+    """One layer's cache from k and v [n_pages, page_tokens, n_heads, head_dim]: strided views of
+    a pool, with equal strides. float8_e4m3fn ones take a float32 scale per head each."""
+    _dense_rows(k, 4, "k")
+    _dense_rows(v, 4, "v")
+    if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
+        raise ValueError("k and v must have equal shapes, strides and dtypes")
+    es = k.element_size()
+    for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
+        if s is not None and (tuple(s.shape) != (k.shape[2],) or str(s.dtype) != "torch.float32"):
+            raise ValueError(f"{name} must be float32 [{k.shape[2]}]")
+    c = KvCache(k.data_ptr(), v.data_ptr(), _addr(k_scale), _addr(v_scale), k.stride(0) * es,
+                k.stride(1) * es, k.stride(2) * es, k.shape[0], k.shape[1], k.shape[2],
+                k.shape[3], _dtype(k, "k"), 0)
+    c.tensors = (k, v, k_scale, v_scale)
+    return c
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = EP_ROPE_NONE,
+               factor: float = 1.0, orig_tokens: float = 0.0, beta_fast: float = 32.0,
+               beta_slow: float = 1.0):
+    """Host-only pair frequencies: (float32 numpy array [rot_dim / 2], mscale)."""
+    import numpy as np
+    out = np.zeros(max(int(rot_dim) // 2, 1), np.float32)
+    mscale = ctypes.c_float()
+    _check(_lib.ep_rope_freqs(int(rot_dim), float(base), int(scaling), float(factor),
+                              float(orig_tokens), float(beta_fast), float(beta_slow),
+                              out.ctypes.data, ctypes.byref(mscale)), "ep_rope_freqs")
+    return out, mscale.value
+
+
+def make_rope(inv_freq, rot_dim: int, layout: int = EP_ROPE_HALF, mscale: float = 1.0) -> Rope:
+    """Rotary positions from a float32 tensor of rot_dim / 2 frequencies."""
+    if str(inv_freq.dtype) != "torch.float32" or inv_freq.numel() != int(rot_dim) // 2:
+        raise ValueError(f"inv_freq must be float32 [{int(rot_dim) // 2}]")
+    r = Rope(_addr(inv_freq), int(rot_dim), int(layout), float(mscale), 0)
+    r.tensors = (inv_freq,)
+    return r
+
+
+def _rows(t, name: str) -> Rows:
+    _dense_rows(t, 3, name)
+    es = t.element_size()
+    return Rows(t.data_ptr(), t.stride(0) * es, t.stride(1) * es)
+
+
+def _batch(cache: KvCache, tables, lens, q_off, rows, n_heads) -> KvBatch:
+    """The batch of `rows`, name: tensor, each [tokens, n_heads[name], head_dim] of one dtype."""
+    seqs = tables.shape[0]
+    first = next(iter(rows.values()))
+    for name, t in rows.items():
+        want = (first.shape[0], n_heads[name], cache.head_dim)
+        if tuple(t.shape) != want or t.dtype != first.dtype:
+            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, not {first.dtype} {want}")
+    return KvBatch(_ints(tables, (None, None), "tables"), _ints(lens, (seqs,), "lens"),
+                   None if q_off is None else _ints(q_off, (seqs + 1,), "q_off"), seqs,
+                   tables.shape[1], first.shape[0], _dtype(first, "rows"))
+
+
+def kv_append(cache: KvCache, tables, lens, q_off, q, k, v, q_out, rope, status,
+              stream=None) -> None:
+    """Rotate the new tokens' q into q_out (which may be q) and write their rotated k, and v, to
+    the pages. q and q_out None: only k and v. rope None: no rotation. q_off None: one new token
+    per sequence."""
+    kv = cache.n_heads
+    rows, heads = {"k": k, "v": v}, {"k": kv, "v": kv}
+    if (q is None) != (q_out is None):
+        raise ValueError("q and q_out must be given together")
+    if q is not None:
+        rows.update(q=q, q_out=q_out)
+        heads.update(q=q.shape[1], q_out=q.shape[1])
+    b = _batch(cache, tables, lens, q_off, rows, heads)
+    _check(_lib.ep_kv_append(
+        ctypes.byref(cache), ctypes.byref(b), None if q is None else _rows(q, "q"),
+        0 if q is None else q.shape[1], _rows(k, "k"), _rows(v, "v"),
+        None if q is None else _rows(q_out, "q_out"), None if rope is None else ctypes.byref(rope),
+        _addr(status), _stream(stream)), "ep_kv_append")
+
+
+def kv_attend_bytes(cache: KvCache, n_seqs: int, n_groups: int, n_tokens: int, n_heads: int,
+                    max_new: int = 1) -> int:
+    return int(_lib.ep_kv_attend_bytes(ctypes.byref(cache), int(n_seqs), int(n_groups),
+                                       int(n_tokens), int(n_heads), int(max_new)))
+
+
+def kv_attend(cache: KvCache, tables, lens, q_off, max_new: int, group_off, shared, q, out, lse,
+              sm_scale: float, ws, status, stream=None) -> None:
+    """Attention of the new tokens' q over their pages into out, and lse (or None). group_off and
+    shared (or both None): ranges of sequences that share their leading tokens."""
+    heads = q.shape[1]
+    b = _batch(cache, tables, lens, q_off, {"q": q, "out": out}, {"q": heads, "out": heads})
+    if (group_off is None) != (shared is None):
+        raise ValueError("group_off and shared must be given together")
+    groups = None
+    if shared is not None:
+        n = shared.numel()
+        groups = KvGroups(_ints(group_off, (n + 1,), "group_off"), _ints(shared, (n,), "shared"),
+                          n, 0)
+    if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or
+                            str(lse.dtype) != "torch.float32"):
+        raise ValueError(f"lse must be float32 {tuple(q.shape[:2])}")
+    _check(_lib.ep_kv_attend(
+        ctypes.byref(cache), ctypes.byref(b), None if groups is None else ctypes.byref(groups),
+        int(max_new), _rows(q, "q"), heads, _rows(out, "out"), _addr(lse), float(sm_scale),
+        _addr(ws), _addr(status), _stream(stream)), "ep_kv_attend")
 
 
 def probe_copy(dst, src, nbytes: int, stream=None) -> None:

@@ -695,6 +695,7 @@ const char* ep_status_string(int code) {
     case EP_STATUS_BAD_EXPERT | EP_STATUS_CAPACITY:
       return "expert id out of range and receive capacity exceeded";
     case EP_STATUS_BAD_REGION: return "KV region outside its pools (skipped)";
+    case EP_STATUS_BAD_PAGE: return "page, sequence or length out of range (skipped)";
     default: return "unknown code";
   }
 }

@@ -130,6 +130,34 @@ hipError_t launch_kv_push_staged(int ranks, const ep_kv_region* reg, int64_t m, 
                                  const void* src, int64_t src_rank_bytes, void* dst,
                                  int64_t dst_rank_bytes, void* bounce, int64_t round_bytes,
                                  int32_t* notify, int32_t* status, hipStream_t stream);
+// Pages of a KV cache. Workspace arrays (int32): pages [n_pages], src and dst
+// [n_pages / 2 + 1], first [n_seqs], start and len [m], counts [chunks + 1].
+struct PagesWs {
+  int32_t *pages, *src, *dst, *first, *start, *len, *counts;
+};
+constexpr int kKvCompactChunk = 2048;  // pages per block of a compaction's passes
+int64_t kv_page_pieces(int64_t page_bytes);
+hipError_t launch_kv_extend(const ep_kv_pages& g, const int32_t* seqs, const int32_t* add, int m,
+                            const PagesWs& ws, int32_t* status, hipStream_t stream);
+hipError_t launch_kv_fork(const ep_kv_pages& g, const int32_t* parents, const int32_t* children,
+                          int m, const PagesWs& ws, int32_t* status, hipStream_t stream);
+hipError_t launch_kv_free(const ep_kv_pages& g, const int32_t* seqs, int m, int32_t* status,
+                          hipStream_t stream);
+hipError_t launch_kv_compact(const ep_kv_pages& g, int32_t* n_live, const PagesWs& ws,
+                             int32_t* status, hipStream_t stream);
+hipError_t launch_kv_copy_pages(const ep_kv_pages& g, const int32_t* src, const int32_t* dst,
+                                int m, const PagesWs& ws, int32_t* status, hipStream_t stream);
+// New tokens over one layer's pages (arguments validated by the ABI layer;
+// no rotation: rope.rot_dim 0; no queries: q.p null).
+hipError_t launch_kv_append(const ep_kv_cache& c, const ep_kv_batch& b, const ep_rows& q,
+                            int n_heads, const ep_rows& k, const ep_rows& v, const ep_rows& q_out,
+                            const ep_rope& rope, int32_t* status, hipStream_t stream);
+size_t kv_attend_bytes(const ep_kv_cache& c, int n_seqs, int n_groups, int n_tokens, int n_heads,
+                       int max_new);
+hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep_kv_groups& g,
+                            int max_new, const ep_rows& q, int n_heads, const ep_rows& out,
+                            float* lse, float sm_scale, void* ws, int32_t* status,
+                            hipStream_t stream);
 hipError_t launch_probe_copy(void* dst, const void* src, size_t bytes,
                              hipStream_t stream);
 

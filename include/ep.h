@@ -77,6 +77,7 @@ extern "C" {
 #define EP_STATUS_BAD_EXPERT 1 /* an expert id outside [0, E): slot dropped */
 #define EP_STATUS_CAPACITY 2   /* a rank would receive more than cap rows */
 #define EP_STATUS_BAD_REGION 4 /* a KV region outside its pools: skipped */
+#define EP_STATUS_BAD_PAGE 8   /* a page, sequence or length outside its range */
 
 /* Payload formats of the dispatched rows. */
 #define EP_PAYLOAD_BF16 0     /* one plane: H bf16 values, 2H bytes per row */
@@ -421,6 +422,216 @@ EP_API int ep_kv_push_staged_static(int32_t ranks, const ep_kv_region *regions,
                                     void *dst_pool, int64_t dst_rank_bytes,
                                     int32_t bounce_slots, int32_t *notify,
                                     int32_t *status, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * Pages of a KV cache on the decoder: the pool that ep_kv_push fills, its
+ * page tables and its reference counts, all in device memory and changed in
+ * stream order, so that a serving step can be captured into a graph.
+ *
+ * Token i of sequence b lives in slot i % page_tokens of page
+ * tables[b][i / page_tokens]; a sequence of lens[b] tokens uses the first
+ * ceil(lens[b] / page_tokens) entries of its row, and the calls below leave
+ * -1 behind them. Page p is free when refs[p] <= 0; otherwise refs[p] table
+ * entries (or other holders) use it. There is no list of free pages: a call
+ * that needs pages takes the free ones with the lowest ids, in request
+ * order, so equal states give equal results.
+ *
+ * Each call takes m requests as device arrays (m <= EP_KV_MAX_REQUESTS) and
+ * a workspace of ep_kv_pages_bytes(g, m) bytes (16-byte aligned) that holds
+ * nothing between calls; calls that may overlap need one each. A request
+ * that names a sequence or a page out of range, or a length that the table
+ * cannot hold, is skipped and sets EP_STATUS_BAD_PAGE. Of several requests
+ * for one sequence the first counts, the others are skipped and flagged.
+ * ---------------------------------------------------------------------- */
+typedef struct ep_kv_pages {
+  int32_t *tables;     /* [n_seqs][max_pages] */
+  int32_t *lens;       /* [n_seqs] */
+  int32_t *refs;       /* [n_pages] */
+  void *pool;          /* page p of rank r at r * rank_bytes + p * page_bytes */
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t ranks;       /* pools that share the tables (ranks, or layers) */
+  int32_t reserved;    /* 0 */
+  int64_t page_bytes;  /* a multiple of 16 */
+  int64_t rank_bytes;  /* a multiple of 16, >= n_pages * page_bytes */
+} ep_kv_pages;
+
+#define EP_KV_MAX_REQUESTS 16384
+
+/* Workspace bytes of the calls below for up to m requests; 0 if g or m is
+ * invalid. */
+EP_API size_t ep_kv_pages_bytes(const ep_kv_pages *g, int64_t m);
+
+/* seqs[i] grows by add[i] >= 0 tokens: lens follows and the pages that the
+ * new tokens need are appended to its row with a count of 1. Requests are
+ * granted in order while free pages last: request i is refused when the
+ * needs of requests 0..i together exceed the free pages and it needs any; a
+ * refused request changes nothing and sets EP_STATUS_CAPACITY. The pool is
+ * not touched. A last page that is partly filled must be the sequence's own
+ * (ep_kv_fork leaves it so). */
+EP_API int ep_kv_extend(const ep_kv_pages *g, const int32_t *seqs,
+                        const int32_t *add, int64_t m, void *ws,
+                        int32_t *status, hipStream_t stream);
+
+/* children[i], an empty sequence (lens 0), becomes a copy of parents[i] as
+ * it was before the call: it shares the parent's full pages (their counts
+ * rise by one) and gets a page of its own with the bytes of the partly
+ * filled last one, in every rank. Children are granted in order while free
+ * pages last, as in ep_kv_extend; a refused child stays empty and sets
+ * EP_STATUS_CAPACITY. A child that is not empty is skipped and flagged. */
+EP_API int ep_kv_fork(const ep_kv_pages *g, const int32_t *parents,
+                      const int32_t *children, int64_t m, void *ws,
+                      int32_t *status, hipStream_t stream);
+
+/* seqs[i] becomes empty: the counts of its pages fall by one (never below
+ * 0; a page already at 0 sets EP_STATUS_BAD_PAGE), its row becomes -1. */
+EP_API int ep_kv_free(const ep_kv_pages *g, const int32_t *seqs, int64_t m,
+                      void *ws, int32_t *status, hipStream_t stream);
+
+/* Moves the used pages to the front of the pool. With L used pages, the
+ * k-th used page at or above L (ascending) moves to the k-th free page below
+ * L, in every rank; tables and refs follow, and pages L .. n_pages - 1 are
+ * free afterwards. Nothing else moves. n_live (optional, device): L. Other
+ * holders of page ids (a prefix store) find the new id of page p in the
+ * first n_pages int32 of ws: -1 if it did not move. */
+EP_API int ep_kv_compact(const ep_kv_pages *g, int32_t *n_live, void *ws,
+                         int32_t *status, hipStream_t stream);
+
+/* Copies page src[i] to page dst[i] in every rank; counts and tables do not
+ * change. A pair is skipped and flagged when an id is out of range, when an
+ * earlier pair writes the same dst, or when its src is the dst of another
+ * pair (pairs with src == dst do nothing and hinder no other). */
+EP_API int ep_kv_copy_pages(const ep_kv_pages *g, const int32_t *src,
+                            const int32_t *dst, int64_t m, void *ws,
+                            int32_t *status, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * New tokens of a batch over the pages of one layer: rotary positions and
+ * the write of K and V (ep_kv_append), and attention (ep_kv_attend).
+ *
+ * Sequence b has lens[b] tokens including its new ones, which are its last
+ * q_off[b + 1] - q_off[b]; row q_off[b] + j of q, k, v and out belongs to
+ * position lens[b] - (q_off[b + 1] - q_off[b]) + j. Rows at or behind
+ * q_off[n_seqs] belong to no sequence: nothing reads them and they are left
+ * as they were. A table entry outside [0, n_pages), or a position behind
+ * max_pages * page_tokens, sets EP_STATUS_BAD_PAGE; its token is neither
+ * written nor attended to.
+ * ---------------------------------------------------------------------- */
+#define EP_DTYPE_BF16 0
+#define EP_DTYPE_F16 1
+#define EP_DTYPE_E4M3 2 /* OCP e4m3fn; caches only */
+
+/* K and V of one layer: element d of head h of slot t of page p lies at
+ * p * page_stride + t * token_stride + h * head_stride bytes, d dense. All
+ * strides and both bases are multiples of 16 bytes. An e4m3 cache holds
+ * x / scale[h] (one scale per head and side); otherwise the scales are NULL. */
+typedef struct ep_kv_cache {
+  void *k;
+  void *v;
+  const float *k_scale;
+  const float *v_scale;
+  int64_t page_stride;
+  int64_t token_stride;
+  int64_t head_stride;
+  int32_t n_pages;
+  int32_t page_tokens;
+  int32_t n_heads;
+  int32_t head_dim;    /* a multiple of 8 (16 for e4m3), at most 256 */
+  int32_t dtype;
+  int32_t reserved;    /* 0 */
+} ep_kv_cache;
+
+typedef struct ep_kv_batch {
+  const int32_t *tables; /* [n_seqs][max_pages] */
+  const int32_t *lens;   /* [n_seqs] */
+  const int32_t *q_off;  /* [n_seqs + 1] ascending from 0; NULL: one new token each */
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t n_tokens;      /* rows of q, k, v and out */
+  int32_t dtype;         /* EP_DTYPE_BF16 or EP_DTYPE_F16, of those rows */
+} ep_kv_batch;
+
+/* Rows [n_tokens][heads][head_dim], the last axis dense; strides in bytes,
+ * multiples of 16, the base too. */
+typedef struct ep_rows {
+  void *p;
+  int64_t token_stride;
+  int64_t head_stride;
+} ep_rows;
+
+#define EP_ROPE_HALF 0        /* pairs (i, i + rot_dim / 2) */
+#define EP_ROPE_INTERLEAVED 1 /* pairs (2 i, 2 i + 1) */
+
+/* Pair i < rot_dim / 2 of the leading rot_dim elements of a head turns by
+ * position * inv_freq[i] radians (taken in 64 bits, so that far positions
+ * lose nothing) and is multiplied by mscale; the others stay as they are. */
+typedef struct ep_rope {
+  const float *inv_freq; /* device [rot_dim / 2] */
+  int32_t rot_dim;       /* even, at most head_dim */
+  int32_t layout;
+  float mscale;
+  int32_t reserved;      /* 0 */
+} ep_rope;
+
+#define EP_ROPE_NONE 0
+#define EP_ROPE_LINEAR 1 /* frequencies / factor */
+#define EP_ROPE_NTK 2    /* base * factor^(rot_dim / (rot_dim - 2)) */
+#define EP_ROPE_YARN 3   /* high frequencies kept, low ones / factor, a ramp between */
+
+/* Host only. inv_freq[i] = base^(-2 i / rot_dim), i < rot_dim / 2, changed
+ * by the scaling; *mscale is 1, or 0.1 ln(factor) + 1 for YaRN. YaRN's ramp
+ * runs over the pairs that turn between beta_fast and beta_slow times in
+ * orig_tokens positions (both ends rounded outwards to whole pairs). */
+EP_API int ep_rope_freqs(int32_t rot_dim, double base, int32_t scaling,
+                         double factor, double orig_tokens, double beta_fast,
+                         double beta_slow, float *inv_freq, float *mscale);
+
+/* q_out = rotated q; rotated k and v go to the new tokens' slots, rounded
+ * once to the cache's type (nearest even; e4m3 saturates at 448). rope NULL:
+ * no rotation. q_out may be q itself (same strides) but may not overlap it
+ * otherwise; q and q_out both with p NULL: only k and v are handled. The
+ * slots must be the sequence's own (refs 1), as ep_kv_extend leaves them. */
+EP_API int ep_kv_append(const ep_kv_cache *c, const ep_kv_batch *b,
+                        const ep_rows *q, int32_t n_heads, const ep_rows *k,
+                        const ep_rows *v, const ep_rows *q_out,
+                        const ep_rope *rope, int32_t *status,
+                        hipStream_t stream);
+
+/* Sequences that share leading pages: group j is sequences
+ * group_off[j] .. group_off[j + 1] - 1, whose rows of the table agree over
+ * their first shared[j] tokens. Those are read through the row of the
+ * group's first sequence, once for all its rows. n_groups 0: nothing is
+ * shared. Sequences outside group_off[0] .. group_off[n_groups] - 1 share
+ * nothing. */
+typedef struct ep_kv_groups {
+  const int32_t *group_off; /* [n_groups + 1], ascending */
+  const int32_t *shared;    /* [n_groups] */
+  int32_t n_groups;
+  int32_t reserved;         /* 0 */
+} ep_kv_groups;
+
+/* Workspace bytes of ep_kv_attend; 0 if the sizes are invalid. max_new: the
+ * most new tokens any sequence has. */
+EP_API size_t ep_kv_attend_bytes(const ep_kv_cache *c, int32_t n_seqs,
+                                 int32_t n_groups, int32_t n_tokens,
+                                 int32_t n_heads, int32_t max_new);
+
+/* Causal attention of the new tokens over their sequences' pages (the new
+ * tokens' own K and V are there: append first). Head h reads KV head
+ * h / (n_heads / c->n_heads). With s_i = sm_scale * q . k_i over positions
+ * i <= the row's own: lse = log sum exp s_i, out = sum exp(s_i - lse) v_i,
+ * rounded once from 32-bit sums. A row that sees nothing gets zeros and -inf.
+ * lse: float [n_tokens][n_heads], or NULL. Tokens of a sequence behind its
+ * first max_new ones are skipped and set EP_STATUS_BAD_PAGE.
+ * The workspace (16-byte aligned) holds nothing between calls; calls that
+ * may overlap, graphs among them, need one each. */
+EP_API int ep_kv_attend(const ep_kv_cache *c, const ep_kv_batch *b,
+                        const ep_kv_groups *groups, int32_t max_new,
+                        const ep_rows *q, int32_t n_heads, const ep_rows *out,
+                        float *lse, float sm_scale, void *ws, int32_t *status,
+                        hipStream_t stream);
 
 /* Stand-in for the grouped GEMM (outside the method; used by tests and the
  * benchmark to produce expert outputs). expert_out is bf16 [N][cap][H].
