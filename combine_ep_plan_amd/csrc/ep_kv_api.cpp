@@ -362,6 +362,10 @@ size_t ep_kv_attend_bytes(const ep_kv_cache* c, int32_t n_seqs, int32_t n_groups
     fail(EP_ERR_INVALID_ARG, "ep_kv_attend_bytes: bad sizes");
     return 0;
   }
+  if ((int64_t)n_tokens * n_heads >= (int64_t)1 << 31) {
+    fail(EP_ERR_UNSUPPORTED, "n_tokens * n_heads must be < 2^31");
+    return 0;
+  }
   return ep::kv_attend_bytes(*c, n_seqs, n_groups, n_tokens, n_heads, max_new);
 }
 
@@ -377,8 +381,8 @@ int ep_kv_attend(const ep_kv_cache* c, const ep_kv_batch* b, const ep_kv_groups*
   if (groups) g = *groups;
   if (g.n_groups < 0 || g.reserved != 0)
     return fail(EP_ERR_INVALID_ARG, "groups: bad sizes, or reserved not 0");
-  if (mul(b->n_tokens, (int64_t)n_heads * c->head_dim * 4) < 0)
-    return fail(EP_ERR_UNSUPPORTED, "too many rows");
+  if ((int64_t)b->n_tokens * n_heads >= (int64_t)1 << 31)
+    return fail(EP_ERR_UNSUPPORTED, "n_tokens * n_heads must be < 2^31");
   DeviceScope scope(stream);
   if (scope.error() != hipSuccess) return fail_hip(scope.error(), "device");
   const int dev = scope.device();

@@ -1,20 +1,53 @@
-// Attention of new tokens over the pages of a cache.
+// Attention of new tokens over the pages of a cache, leading pages that
+// sequences share being read once for all of them.
 //
 // With s_i = scale q.k_i over the keys a row sees, m = max s_i and
-// l = sum exp(s_i - m): out = sum exp(s_i - m) v_i / l, lse = m + log l. One
-// pass over the keys keeps m, l and the sum, and scales them by
-// exp(m_old - m_new) when the maximum grows.
+// l = sum exp(s_i - m): out = sum exp(s_i - m) v_i / l, lse = m + log l.
+// Both sums are associative once rescaled to a common m, so the keys of a
+// row may be cut anywhere: pieces keep (m, l, sum) in 32 bits and a second
+// launch joins them.
 //
-// One wave takes one row and head: a lane scores one key of 64, then owns
-// every 64th element of the output.
+// Units. A prefix unit is a group: all its rows (new tokens x the query heads
+// of one KV head) over the shared keys. A suffix unit is a sequence: its rows
+// over the keys behind them. Units are cut into items of at most kRows rows
+// and one KV head, items into tiles of kTile keys.
+//
+// Work. The tiles of all items stand in one line, weighted by what they cost,
+// and each of the launch's workgroups takes an equal length of it, whatever
+// the lengths of the sequences: no list of work is kept, every workgroup sums
+// the units itself (two loads per unit). A workgroup's part of an item is a
+// piece; workgroup w's piece of item i has number w + i, which no other piece
+// has, since both only grow along the line.
+//
+// Matrix products. Scores are formed transposed, S^T = K Q^T, with 32x32x16
+// products: a lane then holds 16 keys of one row, so that maximum, sum and
+// rescale need no more than one exchange between lanes l and l + 32, and the
+// probabilities are already laid out as the second operand of
+// O^T += V^T P^T. The k order of that product is a free choice as long as
+// both sides take it: slot (half h, j) of its step s is key 16 s + 8 (j / 4)
+// + 4 h + j % 4, the order the scores come out in. V is read from LDS through
+// the transposing read, four keys of one column per lane.
 #include "ep_kernels.hpp"
 #include "ep_kv_device.hpp"
 
 namespace ep {
 namespace {
 
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef uint8_t __attribute__((address_space(3))) lds_u8;
+
 constexpr int kBlock = 256;
-constexpr int kMaxDim = 256;
+constexpr int kWaves = kBlock / kWave;
+constexpr int kTile = 128;       // keys of a tile
+constexpr int kNone = 0x7fffffff;
+constexpr int kRowsSplit = 32;   // rows of an item whose keys the waves share out
+constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
+// Weights of a tile of either kind.
+constexpr int kCostSplit = 1;
+constexpr int kCostBlock = 1;
 
 struct Attend {
   ep_kv_cache c;
@@ -23,123 +56,1022 @@ struct Attend {
   ep_rows q, out;
   float* lse;
   float scale;
-  int heads, max_new;
+  int heads, share, max_new;  // share: query heads per KV head
+  int workers;
+  // Workspace: per unit its place in the line and its first item, the
+  // line's length, and the pieces' sums and (m, l) by number and row.
+  int64_t* line;
+  int32_t* items;
+  float* sum[2];      // [0]: prefix pieces, [1]: suffix pieces
+  float2* stat[2];
+  int pieces[2], rows[2];  // pieces that fit, rows of each
   int32_t* status;
 };
 
-template <int QT, int CT>
-__global__ __launch_bounds__(kBlock) void attend_kernel(Attend a) {
-  __shared__ float q[kBlock / kWave][kMaxDim];
-  __shared__ float prob[kBlock / kWave][kWave];
-  __shared__ int64_t slot[kBlock / kWave][kWave];
-  const int wave = wave_uniform(threadIdx.x / kWave), lane = lane_id();
-  const int64_t unit = (int64_t)blockIdx.x * (kBlock / kWave) + wave;
-  const int row = wave_uniform((int)(unit / a.heads)), head = wave_uniform((int)(unit % a.heads));
-  const int s = row < a.b.n_tokens ? seq_of_row(a.b, row) : -1;
-  int64_t n = 0;
-  bool skip = s < 0;
-  bool bad = false;
-  const int dim = a.c.head_dim, bt = a.c.page_tokens;
-  if (s >= 0) {
-    const int first = first_row(a.b, s), end = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
-    n = (int64_t)a.b.lens[s] - (end - first) + (row - first) + 1;
-    if (row - first >= a.max_new) skip = bad = true;
-    const int64_t cap = (int64_t)a.b.max_pages * bt;
-    if (n > cap) {
-      n = cap;
-      bad = true;
-    }
-    const uint8_t* p = (const uint8_t*)a.q.p + row * a.q.token_stride + head * a.q.head_stride;
-    for (int d = lane; d < dim; d += kWave) q[wave][d] = load1<QT>(p + 2 * d) * a.scale;
+// ---------------------------------------------------------------------------
+// Units
+// ---------------------------------------------------------------------------
+struct Unit {
+  int row0, rows;     // first new token, rows per KV head
+  int lo, hi;         // keys
+  int tile_rows;      // rows of an item
+  int items;          // items per KV head
+  int tiles;          // tiles of an item
+  int cost;           // of a tile
+  bool is_short;      // suffix: the shared keys reach past the first new token
+};
+
+__device__ __forceinline__ int clamp_int(int64_t v, int64_t lo, int64_t hi) {
+  return (int)(v < lo ? lo : v > hi ? hi : v);
+}
+
+__device__ __forceinline__ int key_cap(const Attend& a) {
+  const int64_t cap = (int64_t)a.b.max_pages * a.c.page_tokens;
+  return cap < 0x7fffffff ? (int)cap : 0x7fffffff;
+}
+
+// The group of sequence s, or -1.
+__device__ __forceinline__ int group_of(const Attend& a, int s) {
+  int lo = 0, hi = a.g.n_groups;  // last group that starts at or before s
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (a.g.group_off[mid] <= s) lo = mid;
+    else hi = mid;
   }
-  const int kvh = head / (a.heads / a.c.n_heads);
-  const uint8_t* kb = (const uint8_t*)a.c.k + kvh * a.c.head_stride;
-  const uint8_t* vb = (const uint8_t*)a.c.v + kvh * a.c.head_stride;
-  const float ks = CT == EP_DTYPE_E4M3 ? a.c.k_scale[kvh] : 1.0f;
-  const float vs = CT == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f;
-  float m = -__builtin_inff(), l = 0.0f, o[kMaxDim / kWave] = {};
-  for (int64_t t0 = 0; !skip && t0 < n; t0 += kWave) {
-    const int64_t t = t0 + lane;
-    int64_t at = -1;
-    if (t < n) {
-      const int32_t p = a.b.tables[(int64_t)s * a.b.max_pages + t / bt];
-      if (p >= 0 && p < a.c.n_pages)
-        at = p * a.c.page_stride + (t % bt) * a.c.token_stride;
-      else
-        bad = true;
-    }
-    float x = -__builtin_inff();
-    if (at >= 0) {
-      x = 0.0f;
-      for (int d = 0; d < dim; d += 8) {
-        float f[8];
-        load8<CT>(kb + at + d * Fmt<CT>::bytes, f);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x += f[i] * q[wave][d + i];
-      }
-      x *= ks;
-    }
-    float top = x;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
-    top = fmaxf(top, m);
-    if (top == -__builtin_inff()) continue;
-    const float w = __expf(m - top), e = at >= 0 ? __expf(x - top) : 0.0f;
-    float sum = e;
-#pragma unroll
-    for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
-    m = top;
-    l = l * w + sum;
-    prob[wave][lane] = e;
-    slot[wave][lane] = at;
-#pragma unroll
-    for (int i = 0; i < kMaxDim / kWave; ++i) o[i] *= w;
-    for (int j = 0; j < kWave; ++j) {
-      const int64_t sj = slot[wave][j];
-      if (sj < 0) continue;
-      const float pj = prob[wave][j];
-#pragma unroll
-      for (int i = 0; i < kMaxDim / kWave; ++i) {
-        const int d = lane + i * kWave;
-        if (d < dim) o[i] += pj * load1<CT>(vb + sj + d * Fmt<CT>::bytes);
+  return lo < a.g.n_groups && a.g.group_off[lo] <= s && s < a.g.group_off[lo + 1] ? lo : -1;
+}
+
+// First new token of sequence s and their number; 0 where the offsets are
+// not those of a batch.
+__device__ __forceinline__ int new_of(const Attend& a, int s, int* row0) {
+  const int lo = a.b.q_off ? a.b.q_off[s] : s, hi = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
+  *row0 = lo;
+  return lo >= 0 && hi > lo && hi <= a.b.n_tokens ? hi - lo : 0;
+}
+
+__device__ __forceinline__ Unit unit_of(const Attend& a, int u) {
+  Unit t;
+  t.is_short = false;
+  if (u < a.g.n_groups) {
+    const int s0 = a.g.group_off[u], s1 = a.g.group_off[u + 1];
+    t.row0 = t.rows = t.lo = t.hi = 0;
+    if (s0 >= 0 && s0 < s1 && s1 <= a.b.n_seqs) {
+      const int lo = a.b.q_off ? a.b.q_off[s0] : s0;
+      int hi = a.b.q_off ? a.b.q_off[s1] : s1;
+      if (!a.b.q_off && hi > a.b.n_tokens) hi = a.b.n_tokens;
+      if (lo >= 0 && lo < hi && hi <= a.b.n_tokens) {
+        t.row0 = lo;
+        t.rows = (hi - lo) * a.share;
+        t.hi = clamp_int(a.g.shared[u], 0, key_cap(a));
       }
     }
+  } else {
+    const int s = u - a.g.n_groups;
+    const int n = new_of(a, s, &t.row0), len = a.b.lens[s];
+    t.rows = (n < a.max_new ? n : a.max_new) * a.share;
+    const int j = group_of(a, s);
+    const int shared = j >= 0 ? a.g.shared[j] : 0;
+    t.lo = clamp_int(shared, 0, key_cap(a));
+    t.hi = clamp_int(len, t.lo, key_cap(a));
+    t.is_short = (int64_t)len - n + 1 < shared;
   }
-  if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
-  if (skip) return;
-  uint8_t* to = (uint8_t*)a.out.p + row * a.out.token_stride + head * a.out.head_stride;
-  const float inv = l > 0.0f ? vs / l : (l == 0.0f ? 0.0f : l);
+  const bool split = t.rows <= kRowsSplit;
+  t.tile_rows = split ? kRowsSplit : kRowsBlock;
+  t.cost = split ? kCostSplit : kCostBlock;
+  t.items = (t.rows + t.tile_rows - 1) / t.tile_rows;
+  t.tiles = t.items > 0 ? (int)(((int64_t)t.hi - t.lo + kTile - 1) / kTile) : 0;
+  return t;
+}
+
+__device__ __forceinline__ int64_t unit_length(const Attend& a, const Unit& u) {
+  return (int64_t)u.items * a.c.n_heads * u.tiles * u.cost;
+}
+
+// Workgroup w takes [begin(w), begin(w + 1)) of a line of n.
+__device__ __forceinline__ int64_t begin_of(const Attend& a, int64_t w, int64_t n) {
+  return w * n / a.workers;
+}
+__device__ __forceinline__ int worker_of(const Attend& a, int64_t x, int64_t n) {
+  return (int)(((x + 1) * a.workers - 1) / n);
+}
+
+// Tiles of an item that starts at `at` whose first points lie before x.
+__device__ __forceinline__ int tiles_before(const Unit& u, int64_t at, int64_t x) {
+  return clamp_int((x - at + u.cost - 1) / u.cost, 0, u.tiles);
+}
+
+// ---------------------------------------------------------------------------
+// Tiles in LDS. Rows of DP elements of 16 bits in chunks of 16 bytes; chunk c
+// of key t lies at chunk place_k(t, c) or place_v(t, c) of its row, so that
+// the reads below spread over the banks.
+// ---------------------------------------------------------------------------
+// K is read by 32 lanes that hold 32 keys, chunk 2 step + half of each.
+template <int DP>
+__device__ __forceinline__ int place_k(int t, int c) {
+  return DP == 64 ? c ^ ((t >> 1) & 7) : c ^ (t & 15);
+}
+// V is read as 64 bytes (4 chunks) of 4 consecutive keys per half wave.
+template <int DP>
+__device__ __forceinline__ int place_v(int t, int c) {
+  return DP == 64 ? c ^ ((((t >> 1) & 1) << 2) | ((t >> 2) & 3))
+                  : c ^ (((t & 3) << 2) | ((t >> 2) & 3));
+}
+
+// Sixteen e4m3 values as 16-bit ones (exact).
+template <int QT>
+__device__ __forceinline__ void widen(const u32x4& in, u32x4 out[2]) {
 #pragma unroll
-  for (int i = 0; i < kMaxDim / kWave; ++i) {
-    const int d = lane + i * kWave;
-    if (d < dim) store1<QT>(to + 2 * d, o[i] * inv);
+  for (int i = 0; i < 4; ++i) {
+    const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(in[i], false);
+    const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(in[i], true);
+    uint32_t w0, w1;
+    if constexpr (QT == EP_DTYPE_BF16) {
+      w0 = __builtin_amdgcn_perm(__float_as_uint(lo[1]), __float_as_uint(lo[0]), 0x07060302u);
+      w1 = __builtin_amdgcn_perm(__float_as_uint(hi[1]), __float_as_uint(hi[0]), 0x07060302u);
+    } else {
+      w0 = as<uint32_t>(__builtin_amdgcn_cvt_pkrtz(lo[0], lo[1]));
+      w1 = as<uint32_t>(__builtin_amdgcn_cvt_pkrtz(hi[0], hi[1]));
+    }
+    out[i / 2][2 * (i % 2)] = w0;
+    out[i / 2][2 * (i % 2) + 1] = w1;
   }
-  if (a.lse && lane == 0)
-    a.lse[(int64_t)row * a.heads + head] = l == 0.0f ? -__builtin_inff() : m + __logf(l);
+}
+
+// Zeroes the infinities and NaN of a chunk; returns whether there were any.
+template <int QT>
+__device__ __forceinline__ bool drop_special(u32x4& v) {
+  constexpr uint32_t ex = QT == EP_DTYPE_BF16 ? 0x7f80u : 0x7c00u;
+  bool any = false;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    uint32_t w = v[i];
+    if ((w & ex) == ex) {
+      w &= 0xffff0000u;
+      any = true;
+    }
+    if ((w & (ex << 16)) == ex << 16) {
+      w &= 0xffffu;
+      any = true;
+    }
+    v[i] = w;
+  }
+  return any;
+}
+
+// KEYS rows of K and V on their way from the pages to LDS, by THREADS threads.
+template <int DP, int QT, int CT, int KEYS, int THREADS>
+struct Stage {
+  static constexpr int cb = Fmt<CT>::bytes;
+  static constexpr int chunks = DP * cb / 16;  // 16-byte chunks of a row in the cache
+  static constexpr int step = THREADS / chunks;
+  static constexpr int n = KEYS / step;
+  static_assert(THREADS % chunks == 0 && KEYS % step == 0, "a pass takes whole rows");
+  u32x4 k[n], v[n];
+
+  // slot: this lane's key's byte offset, lane i holding key i (mod KEYS);
+  // -1: none. Rows without a slot and chunks past the head read the
+  // cache's first bytes instead (always in range) and are zeroed later.
+  __device__ __forceinline__ void load(const uint8_t* kb, const uint8_t* vb, int64_t slot, int tid,
+                                       int head_bytes) {
+    const int c = tid % chunks * 16;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int64_t at = __shfl(slot, tid / chunks + j * step);
+      const int64_t off = at >= 0 && c < head_bytes ? at + c : 0;
+      k[j] = *(const u32x4*)(kb + off);
+      v[j] = *(const u32x4*)(vb + off);
+    }
+  }
+
+  // Writes both tiles. CHECK: infinities and NaN of V go to LDS as zeros;
+  // returns the lowest key (of this thread's) that holds one, else kNone.
+  template <bool CHECK>
+  __device__ __forceinline__ int store(uint8_t* lk, uint8_t* lv, uint64_t valid, int tid,
+                                       int head_bytes) const {
+    const int c = tid % chunks;
+    const int whole = c * 16 < head_bytes ? -1 : 0;
+    int special = kNone;
+#pragma unroll
+    for (int j = 0; j < n; ++j) {
+      const int t = tid / chunks + j * step;
+      const uint32_t keep = (uint32_t)(whole & -(int)((valid >> t) & 1));
+      const u32x4 x = k[j] & keep, y = v[j] & keep;
+      if constexpr (CT == EP_DTYPE_E4M3) {
+        u32x4 wx[2], wy[2];
+        widen<QT>(x, wx);
+        widen<QT>(y, wy);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (CHECK && drop_special<QT>(wy[i]) && t < special) special = t;
+          *(u32x4*)(lk + t * DP * 2 + place_k<DP>(t, 2 * c + i) * 16) = wx[i];
+          *(u32x4*)(lv + t * DP * 2 + place_v<DP>(t, 2 * c + i) * 16) = wy[i];
+        }
+      } else {
+        u32x4 z = y;
+        if (CHECK && drop_special<QT>(z) && t < special) special = t;
+        *(u32x4*)(lk + t * DP * 2 + place_k<DP>(t, c) * 16) = x;
+        *(u32x4*)(lv + t * DP * 2 + place_v<DP>(t, c) * 16) = z;
+      }
+    }
+    return special;
+  }
+};
+
+template <int QT>
+__device__ __forceinline__ f32x16 product(const s16x8& x, const s16x8& y, const f32x16& z) {
+  if constexpr (QT == EP_DTYPE_BF16)
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(as<bf16x8>(x), as<bf16x8>(y), z, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_32x32x16_f16(as<f16x8>(x), as<f16x8>(y), z, 0, 0, 0);
+}
+
+// What a wave keeps of 32 rows: lane l holds row l % 32; register r of block
+// dt of `o` is element 32 dt + 8 (r / 4) + 4 (l / 32) + r % 4 of it.
+template <int DP>
+struct Rows32 {
+  s16x8 q[DP / 16];
+  f32x16 o[DP / 32];
+  float m, l;      // of scores as the product gives them; l of this lane's keys
+  int limit;       // keys below it are seen
+  int row;         // in the unit; -1: none
+
+  __device__ __forceinline__ void clear() {
+    m = -__builtin_inff();
+    l = 0.0f;
+#pragma unroll
+    for (int i = 0; i < DP / 32; ++i) o[i] = f32x16{};
+  }
+};
+
+__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+
+// Key of register i, among 32.
+__device__ __forceinline__ int key_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
+
+// NS * 32 keys in LDS at lk and lv. c > 0: the factor of the scores in powers
+// of two. masked: some row does not see some of the keys; bit t of `see` says
+// whether this lane's row sees key t.
+template <int DP, int QT, int NS>
+__device__ __forceinline__ void step(Rows32<DP>& r, const uint8_t* lk, const uint8_t* lv, float c,
+                                     bool masked, uint64_t see) {
+  const int lane = lane_id(), half = lane / 32, col = lane % 32;
+  f32x16 s[NS];
+#pragma unroll
+  for (int n = 0; n < NS; ++n) {
+    s[n] = f32x16{};
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int t = 32 * n + col;
+      const s16x8 k = *(const s16x8*)(lk + t * DP * 2 + place_k<DP>(t, 2 * i + half) * 16);
+      s[n] = product<QT>(k, r.q[i], s[n]);
+    }
+  }
+  if (masked) {
+#pragma unroll
+    for (int n = 0; n < NS; ++n) {
+      const int bits = (int)(uint32_t)(see >> (32 * n + 4 * half));
+#pragma unroll
+      for (int i = 0; i < 16; ++i) {
+        const uint32_t keep = (uint32_t)(bits << (31 - (8 * (i / 4) + i % 4)) >> 31);
+        s[n][i] = __uint_as_float((__float_as_uint(s[n][i]) & keep) | (~keep & 0xff800000u));
+      }
+    }
+  }
+  float top = r.m;
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
+  top = fmaxf(top, other_half(top));
+  if (ballot(top > r.m)) {
+    // exp2(-inf) = 0 where nothing was seen before; rows that still see
+    // nothing keep their zeros whatever the factor is.
+    const float w = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((r.m - top) * c);
+    r.l *= w;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r.o[d][i] *= w;
+    r.m = top;
+  }
+  const float base = top == -__builtin_inff() ? 0.0f : top * c;
+  float sum = 0.0f;
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+      s[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, -base));
+      sum += s[n][i];
+    }
+  r.l += sum;
+  const lds_u8* v0 = (const lds_u8*)lv;
+  const int i16 = lane % 16, part = (lane / 16) % 2;
+#pragma unroll
+  for (int n = 0; n < NS; ++n)
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      // The weights meet V in the rows' 16-bit type: half a step of it,
+      // relative, per weight; the sum of weights is taken before.
+      s16x8 p;
+      if constexpr (QT == EP_DTYPE_BF16) {
+        bf16x8 w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = (__bf16)s[n][8 * k + j];
+        p = as<s16x8>(w);
+      } else {
+        f16x8 w;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) w[j] = (_Float16)s[n][8 * k + j];
+        p = as<s16x8>(w);
+      }
+      const int t = 32 * n + 16 * k + 4 * half + i16 / 4;
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d) {
+        const int ch = 4 * d + 2 * part + i16 % 4 / 2, in = i16 % 2 * 8;
+        typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
+        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(v0 + t * DP * 2 + place_v<DP>(t, ch) * 16 + in));
+        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (lds_s16x4*)(v0 + (t + 8) * DP * 2 + place_v<DP>(t + 8, ch) * 16 + in));
+        s16x8 v;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          v[j] = lo[j];
+          v[4 + j] = hi[j];
+        }
+        r.o[d] = product<QT>(v, p, r.o[d]);
+      }
+    }
+}
+
+// Bits of the keys t0 .. t0 + 63 below `limit`.
+__device__ __forceinline__ uint64_t below(int limit, int64_t t0) {
+  const int64_t n = limit - t0;
+  return n >= 64 ? ~0ull : n <= 0 ? 0 : (1ull << n) - 1;
+}
+
+struct Shared {
+  int64_t start[kBlock + 1];  // of the units of a round, in the line
+  int32_t item[kBlock + 1];   // first item of each
+  int64_t part[kWaves];
+  int32_t ipart[kWaves];
+  int32_t any_short, special;
+  float stat[2][kWaves][32];
+};
+
+// Bytes of LDS that the tiles take: a workgroup's two halves, or the waves'
+// own tiles.
+template <int DP>
+struct Lds {
+  static constexpr int keys = 64;                      // keys of a block step
+  static constexpr int half = keys * DP * 2;           // K or V of one
+  static constexpr int buffers = DP <= 128 ? 2 : 1;
+  static constexpr int block = 2 * half * buffers;
+  static constexpr int wave = 2 * 32 * DP * 2;         // K and V of 32 keys
+  static constexpr int bytes = block > kWaves * wave ? block : kWaves * wave;
+};
+
+template <int DP, int QT, int CT>
+struct Body {
+  const Attend& a;
+  Shared& sh;
+  uint8_t* lds;
+  Unit u;
+  bool prefix;
+  int unit, kvh, index, lo_tile, hi_tile;  // index: of the item in its KV head
+  int table_row;
+  const uint8_t *kb, *vb;
+  float c;  // factor of the scores, in powers of two; positive
+  bool negate;
+  int head_bytes;
+
+  // Byte offset of key t's slot, or -1.
+  __device__ __forceinline__ int64_t slot_of(int64_t t, bool* bad) const {
+    if (t >= u.hi) return -1;
+    const uint32_t page = (uint32_t)t / (uint32_t)a.c.page_tokens;
+    const int32_t p = a.b.tables[(int64_t)table_row * a.b.max_pages + page];
+    if (p < 0 || p >= a.c.n_pages) {
+      *bad = true;
+      return -1;
+    }
+    return p * a.c.page_stride +
+           (int64_t)((uint32_t)t - page * (uint32_t)a.c.page_tokens) * a.c.token_stride;
+  }
+
+  __device__ __forceinline__ int token_of(int row) const { return u.row0 + row / a.share; }
+  __device__ __forceinline__ int head_of(int row) const {
+    return kvh * a.share + row % a.share;
+  }
+
+  __device__ __forceinline__ void load_rows(Rows32<DP>& r, int row0) const {
+    const int lane = lane_id(), half = lane / 32;
+    const int row = row0 + lane % 32;
+    r.clear();
+    r.row = row < u.rows ? row : -1;
+    const int have = row < u.rows ? row : u.rows - 1;
+    const int token = token_of(have);
+    // Rows past the unit's end see what the unit holds, so that they ask
+    // for no masking.
+    r.limit = u.hi;
+    if (!prefix) {
+      const int s = unit - a.g.n_groups;
+      int first;
+      const int n = new_of(a, s, &first);
+      const int64_t pos = (int64_t)a.b.lens[s] - n + (token - first);
+      r.limit = clamp_int(pos + 1, 0, u.hi);
+    } else if (sh.any_short) {
+      int lo = a.g.group_off[unit], hi = a.g.group_off[unit + 1];
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) / 2;
+        if ((a.b.q_off ? a.b.q_off[mid] : mid) <= token) lo = mid;
+        else hi = mid;
+      }
+      int first;
+      const int n = new_of(a, lo, &first);
+      const int64_t pos = (int64_t)a.b.lens[lo] - n + (token - first);
+      r.limit = clamp_int(pos + 1, 0, u.hi);
+    }
+    const uint8_t* p = (const uint8_t*)a.q.p + (int64_t)token * a.q.token_stride +
+                       (int64_t)head_of(have) * a.q.head_stride;
+#pragma unroll
+    for (int i = 0; i < DP / 16; ++i) {
+      const int d = 16 * i + 8 * half;
+      u32x4 w = {0, 0, 0, 0};
+      if (d < a.c.head_dim) w = *(const u32x4*)(p + 2 * d);
+      if (negate) w ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
+      r.q[i] = as<s16x8>(w);
+    }
+  }
+
+  // The fewest keys that a row of the wave sees.
+  __device__ __forceinline__ int least_limit(const Rows32<DP>& r) const {
+    int v = r.limit;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const int o = __shfl_xor(v, d);
+      v = o < v ? o : v;
+    }
+    return wave_uniform(v);
+  }
+
+  // Infinities and NaN of V at keys that some rows may not see went to LDS as
+  // zeros, since 0 * inf would reach those rows. Here the rows that see such
+  // a key get them: a positive weight changes neither. Keys [t0, end).
+  __device__ __forceinline__ void add_special(Rows32<DP>& r, int64_t t0, int64_t end) const {
+    const int half = lane_id() / 32;
+    for (int64_t t = t0; t < end; ++t) {
+      bool bad = false;
+      const int64_t at = slot_of(t, &bad);
+      if (at < 0 || t >= r.limit) continue;
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d) {
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+          const int e = 32 * d + key_of(i, half);
+          if (e >= a.c.head_dim) continue;
+          const float x = load1<CT>(vb + at + e * Fmt<CT>::bytes);
+          if (!(fabsf(x) < __builtin_inff())) r.o[d][i] += x;
+        }
+        __builtin_amdgcn_sched_barrier(0);  // not all loads at once
+      }
+    }
+  }
+
+  // Rows to their place: the output where this piece is all there is, else
+  // the piece's sums.
+  __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole) const {
+    const int lane = lane_id(), half = lane / 32;
+    if (r.row < 0) return;
+    const float m = r.m == -__builtin_inff() ? r.m : r.m * c;
+    if (whole) {
+      const int token = token_of(r.row), head = head_of(r.row);
+      uint8_t* to = (uint8_t*)a.out.p + (int64_t)token * a.out.token_stride +
+                    (int64_t)head * a.out.head_stride;
+      const float vs = CT == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f;
+      const float inv = r.l == 0.0f ? 0.0f : vs / r.l;
+#pragma unroll
+      for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int e = 32 * d + 8 * i + 4 * half;
+          if (e >= a.c.head_dim) continue;
+          typename Fmt<QT>::elem w[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) w[j] = (typename Fmt<QT>::elem)(r.o[d][4 * i + j] * inv);
+          *(u32x2*)(to + 2 * e) = u32x2{
+              as<uint16_t>(w[0]) | (uint32_t)as<uint16_t>(w[1]) << 16,
+              as<uint16_t>(w[2]) | (uint32_t)as<uint16_t>(w[3]) << 16};
+        }
+      if (a.lse && half == 0)
+        a.lse[(int64_t)token * a.heads + head] =
+            r.l == 0.0f ? -__builtin_inff() : (m + log2f(r.l)) * 0.69314718055994531f;
+      return;
+    }
+    const int kind = prefix ? 0 : 1;
+    if (number >= a.pieces[kind]) {
+      if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+      return;
+    }
+    const int64_t at = number * a.rows[kind] + r.row % u.tile_rows;
+    float* to = a.sum[kind] + at * DP;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        *(f32x4*)(to + 32 * d + 8 * i + 4 * half) = f32x4{
+            r.o[d][4 * i], r.o[d][4 * i + 1], r.o[d][4 * i + 2], r.o[d][4 * i + 3]};
+    if (half == 0) a.stat[kind][at] = make_float2(m, r.l);
+  }
+
+  // Waves share out the rows: 32 each, all keys.
+  __device__ __forceinline__ void block_rows(int64_t number, bool whole) {
+    const int tid = threadIdx.x, wave = wave_uniform(tid / kWave), lane = lane_id();
+    constexpr int keys = Lds<DP>::keys, buffers = Lds<DP>::buffers;
+    Stage<DP, QT, CT, keys, kBlock> st;
+    Rows32<DP> r;
+    bool bad = false;
+    int64_t t0 = u.lo + (int64_t)lo_tile * kTile;
+    const int64_t end = (int64_t)u.lo + (int64_t)hi_tile * kTile < u.hi
+                            ? (int64_t)u.lo + (int64_t)hi_tile * kTile : u.hi;
+    int64_t slot = slot_of(t0 + lane, &bad);
+    st.load(kb, vb, slot, tid, head_bytes);
+    load_rows(r, index * kRowsBlock + wave * 32);
+    const int least = least_limit(r);
+    // The block's least: keys from there on may be hidden from some row.
+    __syncthreads();
+    if (lane == 0) sh.ipart[wave] = least;
+    if (tid == 0) sh.special = kNone;
+    __syncthreads();
+    int fewest = sh.ipart[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) fewest = sh.ipart[w] < fewest ? sh.ipart[w] : fewest;
+    const bool busy = index * kRowsBlock + wave * 32 < u.rows;
+    for (int i = 0; t0 < end; ++i, t0 += keys) {
+      const uint64_t valid = ballot(slot >= 0);
+      uint8_t* lk = lds + (i % buffers) * 2 * Lds<DP>::half;
+      uint8_t* lv = lk + Lds<DP>::half;
+      if (buffers == 1) __syncthreads();  // the last step's reads
+      if (t0 + keys > fewest || ~valid != 0) {
+        const int special = st.template store<true>(lk, lv, valid, tid, head_bytes);
+        if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
+      } else {
+        st.template store<false>(lk, lv, valid, tid, head_bytes);
+      }
+      if (t0 + keys < end) {
+        slot = slot_of(t0 + keys + lane, &bad);
+        st.load(kb, vb, slot, tid, head_bytes);
+      }
+      __syncthreads();
+      if (busy)
+        step<DP, QT, 2>(r, lk, lv, c, t0 + keys > least || ~valid != 0,
+                        valid & below(r.limit, t0));
+    }
+    if (sh.special < end) add_special(r, sh.special, end);
+    if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+    r.l += other_half(r.l);
+    put(r, number, whole);
+    __syncthreads();  // LDS is free for the next item
+  }
+
+  // Waves share out the keys: 32 of every 128 each, the same rows; their
+  // sums are joined at the end.
+  __device__ __forceinline__ void split_keys(int64_t number, bool whole) {
+    const int tid = threadIdx.x, wave = wave_uniform(tid / kWave), lane = lane_id();
+    Stage<DP, QT, CT, 32, kWave> st;
+    Rows32<DP> r;
+    bool bad = false;
+    int64_t t0 = u.lo + (int64_t)lo_tile * kTile + wave * 32;
+    const int64_t end = (int64_t)u.lo + (int64_t)hi_tile * kTile < u.hi
+                            ? (int64_t)u.lo + (int64_t)hi_tile * kTile : u.hi;
+    uint8_t* lk = lds + wave * Lds<DP>::wave;
+    uint8_t* lv = lk + Lds<DP>::wave / 2;
+    int64_t slot = t0 < end ? slot_of(t0 + lane % 32, &bad) : -1;
+    if (t0 < end) st.load(kb, vb, slot, lane, head_bytes);
+    load_rows(r, index * kRowsSplit);
+    const int least = least_limit(r);
+    __syncthreads();
+    if (tid == 0) sh.special = kNone;
+    __syncthreads();
+    for (; t0 < end; t0 += kTile) {
+      const uint64_t valid = ballot(slot >= 0) & 0xffffffffull;
+      const bool edge = t0 + 32 > least || valid != 0xffffffffull;
+      if (edge) {
+        const int special = st.template store<true>(lk, lv, valid, lane, head_bytes);
+        if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
+      } else {
+        st.template store<false>(lk, lv, valid, lane, head_bytes);
+      }
+      if (t0 + kTile < end) {
+        slot = slot_of(t0 + kTile + lane % 32, &bad);
+        st.load(kb, vb, slot, lane, head_bytes);
+      }
+      step<DP, QT, 1>(r, lk, lv, c, edge, valid & below(r.limit, t0));
+    }
+    if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+    r.l += other_half(r.l);
+    // Join: the common maximum, then the sums of waves 2, 3 to 0, 1 and of 1
+    // to 0 through LDS.
+    if (lane < 32) sh.stat[0][wave][lane] = r.m;
+    __syncthreads();  // also: no wave reads its tiles any more
+    const int col = lane % 32;
+    float top = sh.stat[0][0][col];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh.stat[0][w][col]);
+    const float w = r.m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((r.m - top) * c);
+    r.m = top;
+    r.l *= w;
+#pragma unroll
+    for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) r.o[d][i] *= w;
+    f32x4* box = (f32x4*)lds;
+#pragma unroll
+    for (int from = 2; from >= 1; from /= 2) {
+      if (wave >= from && wave < 2 * from) {
+        f32x4* to = box + (wave - from) * (DP / 8) * kWave + lane;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+            to[(4 * d + i) * kWave] = f32x4{r.o[d][4 * i], r.o[d][4 * i + 1], r.o[d][4 * i + 2],
+                                            r.o[d][4 * i + 3]};
+        if (lane < 32) sh.stat[1][wave][lane] = r.l;
+      }
+      __syncthreads();
+      if (wave < from) {
+        const f32x4* of = box + wave * (DP / 8) * kWave + lane;
+#pragma unroll
+        for (int d = 0; d < DP / 32; ++d)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const f32x4 x = of[(4 * d + i) * kWave];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) r.o[d][4 * i + j] += x[j];
+          }
+        r.l += sh.stat[1][wave + from][col];
+      }
+      __syncthreads();
+    }
+    if (wave == 0) {
+      if (sh.special < end) add_special(r, sh.special, end);
+      put(r, number, whole);
+    }
+  }
+
+  // Tiles [lo_tile, hi_tile) of an item.
+  __device__ __forceinline__ void run(int64_t number, bool whole) {
+    kb = (const uint8_t*)a.c.k + kvh * a.c.head_stride;
+    vb = (const uint8_t*)a.c.v + kvh * a.c.head_stride;
+    float f = a.scale * 1.44269504088896341f;
+    if (CT == EP_DTYPE_E4M3) f *= a.c.k_scale[kvh];
+    negate = f < 0.0f;
+    // Equal scores all the same, and no 0 * inf where a key is hidden.
+    c = f == 0.0f ? 1e-30f : fabsf(f);
+    head_bytes = a.c.head_dim * Fmt<CT>::bytes;
+    table_row = prefix ? a.g.group_off[unit] : unit - a.g.n_groups;
+    if (u.tile_rows == kRowsSplit) split_keys(number, whole);
+    else block_rows(number, whole);
+  }
+};
+
+// Exclusive sums of (length, items) over the workgroup's threads, as of unit
+// base + tid, into sh.start and sh.item; entry kBlock holds the totals.
+__device__ __forceinline__ void sum_units(Shared& sh, int64_t length, int32_t items) {
+  const int lane = lane_id(), wave = threadIdx.x / kWave;
+  int64_t x = length;
+  int32_t y = items;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int64_t xo = __shfl_up(x, d);
+    const int32_t yo = __shfl_up(y, d);
+    if (lane >= d) {
+      x += xo;
+      y += yo;
+    }
+  }
+  __syncthreads();
+  if (lane == kWave - 1) {
+    sh.part[wave] = x;
+    sh.ipart[wave] = y;
+  }
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) {
+    x += sh.part[w];
+    y += sh.ipart[w];
+  }
+  sh.start[threadIdx.x + 1] = x;
+  sh.item[threadIdx.x + 1] = y;
+  if (threadIdx.x == 0) {
+    sh.start[0] = 0;
+    sh.item[0] = 0;
+  }
+  __syncthreads();
+}
+
+template <int DP, int QT, int CT>
+__global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Attend a) {
+  __shared__ __attribute__((aligned(16))) uint8_t lds[Lds<DP>::bytes];
+  __shared__ Shared sh;
+  const int tid = threadIdx.x;
+  const int units = a.g.n_groups + a.b.n_seqs;
+  if (tid == 0) sh.any_short = 0;
+  __syncthreads();
+  // The line's length.
+  int64_t total = 0;
+  Unit u;
+  for (int base = 0; base < units; base += kBlock) {
+    int64_t length = 0;
+    int32_t items = 0;
+    if (base + tid < units) {
+      u = unit_of(a, base + tid);
+      length = unit_length(a, u);
+      items = u.items * a.c.n_heads;
+      if (u.is_short) sh.any_short = 1;
+    }
+    sum_units(sh, length, items);
+    total += sh.start[kBlock];
+  }
+  const int64_t begin = begin_of(a, blockIdx.x, total), end = begin_of(a, blockIdx.x + 1, total);
+  const bool scribe = blockIdx.x == 0;
+  if (begin == end && !scribe) return;
+  // Its units: prefix items and suffix items are numbered apart.
+  int64_t at = 0;
+  int64_t item_at = 0, first_suffix = 0;
+  for (int base = 0; base < units; base += kBlock) {
+    if (units > kBlock) {
+      __syncthreads();
+      int64_t length = 0;
+      int32_t items = 0;
+      if (base + tid < units) {
+        u = unit_of(a, base + tid);
+        length = unit_length(a, u);
+        items = u.items * a.c.n_heads;
+      }
+      sum_units(sh, length, items);
+    }
+    const int count = units - base < kBlock ? units - base : kBlock;
+    const int groups = a.g.n_groups - base;  // of this round
+    if (groups >= 0 && groups <= count) first_suffix = item_at + sh.item[groups];
+    if (scribe && tid < count) {
+      a.line[base + tid] = at + sh.start[tid];
+      a.items[base + tid] =
+          (int32_t)(item_at + sh.item[tid] - (base + tid < a.g.n_groups ? 0 : first_suffix));
+    }
+    const int64_t stop = at + sh.start[count];
+    const int64_t item_stop = item_at + sh.item[count];
+    if (begin < stop && end > at && begin < end) {
+      // First unit that reaches past `begin`.
+      int lo = 0, hi = count;
+      while (lo < hi) {
+        const int mid = (lo + hi) / 2;
+        if (at + sh.start[mid + 1] > begin) hi = mid;
+        else lo = mid + 1;
+      }
+      for (int k = lo; k < count && at + sh.start[k] < end; ++k) {
+        const int64_t from = at + sh.start[k];
+        const int32_t first = sh.item[k];
+        const Unit v = unit_of(a, base + k);
+        const int64_t len = (int64_t)v.tiles * v.cost;
+        if (len == 0) continue;
+        const int n = v.items * a.c.n_heads;
+        const int64_t i0 = begin > from ? (begin - from) / len : 0;
+        for (int64_t i = i0; i < n && from + i * len < end; ++i) {
+          Body<DP, QT, CT> b{a, sh, lds};
+          b.u = v;
+          b.unit = base + k;
+          b.prefix = base + k < a.g.n_groups;
+          b.kvh = (int)(i / v.items);
+          b.index = (int)(i % v.items);
+          const int64_t start = from + i * len;
+          b.lo_tile = tiles_before(v, start, begin);
+          b.hi_tile = tiles_before(v, start, end);
+          if (b.lo_tile >= b.hi_tile) continue;
+          const int64_t number = item_at + first + i - (b.prefix ? 0 : first_suffix) + blockIdx.x;
+          const bool whole = !b.prefix && v.lo == 0 && b.lo_tile == 0 && b.hi_tile == v.tiles;
+          b.run(number, whole);
+        }
+      }
+    }
+    at = stop;
+    item_at = item_stop;
+  }
+  if (scribe && tid == 0) a.line[units] = total;
+}
+
+// ---------------------------------------------------------------------------
+// Joining the pieces: one wave per row and head.
+// ---------------------------------------------------------------------------
+struct Part {
+  int64_t start;  // of the row's item, in the line
+  int item, row;  // number of the item, row of the piece
+  int kind;
+  Unit u;
+  int w0, n;      // workgroups that may hold pieces of it: w0 .. w0 + n - 1
+};
+
+__device__ __forceinline__ Part part_of(const Attend& a, int unit, int token, int share_row,
+                                        int kvh, int64_t total) {
+  Part p;
+  p.u = unit_of(a, unit);
+  p.kind = unit < a.g.n_groups ? 0 : 1;
+  p.n = 0;
+  const int row = (token - p.u.row0) * a.share + share_row;
+  if (p.u.tiles == 0 || row < 0 || row >= p.u.rows) return p;
+  const int i = kvh * p.u.items + row / p.u.tile_rows;
+  const int64_t len = (int64_t)p.u.tiles * p.u.cost;
+  p.start = a.line[unit] + i * len;
+  p.item = a.items[unit] + i;
+  p.row = row % p.u.tile_rows;
+  p.w0 = worker_of(a, p.start, total);
+  p.n = worker_of(a, p.start + len - p.u.cost, total) - p.w0 + 1;
+  return p;
+}
+
+template <int DP, int QT>
+__global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
+  constexpr int per = DP / kWave;  // elements of a lane, consecutive
+  const int lane = lane_id();
+  const int units = a.g.n_groups + a.b.n_seqs;
+  const int64_t total = a.line[units];
+  const int64_t stride = (int64_t)gridDim.x * kWaves;
+  for (int64_t i = (int64_t)blockIdx.x * kWaves + wave_uniform(threadIdx.x / kWave); i < rows;
+       i += stride) {
+    const int token = (int)(i / a.heads), head = (int)(i % a.heads), kvh = head / a.share;
+    const int s = seq_of_row(a.b, token);
+    if (s < 0) continue;
+    int first;
+    const int n = new_of(a, s, &first);
+    const int64_t last = (int64_t)a.b.lens[s] - n + (token - first);
+    if (token - first >= a.max_new || n == 0) {
+      if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+      continue;
+    }
+    // Positions behind the table's end.
+    if (last >= key_cap(a) && lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+    const int j = group_of(a, s);
+    Part part[2];
+    part[0].n = 0;
+    if (j >= 0) part[0] = part_of(a, j, token, head % a.share, kvh, total);
+    part[1] = part_of(a, a.g.n_groups + s, token, head % a.share, kvh, total);
+    // Written whole by the first launch.
+    if (part[1].n > 0 && part[1].u.lo == 0 &&
+        begin_of(a, part[1].w0, total) <= part[1].start &&
+        begin_of(a, (int64_t)part[1].w0 + 1, total) >
+            part[1].start + (int64_t)(part[1].u.tiles - 1) * part[1].u.cost)
+      continue;
+    const int most = part[0].n + part[1].n;
+    float m = -__builtin_inff(), l = 0.0f, o[per] = {};
+    for (int k0 = 0; k0 < most; k0 += kWave) {
+      const int k = k0 + lane;
+      const int kind = k < part[0].n ? 0 : 1;
+      const Part& p = kind == 0 ? part[0] : part[1];
+      const int w = p.w0 + (kind == 0 ? k : k - part[0].n);
+      int64_t at = -1;
+      float2 st = make_float2(-__builtin_inff(), 0.0f);
+      if (k < most &&
+          tiles_before(p.u, p.start, begin_of(a, w, total)) <
+              tiles_before(p.u, p.start, begin_of(a, (int64_t)w + 1, total))) {
+        const int64_t number = (int64_t)w + p.item;
+        if (number < a.pieces[kind]) {
+          at = number * a.rows[kind] + p.row;
+          st = a.stat[kind][at];
+          if (st.x == -__builtin_inff()) at = -1;
+        }
+      }
+      float top = st.x;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+      top = fmaxf(top, m);
+      if (top == -__builtin_inff()) continue;
+      const float scale = __builtin_amdgcn_exp2f(m - top);
+      const float wgt = at >= 0 ? __builtin_amdgcn_exp2f(st.x - top) : 0.0f;
+      float sum = wgt * st.y;
+#pragma unroll
+      for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
+      l = l * scale + sum;
+      m = top;
+#pragma unroll
+      for (int e = 0; e < per; ++e) o[e] *= scale;
+      const int64_t tagged = at < 0 ? -1 : at * 2 + kind;
+      for (uint64_t mask = ballot(at >= 0); mask; mask &= mask - 1) {
+        const int src = __builtin_ctzll(mask);
+        const int64_t from = __shfl(tagged, src);
+        const float f = __shfl(wgt, src);
+        const float* x = (from & 1 ? a.sum[1] : a.sum[0]) + (from >> 1) * DP + lane * per;
+#pragma unroll
+        for (int e = 0; e < per; ++e) o[e] += f * x[e];
+      }
+    }
+    uint8_t* to = (uint8_t*)a.out.p + (int64_t)token * a.out.token_stride +
+                  (int64_t)head * a.out.head_stride;
+    const float vs = a.c.dtype == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f;
+    const float inv = l == 0.0f ? 0.0f : vs / l;
+#pragma unroll
+    for (int e = 0; e < per; ++e) {
+      const int d = lane * per + e;
+      if (d < a.c.head_dim) store1<QT>(to + 2 * d, o[e] * inv);
+    }
+    if (a.lse && lane == 0)
+      a.lse[i] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.69314718055994531f;
+  }
+}
+
+struct Layout {
+  int dim;  // padded head size
+  int workers;
+  int pieces[2], rows[2];
+  size_t line, items, stat[2], sum[2], bytes;
+};
+
+size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
+
+Layout layout(const ep_kv_cache& c, int n_seqs, int n_groups, int n_tokens, int n_heads,
+              int max_new) {
+  Layout l{};
+  l.dim = c.head_dim <= 64 ? 64 : c.head_dim <= 128 ? 128 : 256;
+  l.workers = l.dim <= 128 ? 512 : 256;
+  const int64_t rows = (int64_t)n_tokens * (n_heads / c.n_heads);  // per KV head
+  const int64_t most = (int64_t)max_new * (n_heads / c.n_heads);
+  l.rows[0] = n_groups > 0 ? kRowsBlock : 0;
+  l.rows[1] = most <= kRowsSplit ? kRowsSplit : kRowsBlock;
+  // Items: one per unit and full tile_rows more; units of few rows take one.
+  const int64_t items0 = n_groups > 0 ? (rows / kRowsBlock + n_groups) * c.n_heads : 0;
+  const int64_t full = most <= kRowsSplit ? 0 : rows / kRowsBlock;
+  const int64_t items1 = (full + (n_seqs < n_tokens ? n_seqs : n_tokens)) * c.n_heads;
+  const int64_t p0 = items0 > 0 ? items0 + l.workers : 0, p1 = items1 + l.workers;
+  l.pieces[0] = (int)(p0 < 0x7fffffff ? p0 : 0x7fffffff);
+  l.pieces[1] = (int)(p1 < 0x7fffffff ? p1 : 0x7fffffff);
+  size_t at = 0;
+  const int64_t units = (int64_t)n_seqs + n_groups;
+  l.line = at;
+  at += up((size_t)(units + 1) * 8);
+  l.items = at;
+  at += up((size_t)units * 4);
+  for (int k = 0; k < 2; ++k) {
+    l.stat[k] = at;
+    at += up((size_t)l.pieces[k] * l.rows[k] * 8);
+    l.sum[k] = at;
+    at += up((size_t)l.pieces[k] * l.rows[k] * l.dim * 4);
+  }
+  l.bytes = at;
+  return l;
+}
+
+template <int DP, int QT, int CT>
+hipError_t launch(const Attend& a, hipStream_t stream) {
+  hipLaunchKernelGGL((attend_kernel<DP, QT, CT>), dim3(a.workers), dim3(kBlock), 0, stream, a);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t rows = (int64_t)a.b.n_tokens * a.heads, blocks = (rows + kWaves - 1) / kWaves;
+  const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
+  hipLaunchKernelGGL((join_kernel<DP, QT>), dim3(grid), dim3(kBlock), 0, stream, a, rows);
+  return hipGetLastError();
+}
+
+template <int DP>
+hipError_t launch_dim(const Attend& a, hipStream_t stream) {
+  const bool e4m3 = a.c.dtype == EP_DTYPE_E4M3;
+  if (a.b.dtype == EP_DTYPE_BF16)
+    return e4m3 ? launch<DP, EP_DTYPE_BF16, EP_DTYPE_E4M3>(a, stream)
+                : launch<DP, EP_DTYPE_BF16, EP_DTYPE_BF16>(a, stream);
+  return e4m3 ? launch<DP, EP_DTYPE_F16, EP_DTYPE_E4M3>(a, stream)
+              : launch<DP, EP_DTYPE_F16, EP_DTYPE_F16>(a, stream);
 }
 
 }  // namespace
 
-size_t kv_attend_bytes(const ep_kv_cache&, int, int, int, int, int) { return 256; }
+size_t kv_attend_bytes(const ep_kv_cache& c, int n_seqs, int n_groups, int n_tokens, int n_heads,
+                       int max_new) {
+  return layout(c, n_seqs, n_groups, n_tokens, n_heads, max_new).bytes;
+}
 
 hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep_kv_groups& g,
                             int max_new, const ep_rows& q, int n_heads, const ep_rows& out,
-                            float* lse, float sm_scale, void*, int32_t* status,
+                            float* lse, float sm_scale, void* ws, int32_t* status,
                             hipStream_t stream) {
-  const Attend a{c, b, g, q, out, lse, sm_scale, n_heads, max_new, status};
-  const unsigned grid = (unsigned)(((int64_t)b.n_tokens * n_heads + 3) / 4);
-  const bool e4m3 = c.dtype == EP_DTYPE_E4M3;
-  if (b.dtype == EP_DTYPE_BF16) {
-    if (e4m3)
-      hipLaunchKernelGGL((attend_kernel<EP_DTYPE_BF16, EP_DTYPE_E4M3>), dim3(grid), dim3(kBlock), 0, stream, a);
-    else
-      hipLaunchKernelGGL((attend_kernel<EP_DTYPE_BF16, EP_DTYPE_BF16>), dim3(grid), dim3(kBlock), 0, stream, a);
-  } else if (e4m3) {
-    hipLaunchKernelGGL((attend_kernel<EP_DTYPE_F16, EP_DTYPE_E4M3>), dim3(grid), dim3(kBlock), 0, stream, a);
-  } else {
-    hipLaunchKernelGGL((attend_kernel<EP_DTYPE_F16, EP_DTYPE_F16>), dim3(grid), dim3(kBlock), 0, stream, a);
-  }
-  return hipGetLastError();
+  const Layout l = layout(c, b.n_seqs, g.n_groups, b.n_tokens, n_heads, max_new);
+  char* p = (char*)ws;
+  const Attend a{c,
+                 b,
+                 g,
+                 q,
+                 out,
+                 lse,
+                 sm_scale,
+                 n_heads,
+                 n_heads / c.n_heads,
+                 max_new,
+                 l.workers,
+                 (int64_t*)(p + l.line),
+                 (int32_t*)(p + l.items),
+                 {(float*)(p + l.sum[0]), (float*)(p + l.sum[1])},
+                 {(float2*)(p + l.stat[0]), (float2*)(p + l.stat[1])},
+                 {l.pieces[0], l.pieces[1]},
+                 {l.rows[0], l.rows[1]},
+                 status};
+  if (l.dim == 64) return launch_dim<64>(a, stream);
+  if (l.dim == 128) return launch_dim<128>(a, stream);
+  return launch_dim<256>(a, stream);
 }
 
 }  // namespace ep
