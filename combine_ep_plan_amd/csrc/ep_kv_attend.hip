@@ -27,6 +27,8 @@
 // both sides take it: slot (half h, j) of its step s is key 16 s + 8 (j / 4)
 // + 4 h + j % 4, the order the scores come out in. V is read from LDS through
 // the transposing read, four keys of one column per lane.
+#include <type_traits>
+
 #include "ep_kernels.hpp"
 #include "ep_kv_device.hpp"
 
@@ -45,9 +47,34 @@ constexpr int kTile = 128;       // keys of a tile
 constexpr int kNone = 0x7fffffff;
 constexpr int kRowsSplit = 32;   // rows of an item whose keys the waves share out
 constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
-// Weights of a tile of either kind.
-constexpr int kCostSplit = 1;
-constexpr int kCostBlock = 1;
+constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
+// Costs in the line: of a tile of either kind, and of starting on an item.
+constexpr int kCostSplit = 4;
+constexpr int kCostBlock = 4;
+constexpr int kCostItem = 4;
+
+// A unit as the line of work has it.
+struct Unit {
+  int64_t start;  // in the line
+  int item;       // first item, among those of its kind
+  int row0, rows; // first new token, rows per KV head
+  int lo, hi;     // keys
+  int seq;        // whose row of the table holds the keys
+  int group;      // of a sequence; -1: none
+  int len, fresh; // of a sequence: tokens, new ones among them
+
+  __device__ __forceinline__ bool split() const { return rows <= kRowsSplit; }
+  __device__ __forceinline__ int tile_rows() const { return split() ? kRowsSplit : kRowsBlock; }
+  __device__ __forceinline__ int items() const { return (rows + tile_rows() - 1) / tile_rows(); }
+  __device__ __forceinline__ int tiles() const {  // of an item
+    return rows > 0 ? (int)(((int64_t)hi - lo + kTile - 1) / kTile) : 0;
+  }
+  __device__ __forceinline__ int cost() const { return split() ? kCostSplit : kCostBlock; }
+  __device__ __forceinline__ int64_t item_length() const {
+    const int64_t n = tiles();
+    return n > 0 ? kCostItem + n * cost() : 0;
+  }
+};
 
 struct Attend {
   ep_kv_cache c;
@@ -58,29 +85,27 @@ struct Attend {
   float scale;
   int heads, share, max_new;  // share: query heads per KV head
   int workers;
-  // Workspace: per unit its place in the line and its first item, the
-  // line's length, and the pieces' sums and (m, l) by number and row.
-  int64_t* line;
-  int32_t* items;
+  // Workspace: the units, with the line's length behind the last as its
+  // start, and the pieces' sums and (m, l) by number and row.
+  Unit* units;
   float* sum[2];      // [0]: prefix pieces, [1]: suffix pieces
   float2* stat[2];
   int pieces[2], rows[2];  // pieces that fit, rows of each
   int32_t* status;
 };
 
+struct Shared {
+  Unit unit[kBlock];         // of a round
+  int64_t part[kWaves];
+  int32_t ipart[kWaves], spart[kWaves];
+  int32_t group_off[kGroupTable + 1], shared[kGroupTable];
+  int32_t any_short, special, first;
+  float stat[2][kWaves][32];
+};
+
 // ---------------------------------------------------------------------------
 // Units
 // ---------------------------------------------------------------------------
-struct Unit {
-  int row0, rows;     // first new token, rows per KV head
-  int lo, hi;         // keys
-  int tile_rows;      // rows of an item
-  int items;          // items per KV head
-  int tiles;          // tiles of an item
-  int cost;           // of a tile
-  bool is_short;      // suffix: the shared keys reach past the first new token
-};
-
 __device__ __forceinline__ int clamp_int(int64_t v, int64_t lo, int64_t hi) {
   return (int)(v < lo ? lo : v > hi ? hi : v);
 }
@@ -90,64 +115,70 @@ __device__ __forceinline__ int key_cap(const Attend& a) {
   return cap < 0x7fffffff ? (int)cap : 0x7fffffff;
 }
 
-// The group of sequence s, or -1.
-__device__ __forceinline__ int group_of(const Attend& a, int s) {
-  int lo = 0, hi = a.g.n_groups;  // last group that starts at or before s
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (a.g.group_off[mid] <= s) lo = mid;
-    else hi = mid;
-  }
-  return lo < a.g.n_groups && a.g.group_off[lo] <= s && s < a.g.group_off[lo + 1] ? lo : -1;
-}
-
-// First new token of sequence s and their number; 0 where the offsets are
-// not those of a batch.
-__device__ __forceinline__ int new_of(const Attend& a, int s, int* row0) {
-  const int lo = a.b.q_off ? a.b.q_off[s] : s, hi = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
-  *row0 = lo;
+// New tokens between two offsets; 0 where the offsets are not those of a
+// batch.
+__device__ __forceinline__ int fresh_of(const Attend& a, int lo, int hi) {
   return lo >= 0 && hi > lo && hi <= a.b.n_tokens ? hi - lo : 0;
 }
 
-__device__ __forceinline__ Unit unit_of(const Attend& a, int u) {
+// Reads the groups' ranges into LDS where they fit; a barrier must follow.
+__device__ __forceinline__ void load_groups(const Attend& a, Shared& sh) {
+  if (a.g.n_groups > kGroupTable) return;
+  if ((int)threadIdx.x <= a.g.n_groups) sh.group_off[threadIdx.x] = a.g.n_groups > 0 ? a.g.group_off[threadIdx.x] : 0;
+  if ((int)threadIdx.x < a.g.n_groups) sh.shared[threadIdx.x] = a.g.shared[threadIdx.x];
+}
+
+// The group of sequence s, or -1: the last one that starts at or before it.
+__device__ __forceinline__ int group_of(const Attend& a, const int32_t* off, int s) {
+  int lo = 0, hi = a.g.n_groups;
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (off[mid] <= s) lo = mid;
+    else hi = mid;
+  }
+  return lo < a.g.n_groups && off[lo] <= s && s < off[lo + 1] ? lo : -1;
+}
+
+// Unit u but for its place; *late: the shared keys reach past the first new
+// token, so that rows of the group see different ones of them.
+__device__ __forceinline__ Unit unit_of(const Attend& a, const Shared& sh, int u, bool* late) {
+  const int s = u - a.g.n_groups;
+  const bool kept = a.g.n_groups <= kGroupTable;
   Unit t;
-  t.is_short = false;
-  if (u < a.g.n_groups) {
-    const int s0 = a.g.group_off[u], s1 = a.g.group_off[u + 1];
-    t.row0 = t.rows = t.lo = t.hi = 0;
+  t.start = t.item = 0;
+  t.row0 = t.rows = t.lo = t.hi = t.len = t.fresh = 0;
+  t.group = -1;
+  t.seq = s;
+  if (s >= 0) {
+    const int lo = a.b.q_off ? a.b.q_off[s] : s, hi = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
+    t.len = a.b.lens[s];
+    t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
+    const int shared = t.group < 0 ? 0 : kept ? sh.shared[t.group] : a.g.shared[t.group];
+    t.row0 = lo;
+    t.fresh = fresh_of(a, lo, hi);
+    t.rows = (t.fresh < a.max_new ? t.fresh : a.max_new) * a.share;
+    t.lo = clamp_int(shared, 0, key_cap(a));
+    t.hi = clamp_int(t.len, t.lo, key_cap(a));
+    *late = (int64_t)t.len - t.fresh + 1 < shared;
+  } else {
+    const int s0 = kept ? sh.group_off[u] : a.g.group_off[u];
+    const int s1 = kept ? sh.group_off[u + 1] : a.g.group_off[u + 1];
+    t.group = u;
+    t.seq = s0;
+    *late = false;
     if (s0 >= 0 && s0 < s1 && s1 <= a.b.n_seqs) {
       const int lo = a.b.q_off ? a.b.q_off[s0] : s0;
       int hi = a.b.q_off ? a.b.q_off[s1] : s1;
       if (!a.b.q_off && hi > a.b.n_tokens) hi = a.b.n_tokens;
-      if (lo >= 0 && lo < hi && hi <= a.b.n_tokens) {
-        t.row0 = lo;
-        t.rows = (hi - lo) * a.share;
-        t.hi = clamp_int(a.g.shared[u], 0, key_cap(a));
-      }
+      t.row0 = lo;
+      t.rows = fresh_of(a, lo, hi) * a.share;
+      t.hi = clamp_int(kept ? sh.shared[u] : a.g.shared[u], 0, key_cap(a));
     }
-  } else {
-    const int s = u - a.g.n_groups;
-    const int n = new_of(a, s, &t.row0), len = a.b.lens[s];
-    t.rows = (n < a.max_new ? n : a.max_new) * a.share;
-    const int j = group_of(a, s);
-    const int shared = j >= 0 ? a.g.shared[j] : 0;
-    t.lo = clamp_int(shared, 0, key_cap(a));
-    t.hi = clamp_int(len, t.lo, key_cap(a));
-    t.is_short = (int64_t)len - n + 1 < shared;
   }
-  const bool split = t.rows <= kRowsSplit;
-  t.tile_rows = split ? kRowsSplit : kRowsBlock;
-  t.cost = split ? kCostSplit : kCostBlock;
-  t.items = (t.rows + t.tile_rows - 1) / t.tile_rows;
-  t.tiles = t.items > 0 ? (int)(((int64_t)t.hi - t.lo + kTile - 1) / kTile) : 0;
   return t;
 }
 
-__device__ __forceinline__ int64_t unit_length(const Attend& a, const Unit& u) {
-  return (int64_t)u.items * a.c.n_heads * u.tiles * u.cost;
-}
-
-// Workgroup w takes [begin(w), begin(w + 1)) of a line of n.
+// Workgroup w takes [begin_of(w), begin_of(w + 1)) of a line of n.
 __device__ __forceinline__ int64_t begin_of(const Attend& a, int64_t w, int64_t n) {
   return w * n / a.workers;
 }
@@ -155,9 +186,9 @@ __device__ __forceinline__ int worker_of(const Attend& a, int64_t x, int64_t n) 
   return (int)(((x + 1) * a.workers - 1) / n);
 }
 
-// Tiles of an item that starts at `at` whose first points lie before x.
+// Tiles of an item at `at` whose points lie before x.
 __device__ __forceinline__ int tiles_before(const Unit& u, int64_t at, int64_t x) {
-  return clamp_int((x - at + u.cost - 1) / u.cost, 0, u.tiles);
+  return clamp_int((x - at - kCostItem + u.cost() - 1) / u.cost(), 0, u.tiles());
 }
 
 // ---------------------------------------------------------------------------
@@ -218,41 +249,99 @@ __device__ __forceinline__ bool drop_special(u32x4& v) {
   return any;
 }
 
-// KEYS rows of K and V on their way from the pages to LDS, by THREADS threads.
+// Source of the chunks that hold nothing: keys without a slot, and the part
+// of a padded row behind the head.
+__device__ const u32x4 kZeros = {0, 0, 0, 0};
+
+// Starts the copy of 16 bytes per lane to LDS, lane l's to `to` + 16 l. It
+// counts as a vector load; nothing waits for it but settle_copies().
+__device__ __forceinline__ void copy_to_lds(const uint8_t* from, const lds_u8* to) {
+  const int at = wave_uniform((int)(uint32_t)(uintptr_t)to);
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :
+               : "s"(at), "v"(from)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void settle_copies() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+// KEYS rows of K and V on their way from the pages to LDS, by THREADS threads
+// (whole waves). 16-bit rows of up to 128 elements are copied to LDS without
+// passing through registers: a copy fills 1024 bytes of LDS in order, so the
+// order of the chunks is made by what each lane reads. Others go through
+// registers: e4m3 rows are widened on the way.
 template <int DP, int QT, int CT, int KEYS, int THREADS>
 struct Stage {
   static constexpr int cb = Fmt<CT>::bytes;
+  static constexpr bool direct = cb == 2 && DP <= 128;
   static constexpr int chunks = DP * cb / 16;  // 16-byte chunks of a row in the cache
   static constexpr int step = THREADS / chunks;
   static constexpr int n = KEYS / step;
   static_assert(THREADS % chunks == 0 && KEYS % step == 0, "a pass takes whole rows");
-  u32x4 k[n], v[n];
+  u32x4 k[direct ? 1 : n], v[direct ? 1 : n];
 
   // slot: this lane's key's byte offset, lane i holding key i (mod KEYS);
-  // -1: none. Rows without a slot and chunks past the head read the
-  // cache's first bytes instead (always in range) and are zeroed later.
+  // -1: none. lk, lv: where the tiles will be (written here if direct).
+  // ALL: every key has a slot and rows fill their place.
+  template <bool ALL>
   __device__ __forceinline__ void load(const uint8_t* kb, const uint8_t* vb, int64_t slot, int tid,
-                                       int head_bytes) {
-    const int c = tid % chunks * 16;
+                                       int head_bytes, uint8_t* lk, uint8_t* lv) {
+    const int c = tid % chunks;
 #pragma unroll
     for (int j = 0; j < n; ++j) {
-      const int64_t at = __shfl(slot, tid / chunks + j * step);
-      const int64_t off = at >= 0 && c < head_bytes ? at + c : 0;
-      k[j] = *(const u32x4*)(kb + off);
-      v[j] = *(const u32x4*)(vb + off);
+      const int t = tid / chunks + j * step;
+      const int64_t at = __shfl(slot, t);
+      if constexpr (direct) {
+        const int ck = place_k<DP>(t, c) * 16, cv = place_v<DP>(t, c) * 16;
+        const int base = wave_uniform(tid / kWave) * (kWave / chunks) + j * step;  // wave's first row
+        const uint8_t *pk = kb + ck + at, *pv = vb + cv + at;
+        if constexpr (!ALL) {
+          if (at < 0 || ck >= head_bytes) pk = (const uint8_t*)&kZeros;
+          if (at < 0 || cv >= head_bytes) pv = (const uint8_t*)&kZeros;
+        }
+        copy_to_lds(pk, (const lds_u8*)lk + base * DP * 2);
+        copy_to_lds(pv, (const lds_u8*)lv + base * DP * 2);
+      } else {
+        // Nothing is read past a row; what does not exist is zeroed in store().
+        const int64_t off = ALL || (at >= 0 && c * 16 < head_bytes) ? at + c * 16 : 0;
+        k[j] = *(const u32x4*)(kb + off);
+        v[j] = *(const u32x4*)(vb + off);
+      }
     }
   }
 
-  // Writes both tiles. CHECK: infinities and NaN of V go to LDS as zeros;
+  __device__ __forceinline__ void load(const uint8_t* kb, const uint8_t* vb, int64_t slot, int tid,
+                                       int head_bytes, uint8_t* lk, uint8_t* lv) {
+    if (ballot(slot < 0) == 0 && head_bytes == DP * cb)
+      load<true>(kb, vb, slot, tid, head_bytes, lk, lv);
+    else
+      load<false>(kb, vb, slot, tid, head_bytes, lk, lv);
+  }
+
+  // Finishes the tiles. CHECK: infinities and NaN of V are zeroed in LDS;
   // returns the lowest key (of this thread's) that holds one, else kNone.
   template <bool CHECK>
   __device__ __forceinline__ int store(uint8_t* lk, uint8_t* lv, uint64_t valid, int tid,
                                        int head_bytes) const {
     const int c = tid % chunks;
-    const int whole = c * 16 < head_bytes ? -1 : 0;
     int special = kNone;
+    if constexpr (direct) {
+      if constexpr (CHECK) {
 #pragma unroll
-    for (int j = 0; j < n; ++j) {
+        for (int j = 0; j < n; ++j) {
+          const int t = tid / chunks + j * step;
+          u32x4* at = (u32x4*)(lv + t * DP * 2 + c * 16);
+          u32x4 x = *at;
+          if (drop_special<QT>(x)) {
+            *at = x;
+            if (t < special) special = t;
+          }
+        }
+      }
+      return special;
+    }
+    const int whole = c * 16 < head_bytes ? -1 : 0;
+#pragma unroll
+    for (int j = 0; j < (direct ? 0 : n); ++j) {
       const int t = tid / chunks + j * step;
       const uint32_t keep = (uint32_t)(whole & -(int)((valid >> t) & 1));
       const u32x4 x = k[j] & keep, y = v[j] & keep;
@@ -337,24 +426,30 @@ __device__ __forceinline__ void step(Rows32<DP>& r, const uint8_t* lk, const uin
       }
     }
   }
-  float top = r.m;
+  float top = s[0][0];
 #pragma unroll
   for (int n = 0; n < NS; ++n)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
   top = fmaxf(top, other_half(top));
-  if (ballot(top > r.m)) {
+  // m need not be the maximum, only near it: it follows when a row's scores
+  // pass it by 2^kSlack, which keeps every weight under 2^kSlack and spares
+  // the rescale of the sums most of the time (with the maximum itself, some
+  // row of 32 has a new one in almost every step).
+  constexpr float kSlack = 8.0f;
+  if (ballot((top - r.m) * c > kSlack)) {
+    const float m = fmaxf(r.m, top);
     // exp2(-inf) = 0 where nothing was seen before; rows that still see
-    // nothing keep their zeros whatever the factor is.
-    const float w = top == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((r.m - top) * c);
+    // nothing keep their zeros.
+    const float w = m == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((r.m - m) * c);
     r.l *= w;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
       for (int i = 0; i < 16; ++i) r.o[d][i] *= w;
-    r.m = top;
+    r.m = m;
   }
-  const float base = top == -__builtin_inff() ? 0.0f : top * c;
+  const float base = r.m == -__builtin_inff() ? 0.0f : r.m * c;
   float sum = 0.0f;
 #pragma unroll
   for (int n = 0; n < NS; ++n)
@@ -410,23 +505,13 @@ __device__ __forceinline__ uint64_t below(int limit, int64_t t0) {
   return n >= 64 ? ~0ull : n <= 0 ? 0 : (1ull << n) - 1;
 }
 
-struct Shared {
-  int64_t start[kBlock + 1];  // of the units of a round, in the line
-  int32_t item[kBlock + 1];   // first item of each
-  int64_t part[kWaves];
-  int32_t ipart[kWaves];
-  int32_t any_short, special;
-  float stat[2][kWaves][32];
-};
-
 // Bytes of LDS that the tiles take: a workgroup's two halves, or the waves'
 // own tiles.
 template <int DP>
 struct Lds {
-  static constexpr int keys = 64;                      // keys of a block step
+  static constexpr int keys = DP <= 128 ? 64 : 32;     // keys of a block step
   static constexpr int half = keys * DP * 2;           // K or V of one
-  static constexpr int buffers = DP <= 128 ? 2 : 1;
-  static constexpr int block = 2 * half * buffers;
+  static constexpr int block = 2 * half * 2;           // two steps
   static constexpr int wave = 2 * 32 * DP * 2;         // K and V of 32 keys
   static constexpr int bytes = block > kWaves * wave ? block : kWaves * wave;
 };
@@ -438,24 +523,37 @@ struct Body {
   uint8_t* lds;
   Unit u;
   bool prefix;
-  int unit, kvh, index, lo_tile, hi_tile;  // index: of the item in its KV head
-  int table_row;
+  int kvh, index, lo_tile, hi_tile;  // index: of the item in its KV head
   const uint8_t *kb, *vb;
   float c;  // factor of the scores, in powers of two; positive
   bool negate;
   int head_bytes;
 
-  // Byte offset of key t's slot, or -1.
-  __device__ __forceinline__ int64_t slot_of(int64_t t, bool* bad) const {
-    if (t >= u.hi) return -1;
-    const uint32_t page = (uint32_t)t / (uint32_t)a.c.page_tokens;
-    const int32_t p = a.b.tables[(int64_t)table_row * a.b.max_pages + page];
-    if (p < 0 || p >= a.c.n_pages) {
+  // A key's slot is found in two halves, so that the table's entry is on its
+  // way while other work is done.
+  struct Lookup {
+    int32_t page;
+    uint32_t in;  // slot within the page; kNone: no key
+  };
+
+  __device__ __forceinline__ Lookup look_up(int64_t t) const {
+    Lookup l{0, (uint32_t)kNone};
+    if (t < u.hi) {
+      const uint32_t page = (uint32_t)t / (uint32_t)a.c.page_tokens;
+      l.in = (uint32_t)t - page * (uint32_t)a.c.page_tokens;
+      l.page = a.b.tables[(int64_t)u.seq * a.b.max_pages + page];
+    }
+    return l;
+  }
+
+  // Byte offset of the slot, or -1.
+  __device__ __forceinline__ int64_t slot_of(const Lookup& l, bool* bad) const {
+    if (l.in == (uint32_t)kNone) return -1;
+    if (l.page < 0 || l.page >= a.c.n_pages) {
       *bad = true;
       return -1;
     }
-    return p * a.c.page_stride +
-           (int64_t)((uint32_t)t - page * (uint32_t)a.c.page_tokens) * a.c.token_stride;
+    return l.page * a.c.page_stride + (int64_t)l.in * a.c.token_stride;
   }
 
   __device__ __forceinline__ int token_of(int row) const { return u.row0 + row / a.share; }
@@ -474,22 +572,16 @@ struct Body {
     // for no masking.
     r.limit = u.hi;
     if (!prefix) {
-      const int s = unit - a.g.n_groups;
-      int first;
-      const int n = new_of(a, s, &first);
-      const int64_t pos = (int64_t)a.b.lens[s] - n + (token - first);
-      r.limit = clamp_int(pos + 1, 0, u.hi);
+      r.limit = clamp_int((int64_t)u.len - u.fresh + (token - u.row0) + 1, 0, u.hi);
     } else if (sh.any_short) {
-      int lo = a.g.group_off[unit], hi = a.g.group_off[unit + 1];
+      int lo = u.seq, hi = a.g.group_off[u.group + 1];
       while (hi - lo > 1) {
         const int mid = (lo + hi) / 2;
         if ((a.b.q_off ? a.b.q_off[mid] : mid) <= token) lo = mid;
         else hi = mid;
       }
-      int first;
-      const int n = new_of(a, lo, &first);
-      const int64_t pos = (int64_t)a.b.lens[lo] - n + (token - first);
-      r.limit = clamp_int(pos + 1, 0, u.hi);
+      const int last = a.b.q_off ? a.b.q_off[lo + 1] : lo + 1;
+      r.limit = clamp_int((int64_t)a.b.lens[lo] - (last - token) + 1, 0, u.hi);
     }
     const uint8_t* p = (const uint8_t*)a.q.p + (int64_t)token * a.q.token_stride +
                        (int64_t)head_of(have) * a.q.head_stride;
@@ -521,7 +613,7 @@ struct Body {
     const int half = lane_id() / 32;
     for (int64_t t = t0; t < end; ++t) {
       bool bad = false;
-      const int64_t at = slot_of(t, &bad);
+      const int64_t at = slot_of(look_up(t), &bad);
       if (at < 0 || t >= r.limit) continue;
 #pragma unroll
       for (int d = 0; d < DP / 32; ++d) {
@@ -572,7 +664,7 @@ struct Body {
       if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
       return;
     }
-    const int64_t at = number * a.rows[kind] + r.row % u.tile_rows;
+    const int64_t at = number * a.rows[kind] + r.row % u.tile_rows();
     float* to = a.sum[kind] + at * DP;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
@@ -586,19 +678,20 @@ struct Body {
   // Waves share out the rows: 32 each, all keys.
   __device__ __forceinline__ void block_rows(int64_t number, bool whole) {
     const int tid = threadIdx.x, wave = wave_uniform(tid / kWave), lane = lane_id();
-    constexpr int keys = Lds<DP>::keys, buffers = Lds<DP>::buffers;
+    constexpr int keys = Lds<DP>::keys;
+    constexpr uint64_t all = keys == 64 ? ~0ull : (1ull << keys) - 1;
     Stage<DP, QT, CT, keys, kBlock> st;
     Rows32<DP> r;
     bool bad = false;
     int64_t t0 = u.lo + (int64_t)lo_tile * kTile;
     const int64_t end = (int64_t)u.lo + (int64_t)hi_tile * kTile < u.hi
                             ? (int64_t)u.lo + (int64_t)hi_tile * kTile : u.hi;
-    int64_t slot = slot_of(t0 + lane, &bad);
-    st.load(kb, vb, slot, tid, head_bytes);
+    int64_t slot = slot_of(look_up(t0 + lane % keys), &bad);
+    Lookup next = look_up(t0 + keys + lane % keys);
+    st.load(kb, vb, slot, tid, head_bytes, lds, lds + Lds<DP>::half);
     load_rows(r, index * kRowsBlock + wave * 32);
     const int least = least_limit(r);
     // The block's least: keys from there on may be hidden from some row.
-    __syncthreads();
     if (lane == 0) sh.ipart[wave] = least;
     if (tid == 0) sh.special = kNone;
     __syncthreads();
@@ -606,25 +699,38 @@ struct Body {
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) fewest = sh.ipart[w] < fewest ? sh.ipart[w] : fewest;
     const bool busy = index * kRowsBlock + wave * 32 < u.rows;
-    for (int i = 0; t0 < end; ++i, t0 += keys) {
-      const uint64_t valid = ballot(slot >= 0);
-      uint8_t* lk = lds + (i % buffers) * 2 * Lds<DP>::half;
+    // A step's tiles are complete once every wave has seen its own copies
+    // land and met the others; they may be overwritten when all have met
+    // again, in the next step. BUF is a constant, so that the tiles'
+    // addresses are too.
+    auto one = [&](auto buf) {
+      constexpr int BUF = decltype(buf)::value;
+      uint8_t* lk = lds + BUF * 2 * Lds<DP>::half;
       uint8_t* lv = lk + Lds<DP>::half;
-      if (buffers == 1) __syncthreads();  // the last step's reads
-      if (t0 + keys > fewest || ~valid != 0) {
-        const int special = st.template store<true>(lk, lv, valid, tid, head_bytes);
-        if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
-      } else {
-        st.template store<false>(lk, lv, valid, tid, head_bytes);
-      }
-      if (t0 + keys < end) {
-        slot = slot_of(t0 + keys + lane, &bad);
-        st.load(kb, vb, slot, tid, head_bytes);
-      }
+      const uint64_t valid = ballot(slot >= 0) & all;
+      const bool edge = t0 + keys > fewest || valid != all;
+      if constexpr (decltype(st)::direct) settle_copies();
+      int special = kNone;
+      if (edge) special = st.template store<true>(lk, lv, valid, tid, head_bytes);
+      else st.template store<false>(lk, lv, valid, tid, head_bytes);
+      if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
       __syncthreads();
+      if (t0 + keys < end) {
+        slot = slot_of(next, &bad);
+        uint8_t* to = lds + (1 - BUF) * 2 * Lds<DP>::half;
+        st.load(kb, vb, slot, tid, head_bytes, to, to + Lds<DP>::half);
+        next = look_up(t0 + 2 * keys + lane % keys);
+      }
       if (busy)
-        step<DP, QT, 2>(r, lk, lv, c, t0 + keys > least || ~valid != 0,
-                        valid & below(r.limit, t0));
+        step<DP, QT, keys / 32>(r, lk, lv, c, t0 + keys > least || valid != all,
+                                valid & below(r.limit, t0));
+      t0 += keys;
+    };
+    for (;;) {
+      one(std::integral_constant<int, 0>());
+      if (t0 >= end) break;
+      one(std::integral_constant<int, 1>());
+      if (t0 >= end) break;
     }
     if (sh.special < end) add_special(r, sh.special, end);
     if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
@@ -645,27 +751,42 @@ struct Body {
                             ? (int64_t)u.lo + (int64_t)hi_tile * kTile : u.hi;
     uint8_t* lk = lds + wave * Lds<DP>::wave;
     uint8_t* lv = lk + Lds<DP>::wave / 2;
-    int64_t slot = t0 < end ? slot_of(t0 + lane % 32, &bad) : -1;
-    if (t0 < end) st.load(kb, vb, slot, lane, head_bytes);
+    int64_t slot = -1;
+    Lookup next{0, (uint32_t)kNone};
+    if (t0 < end) {
+      slot = slot_of(look_up(t0 + lane % 32), &bad);
+      next = look_up(t0 + kTile + lane % 32);
+      st.load(kb, vb, slot, lane, head_bytes, lk, lv);
+    }
     load_rows(r, index * kRowsSplit);
     const int least = least_limit(r);
-    __syncthreads();
     if (tid == 0) sh.special = kNone;
     __syncthreads();
     for (; t0 < end; t0 += kTile) {
       const uint64_t valid = ballot(slot >= 0) & 0xffffffffull;
       const bool edge = t0 + 32 > least || valid != 0xffffffffull;
-      if (edge) {
-        const int special = st.template store<true>(lk, lv, valid, lane, head_bytes);
-        if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
-      } else {
-        st.template store<false>(lk, lv, valid, lane, head_bytes);
-      }
-      if (t0 + kTile < end) {
-        slot = slot_of(t0 + kTile + lane % 32, &bad);
-        st.load(kb, vb, slot, lane, head_bytes);
+      if constexpr (decltype(st)::direct) settle_copies();
+      int special = kNone;
+      if (edge) special = st.template store<true>(lk, lv, valid, lane, head_bytes);
+      else st.template store<false>(lk, lv, valid, lane, head_bytes);
+      if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
+      if constexpr (!decltype(st)::direct) {
+        if (t0 + kTile < end) {
+          slot = slot_of(next, &bad);
+          st.load(kb, vb, slot, lane, head_bytes, lk, lv);
+          next = look_up(t0 + 2 * kTile + lane % 32);
+        }
       }
       step<DP, QT, 1>(r, lk, lv, c, edge, valid & below(r.limit, t0));
+      if constexpr (decltype(st)::direct) {
+        if (t0 + kTile < end) {
+          slot = slot_of(next, &bad);
+          // The step's reads of the tiles are done: the products took them.
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+          st.load(kb, vb, slot, lane, head_bytes, lk, lv);
+          next = look_up(t0 + 2 * kTile + lane % 32);
+        }
+      }
     }
     if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
     r.l += other_half(r.l);
@@ -728,43 +849,69 @@ struct Body {
     // Equal scores all the same, and no 0 * inf where a key is hidden.
     c = f == 0.0f ? 1e-30f : fabsf(f);
     head_bytes = a.c.head_dim * Fmt<CT>::bytes;
-    table_row = prefix ? a.g.group_off[unit] : unit - a.g.n_groups;
-    if (u.tile_rows == kRowsSplit) split_keys(number, whole);
+    if (u.split()) split_keys(number, whole);
     else block_rows(number, whole);
   }
 };
 
-// Exclusive sums of (length, items) over the workgroup's threads, as of unit
-// base + tid, into sh.start and sh.item; entry kBlock holds the totals.
-__device__ __forceinline__ void sum_units(Shared& sh, int64_t length, int32_t items) {
-  const int lane = lane_id(), wave = threadIdx.x / kWave;
-  int64_t x = length;
-  int32_t y = items;
+// Units base .. base + kBlock - 1 into sh.unit, placed behind `at` in the
+// line and item[kind] of either kind, all of which move on by theirs.
+__device__ __forceinline__ void place_units(const Attend& a, Shared& sh, int base, int64_t& at,
+                                            int32_t item[2]) {
+  const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave, u = base + tid;
+  const int count = a.g.n_groups + a.b.n_seqs;
+  const bool suffix = u >= a.g.n_groups;
+  Unit t;
+  int64_t x = 0;
+  int32_t y[2] = {0, 0};
+  if (u < count) {
+    bool late;
+    t = unit_of(a, sh, u, &late);
+    if (late) sh.any_short = 1;
+    if (t.tiles() > 0) {
+      y[suffix] = t.items() * a.c.n_heads;
+      x = y[suffix] * t.item_length();
+    }
+  }
+  const int64_t x0 = x;
+  const int32_t y0 = y[0], y1 = y[1];
 #pragma unroll
   for (int d = 1; d < kWave; d <<= 1) {
     const int64_t xo = __shfl_up(x, d);
-    const int32_t yo = __shfl_up(y, d);
+    const int32_t yo = __shfl_up(y[0], d), zo = __shfl_up(y[1], d);
     if (lane >= d) {
       x += xo;
-      y += yo;
+      y[0] += yo;
+      y[1] += zo;
     }
   }
-  __syncthreads();
   if (lane == kWave - 1) {
     sh.part[wave] = x;
-    sh.ipart[wave] = y;
+    sh.ipart[wave] = y[0];
+    sh.spart[wave] = y[1];
   }
   __syncthreads();
-  for (int w = 0; w < wave; ++w) {
-    x += sh.part[w];
-    y += sh.ipart[w];
+  int64_t all = 0;
+  int32_t all0 = 0, all1 = 0;
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    if (w < wave) {
+      x += sh.part[w];
+      y[0] += sh.ipart[w];
+      y[1] += sh.spart[w];
+    }
+    all += sh.part[w];
+    all0 += sh.ipart[w];
+    all1 += sh.spart[w];
   }
-  sh.start[threadIdx.x + 1] = x;
-  sh.item[threadIdx.x + 1] = y;
-  if (threadIdx.x == 0) {
-    sh.start[0] = 0;
-    sh.item[0] = 0;
+  if (u < count) {
+    t.start = at + x - x0;
+    t.item = suffix ? item[1] + y[1] - y1 : item[0] + y[0] - y0;
+    sh.unit[tid] = t;
   }
+  at += all;
+  item[0] += all0;
+  item[1] += all1;
   __syncthreads();
 }
 
@@ -775,87 +922,53 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
   const int tid = threadIdx.x;
   const int units = a.g.n_groups + a.b.n_seqs;
   if (tid == 0) sh.any_short = 0;
+  load_groups(a, sh);
   __syncthreads();
-  // The line's length.
+  // The line's length; a batch of up to kBlock units stays in LDS.
   int64_t total = 0;
-  Unit u;
-  for (int base = 0; base < units; base += kBlock) {
-    int64_t length = 0;
-    int32_t items = 0;
-    if (base + tid < units) {
-      u = unit_of(a, base + tid);
-      length = unit_length(a, u);
-      items = u.items * a.c.n_heads;
-      if (u.is_short) sh.any_short = 1;
-    }
-    sum_units(sh, length, items);
-    total += sh.start[kBlock];
-  }
+  int32_t item[2] = {0, 0};
+  for (int base = 0; base < units; base += kBlock) place_units(a, sh, base, total, item);
   const int64_t begin = begin_of(a, blockIdx.x, total), end = begin_of(a, blockIdx.x + 1, total);
   const bool scribe = blockIdx.x == 0;
   if (begin == end && !scribe) return;
-  // Its units: prefix items and suffix items are numbered apart.
   int64_t at = 0;
-  int64_t item_at = 0, first_suffix = 0;
-  for (int base = 0; base < units; base += kBlock) {
-    if (units > kBlock) {
-      __syncthreads();
-      int64_t length = 0;
-      int32_t items = 0;
-      if (base + tid < units) {
-        u = unit_of(a, base + tid);
-        length = unit_length(a, u);
-        items = u.items * a.c.n_heads;
-      }
-      sum_units(sh, length, items);
-    }
+  item[0] = item[1] = 0;
+  for (int base = 0; base < units && (scribe || at < end); base += kBlock) {
+    const int64_t from = at;
+    if (units > kBlock) place_units(a, sh, base, at, item);
+    else at = total;
     const int count = units - base < kBlock ? units - base : kBlock;
-    const int groups = a.g.n_groups - base;  // of this round
-    if (groups >= 0 && groups <= count) first_suffix = item_at + sh.item[groups];
-    if (scribe && tid < count) {
-      a.line[base + tid] = at + sh.start[tid];
-      a.items[base + tid] =
-          (int32_t)(item_at + sh.item[tid] - (base + tid < a.g.n_groups ? 0 : first_suffix));
-    }
-    const int64_t stop = at + sh.start[count];
-    const int64_t item_stop = item_at + sh.item[count];
-    if (begin < stop && end > at && begin < end) {
-      // First unit that reaches past `begin`.
-      int lo = 0, hi = count;
-      while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (at + sh.start[mid + 1] > begin) hi = mid;
-        else lo = mid + 1;
-      }
-      for (int k = lo; k < count && at + sh.start[k] < end; ++k) {
-        const int64_t from = at + sh.start[k];
-        const int32_t first = sh.item[k];
-        const Unit v = unit_of(a, base + k);
-        const int64_t len = (int64_t)v.tiles * v.cost;
-        if (len == 0) continue;
-        const int n = v.items * a.c.n_heads;
-        const int64_t i0 = begin > from ? (begin - from) / len : 0;
-        for (int64_t i = i0; i < n && from + i * len < end; ++i) {
-          Body<DP, QT, CT> b{a, sh, lds};
-          b.u = v;
-          b.unit = base + k;
-          b.prefix = base + k < a.g.n_groups;
-          b.kvh = (int)(i / v.items);
-          b.index = (int)(i % v.items);
-          const int64_t start = from + i * len;
-          b.lo_tile = tiles_before(v, start, begin);
-          b.hi_tile = tiles_before(v, start, end);
-          if (b.lo_tile >= b.hi_tile) continue;
-          const int64_t number = item_at + first + i - (b.prefix ? 0 : first_suffix) + blockIdx.x;
-          const bool whole = !b.prefix && v.lo == 0 && b.lo_tile == 0 && b.hi_tile == v.tiles;
-          b.run(number, whole);
-        }
+    if (scribe && tid < count) a.units[base + tid] = sh.unit[tid];
+    if (begin >= at || end <= from) continue;
+    // The unit that holds `begin`, or this round's first.
+    const int64_t stop = tid + 1 < count ? sh.unit[tid + 1].start : at;
+    if (tid == 0) sh.first = 0;
+    __syncthreads();
+    if (tid < count && sh.unit[tid].start <= begin && begin < stop) sh.first = tid;
+    __syncthreads();
+    for (int k = sh.first; k < count; ++k) {
+      const Unit v = sh.unit[k];
+      if (v.start >= end) break;
+      const int64_t len = v.item_length();
+      if (len == 0) continue;
+      const int per = v.items(), n = per * a.c.n_heads;
+      const int64_t i0 = begin > v.start ? (begin - v.start) / len : 0;
+      for (int64_t i = i0; i < n && v.start + i * len < end; ++i) {
+        Body<DP, QT, CT> b{a, sh, lds};
+        b.u = v;
+        b.prefix = base + k < a.g.n_groups;
+        b.kvh = (int)i / per;
+        b.index = (int)i % per;
+        const int64_t start = v.start + i * len;
+        b.lo_tile = tiles_before(v, start, begin);
+        b.hi_tile = tiles_before(v, start, end);
+        if (b.lo_tile >= b.hi_tile) continue;
+        const bool whole = !b.prefix && v.lo == 0 && b.lo_tile == 0 && b.hi_tile == v.tiles();
+        b.run((int64_t)v.item + i + blockIdx.x, whole);
       }
     }
-    at = stop;
-    item_at = item_stop;
   }
-  if (scribe && tid == 0) a.line[units] = total;
+  if (scribe && tid == 0) a.units[units].start = total;
 }
 
 // ---------------------------------------------------------------------------
@@ -864,73 +977,71 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
 struct Part {
   int64_t start;  // of the row's item, in the line
   int item, row;  // number of the item, row of the piece
-  int kind;
-  Unit u;
   int w0, n;      // workgroups that may hold pieces of it: w0 .. w0 + n - 1
 };
 
-__device__ __forceinline__ Part part_of(const Attend& a, int unit, int token, int share_row,
+__device__ __forceinline__ Part part_of(const Attend& a, const Unit& u, int token, int share_row,
                                         int kvh, int64_t total) {
   Part p;
-  p.u = unit_of(a, unit);
-  p.kind = unit < a.g.n_groups ? 0 : 1;
   p.n = 0;
-  const int row = (token - p.u.row0) * a.share + share_row;
-  if (p.u.tiles == 0 || row < 0 || row >= p.u.rows) return p;
-  const int i = kvh * p.u.items + row / p.u.tile_rows;
-  const int64_t len = (int64_t)p.u.tiles * p.u.cost;
-  p.start = a.line[unit] + i * len;
-  p.item = a.items[unit] + i;
-  p.row = row % p.u.tile_rows;
-  p.w0 = worker_of(a, p.start, total);
-  p.n = worker_of(a, p.start + len - p.u.cost, total) - p.w0 + 1;
+  const int row = (token - u.row0) * a.share + share_row;
+  if (u.tiles() == 0 || row < 0 || row >= u.rows) return p;
+  const int i = kvh * u.items() + row / u.tile_rows();
+  const int64_t len = u.item_length();
+  p.start = u.start + i * len;
+  p.item = u.item + i;
+  p.row = row % u.tile_rows();
+  p.w0 = worker_of(a, p.start + kCostItem, total);
+  p.n = worker_of(a, p.start + len - u.cost(), total) - p.w0 + 1;
   return p;
 }
 
 template <int DP, int QT>
 __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
   constexpr int per = DP / kWave;  // elements of a lane, consecutive
+  constexpr int kAhead = 4;        // pieces read at a time
   const int lane = lane_id();
-  const int units = a.g.n_groups + a.b.n_seqs;
-  const int64_t total = a.line[units];
+  const int64_t total = a.units[a.g.n_groups + a.b.n_seqs].start;
   const int64_t stride = (int64_t)gridDim.x * kWaves;
   for (int64_t i = (int64_t)blockIdx.x * kWaves + wave_uniform(threadIdx.x / kWave); i < rows;
        i += stride) {
     const int token = (int)(i / a.heads), head = (int)(i % a.heads), kvh = head / a.share;
     const int s = seq_of_row(a.b, token);
     if (s < 0) continue;
-    int first;
-    const int n = new_of(a, s, &first);
-    const int64_t last = (int64_t)a.b.lens[s] - n + (token - first);
-    if (token - first >= a.max_new || n == 0) {
+    const Unit su = a.units[a.g.n_groups + s];
+    const int64_t last = (int64_t)su.len - su.fresh + (token - su.row0);
+    if (token - su.row0 >= a.max_new || su.fresh == 0) {
       if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
       continue;
     }
     // Positions behind the table's end.
     if (last >= key_cap(a) && lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
-    const int j = group_of(a, s);
     Part part[2];
+    Unit pu = su;
     part[0].n = 0;
-    if (j >= 0) part[0] = part_of(a, j, token, head % a.share, kvh, total);
-    part[1] = part_of(a, a.g.n_groups + s, token, head % a.share, kvh, total);
+    if (su.group >= 0) {
+      pu = a.units[su.group];
+      part[0] = part_of(a, pu, token, head % a.share, kvh, total);
+    }
+    part[1] = part_of(a, su, token, head % a.share, kvh, total);
     // Written whole by the first launch.
-    if (part[1].n > 0 && part[1].u.lo == 0 &&
-        begin_of(a, part[1].w0, total) <= part[1].start &&
-        begin_of(a, (int64_t)part[1].w0 + 1, total) >
-            part[1].start + (int64_t)(part[1].u.tiles - 1) * part[1].u.cost)
+    if (part[1].n > 0 && su.lo == 0 &&
+        tiles_before(su, part[1].start, begin_of(a, part[1].w0, total)) == 0 &&
+        tiles_before(su, part[1].start, begin_of(a, (int64_t)part[1].w0 + 1, total)) == su.tiles())
       continue;
     const int most = part[0].n + part[1].n;
     float m = -__builtin_inff(), l = 0.0f, o[per] = {};
     for (int k0 = 0; k0 < most; k0 += kWave) {
       const int k = k0 + lane;
-      const int kind = k < part[0].n ? 0 : 1;
-      const Part& p = kind == 0 ? part[0] : part[1];
-      const int w = p.w0 + (kind == 0 ? k : k - part[0].n);
+      const bool pre = k < part[0].n;
+      const Part& p = pre ? part[0] : part[1];
+      const Unit& u = pre ? pu : su;
+      const int w = p.w0 + (pre ? k : k - part[0].n);
       int64_t at = -1;
       float2 st = make_float2(-__builtin_inff(), 0.0f);
-      if (k < most &&
-          tiles_before(p.u, p.start, begin_of(a, w, total)) <
-              tiles_before(p.u, p.start, begin_of(a, (int64_t)w + 1, total))) {
+      if (k < most && tiles_before(u, p.start, begin_of(a, w, total)) <
+                          tiles_before(u, p.start, begin_of(a, (int64_t)w + 1, total))) {
+        const int kind = pre ? 0 : 1;
         const int64_t number = (int64_t)w + p.item;
         if (number < a.pieces[kind]) {
           at = number * a.rows[kind] + p.row;
@@ -952,14 +1063,27 @@ __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
       m = top;
 #pragma unroll
       for (int e = 0; e < per; ++e) o[e] *= scale;
-      const int64_t tagged = at < 0 ? -1 : at * 2 + kind;
-      for (uint64_t mask = ballot(at >= 0); mask; mask &= mask - 1) {
-        const int src = __builtin_ctzll(mask);
-        const int64_t from = __shfl(tagged, src);
-        const float f = __shfl(wgt, src);
-        const float* x = (from & 1 ? a.sum[1] : a.sum[0]) + (from >> 1) * DP + lane * per;
+      const float* x = at < 0 ? nullptr : (pre ? a.sum[0] : a.sum[1]) + at * DP;
+      uint64_t mask = ballot(at >= 0);
+      while (mask) {
+        float v[kAhead][per], f[kAhead];
 #pragma unroll
-        for (int e = 0; e < per; ++e) o[e] += f * x[e];
+        for (int j = 0; j < kAhead; ++j) {
+          f[j] = 0.0f;
+#pragma unroll
+          for (int e = 0; e < per; ++e) v[j][e] = 0.0f;
+          if (mask == 0) continue;
+          const int src = __builtin_ctzll(mask);
+          mask &= mask - 1;
+          f[j] = __shfl(wgt, src);
+          const float* y = (const float*)__shfl((uint64_t)x, src) + lane * per;
+#pragma unroll
+          for (int e = 0; e < per; ++e) v[j][e] = y[e];
+        }
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j)
+#pragma unroll
+          for (int e = 0; e < per; ++e) o[e] += f[j] * v[j][e];
       }
     }
     uint8_t* to = (uint8_t*)a.out.p + (int64_t)token * a.out.token_stride +
@@ -980,7 +1104,7 @@ struct Layout {
   int dim;  // padded head size
   int workers;
   int pieces[2], rows[2];
-  size_t line, items, stat[2], sum[2], bytes;
+  size_t units, stat[2], sum[2], bytes;
 };
 
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1003,10 +1127,8 @@ Layout layout(const ep_kv_cache& c, int n_seqs, int n_groups, int n_tokens, int 
   l.pieces[1] = (int)(p1 < 0x7fffffff ? p1 : 0x7fffffff);
   size_t at = 0;
   const int64_t units = (int64_t)n_seqs + n_groups;
-  l.line = at;
-  at += up((size_t)(units + 1) * 8);
-  l.items = at;
-  at += up((size_t)units * 4);
+  l.units = at;
+  at += up((size_t)(units + 1) * sizeof(Unit));
   for (int k = 0; k < 2; ++k) {
     l.stat[k] = at;
     at += up((size_t)l.pieces[k] * l.rows[k] * 8);
@@ -1062,8 +1184,7 @@ hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                  n_heads / c.n_heads,
                  max_new,
                  l.workers,
-                 (int64_t*)(p + l.line),
-                 (int32_t*)(p + l.items),
+                 (Unit*)(p + l.units),
                  {(float*)(p + l.sum[0]), (float*)(p + l.sum[1])},
                  {(float2*)(p + l.stat[0]), (float2*)(p + l.stat[1])},
                  {l.pieces[0], l.pieces[1]},
