@@ -12,12 +12,14 @@
 // over the keys behind them. Units are cut into items of at most kRows rows
 // and one KV head, items into tiles of kTile keys.
 //
-// Work. The tiles of all items stand in one line, weighted by what they cost,
-// and each of the launch's workgroups takes an equal length of it, whatever
-// the lengths of the sequences: no list of work is kept, every workgroup sums
-// the units itself (two loads per unit). A workgroup's part of an item is a
-// piece; workgroup w's piece of item i has number w + i, which no other piece
-// has, since both only grow along the line.
+// Work. The tiles of all items stand in two lines, prefix and suffix items,
+// weighted by what they cost. Each of the 8 XCDs takes an equal length of
+// both, so that row tiles that read the same keys meet in one L2 and every XCD
+// has as much arithmetic (prefix) as reading (suffix) to do; its workgroups
+// take equal lengths of what it has, whatever the lengths of the sequences. No
+// list of work is kept: every workgroup sums the units itself. A workgroup's
+// part of an item is a piece; workgroup w's piece of item i has number w + i,
+// which no other piece of the line has, since both only grow along it.
 //
 // Matrix products. Scores are formed transposed, S^T = K Q^T, with 32x32x16
 // products: a lane then holds 16 keys of one row, so that maximum, sum and
@@ -55,7 +57,7 @@ constexpr int kCostItem = 4;
 
 // A unit as the line of work has it.
 struct Unit {
-  int64_t start;  // in the line
+  int64_t start;  // in the lines, the suffix line behind the prefix line
   int item;       // first item, among those of its kind
   int row0, rows; // first new token, rows per KV head
   int lo, hi;     // keys
@@ -85,14 +87,20 @@ struct Attend {
   float scale;
   int heads, share, max_new;  // share: query heads per KV head
   int workers;
-  // Workspace: the units, with the line's length behind the last as its
-  // start, and the pieces' sums and (m, l) by number and row.
+  // Workspace: the units, with the lengths of the lines behind the last as the
+  // starts of two more; per item the workgroups that hold its first and last
+  // tile (the last as its complement where the item was written whole); and
+  // the pieces' sums and (m, l) by number and row.
   Unit* units;
+  int2* span[2];
   float* sum[2];      // [0]: prefix pieces, [1]: suffix pieces
   float2* stat[2];
   int pieces[2], rows[2];  // pieces that fit, rows of each
   int32_t* status;
 };
+
+constexpr int kXcds = 8;
+
 
 struct Shared {
   Unit unit[kBlock];         // of a round
@@ -100,6 +108,7 @@ struct Shared {
   int32_t ipart[kWaves], spart[kWaves];
   int32_t group_off[kGroupTable + 1], shared[kGroupTable];
   int32_t any_short, special, first;
+  int64_t prefix;  // length of the prefix line
   float stat[2][kWaves][32];
 };
 
@@ -178,12 +187,22 @@ __device__ __forceinline__ Unit unit_of(const Attend& a, const Shared& sh, int u
   return t;
 }
 
-// Workgroup w takes [begin_of(w), begin_of(w + 1)) of a line of n.
-__device__ __forceinline__ int64_t begin_of(const Attend& a, int64_t w, int64_t n) {
-  return w * n / a.workers;
-}
-__device__ __forceinline__ int worker_of(const Attend& a, int64_t x, int64_t n) {
-  return (int)(((x + 1) * a.workers - 1) / n);
+// Workgroup w of `workers` (a power of two) is number w % per of XCD w / per.
+// An XCD's lengths of the two lines of p and s stand one behind the other and
+// are cut evenly; [begin, end) is w's part of the line of that kind.
+struct Range {
+  int64_t begin, end;
+};
+
+__device__ __forceinline__ Range range_of(const Attend& a, int kind, int w, int64_t p, int64_t s) {
+  const int per = a.workers / kXcds, x = w / per, i = w % per;
+  const int64_t p0 = p * x / kXcds, p1 = p * (x + 1) / kXcds;
+  const int64_t s0 = s * x / kXcds, s1 = s * (x + 1) / kXcds;
+  const int64_t np = p1 - p0, n = np + s1 - s0;
+  const int64_t lo = (int64_t)((uint64_t)(n * i) / (unsigned)per);
+  const int64_t hi = (int64_t)((uint64_t)(n * (i + 1)) / (unsigned)per);
+  if (kind == 0) return Range{p0 + (lo < np ? lo : np), p0 + (hi < np ? hi : np)};
+  return Range{p + s0 + (lo > np ? lo - np : 0), p + s0 + (hi > np ? hi - np : 0)};
 }
 
 // Tiles of an item at `at` whose points lie before x.
@@ -904,6 +923,7 @@ __device__ __forceinline__ void place_units(const Attend& a, Shared& sh, int bas
     all0 += sh.ipart[w];
     all1 += sh.spart[w];
   }
+  if (u == a.g.n_groups) sh.prefix = at + x - x0;
   if (u < count) {
     t.start = at + x - x0;
     t.item = suffix ? item[1] + y[1] - y1 : item[0] + y[0] - y0;
@@ -928,71 +948,92 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
   int64_t total = 0;
   int32_t item[2] = {0, 0};
   for (int base = 0; base < units; base += kBlock) place_units(a, sh, base, total, item);
-  const int64_t begin = begin_of(a, blockIdx.x, total), end = begin_of(a, blockIdx.x + 1, total);
+  const int64_t prefix = sh.prefix;
   const bool scribe = blockIdx.x == 0;
-  if (begin == end && !scribe) return;
-  int64_t at = 0;
-  item[0] = item[1] = 0;
-  for (int base = 0; base < units && (scribe || at < end); base += kBlock) {
-    const int64_t from = at;
-    if (units > kBlock) place_units(a, sh, base, at, item);
-    else at = total;
-    const int count = units - base < kBlock ? units - base : kBlock;
-    if (scribe && tid < count) a.units[base + tid] = sh.unit[tid];
-    if (begin >= at || end <= from) continue;
-    // The unit that holds `begin`, or this round's first.
-    const int64_t stop = tid + 1 < count ? sh.unit[tid + 1].start : at;
-    if (tid == 0) sh.first = 0;
-    __syncthreads();
-    if (tid < count && sh.unit[tid].start <= begin && begin < stop) sh.first = tid;
-    __syncthreads();
-    for (int k = sh.first; k < count; ++k) {
-      const Unit v = sh.unit[k];
-      if (v.start >= end) break;
-      const int64_t len = v.item_length();
-      if (len == 0) continue;
-      const int per = v.items(), n = per * a.c.n_heads;
-      const int64_t i0 = begin > v.start ? (begin - v.start) / len : 0;
-      for (int64_t i = i0; i < n && v.start + i * len < end; ++i) {
-        Body<DP, QT, CT> b{a, sh, lds};
-        b.u = v;
-        b.prefix = base + k < a.g.n_groups;
-        b.kvh = (int)i / per;
-        b.index = (int)i % per;
-        const int64_t start = v.start + i * len;
-        b.lo_tile = tiles_before(v, start, begin);
-        b.hi_tile = tiles_before(v, start, end);
-        if (b.lo_tile >= b.hi_tile) continue;
-        const bool whole = !b.prefix && v.lo == 0 && b.lo_tile == 0 && b.hi_tile == v.tiles();
-        b.run((int64_t)v.item + i + blockIdx.x, whole);
+  const int per_xcd = a.workers / kXcds;
+  const int w = blockIdx.x % kXcds * per_xcd + blockIdx.x / kXcds;
+#pragma unroll 1
+  for (int kind = 0; kind < 2; ++kind) {
+    const Range part = range_of(a, kind, w, prefix, total - prefix);
+    const int64_t begin = part.begin, end = part.end;
+    const bool write = scribe && kind == 0;
+    if (begin == end && !write) continue;
+    int64_t at = 0;
+    item[0] = item[1] = 0;
+    for (int base = 0; base < units && (write || at < end); base += kBlock) {
+      const int64_t from = at;
+      if (units > kBlock) place_units(a, sh, base, at, item);
+      else at = total;
+      const int count = units - base < kBlock ? units - base : kBlock;
+      if (write && tid < count) a.units[base + tid] = sh.unit[tid];
+      if (begin >= at || end <= from || begin == end) continue;
+      // The unit that holds `begin`, or this round's first.
+      const int64_t stop = tid + 1 < count ? sh.unit[tid + 1].start : at;
+      if (tid == 0) sh.first = 0;
+      __syncthreads();
+      if (tid < count && sh.unit[tid].start <= begin && begin < stop) sh.first = tid;
+      __syncthreads();
+      for (int k = sh.first; k < count; ++k) {
+        const Unit v = sh.unit[k];
+        if (v.start >= end) break;
+        const int64_t len = v.item_length();
+        if (len == 0) continue;
+        const int per = v.items(), n = per * a.c.n_heads, tiles = v.tiles();
+        const int64_t skip = begin > v.start ? begin - v.start : 0;
+        int i = ((skip | len) >> 32) == 0 ? (int)((uint32_t)skip / (uint32_t)len)
+                                          : (int)(skip / len);
+        for (; i < n && v.start + i * len < end; ++i) {
+          Body<DP, QT, CT> b{a, sh, lds};
+          b.u = v;
+          b.prefix = kind == 0;
+          b.kvh = i / per;
+          b.index = i % per;
+          const int64_t start = v.start + i * len;
+          b.lo_tile = tiles_before(v, start, begin);
+          b.hi_tile = tiles_before(v, start, end);
+          if (b.lo_tile >= b.hi_tile) continue;
+          const bool whole = kind == 1 && v.lo == 0 && b.lo_tile == 0 && b.hi_tile == tiles;
+          if (tid == 0 && v.item + i < a.pieces[kind] - a.workers) {
+            if (b.lo_tile == 0) a.span[kind][v.item + i].x = w;
+            if (b.hi_tile == tiles) a.span[kind][v.item + i].y = whole ? ~w : w;
+          }
+          b.run((int64_t)v.item + i + w, whole);
+        }
       }
     }
   }
-  if (scribe && tid == 0) a.units[units].start = total;
+  if (scribe && tid == 0) {
+    a.units[units].start = prefix;
+    a.units[units + 1].start = total;
+  }
 }
 
 // ---------------------------------------------------------------------------
 // Joining the pieces: one wave per row and head.
 // ---------------------------------------------------------------------------
 struct Part {
-  int64_t start;  // of the row's item, in the line
+  int64_t start;  // of the row's item, in the lines
   int item, row;  // number of the item, row of the piece
   int w0, n;      // workgroups that may hold pieces of it: w0 .. w0 + n - 1
+  bool whole;     // written by the first launch
 };
 
-__device__ __forceinline__ Part part_of(const Attend& a, const Unit& u, int token, int share_row,
-                                        int kvh, int64_t total) {
+__device__ __forceinline__ Part part_of(const Attend& a, const Unit& u, int kind, int token,
+                                        int share_row, int kvh) {
   Part p;
   p.n = 0;
+  p.whole = false;
   const int row = (token - u.row0) * a.share + share_row;
   if (u.tiles() == 0 || row < 0 || row >= u.rows) return p;
   const int i = kvh * u.items() + row / u.tile_rows();
-  const int64_t len = u.item_length();
-  p.start = u.start + i * len;
+  p.start = u.start + i * u.item_length();
   p.item = u.item + i;
   p.row = row % u.tile_rows();
-  p.w0 = worker_of(a, p.start + kCostItem, total);
-  p.n = worker_of(a, p.start + len - u.cost(), total) - p.w0 + 1;
+  if (p.item >= a.pieces[kind] - a.workers) return p;
+  const int2 span = a.span[kind][p.item];
+  p.w0 = span.x;
+  p.whole = span.y < 0;
+  p.n = (p.whole ? ~span.y : span.y) - span.x + 1;
   return p;
 }
 
@@ -1001,7 +1042,8 @@ __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
   constexpr int per = DP / kWave;  // elements of a lane, consecutive
   constexpr int kAhead = 4;        // pieces read at a time
   const int lane = lane_id();
-  const int64_t total = a.units[a.g.n_groups + a.b.n_seqs].start;
+  const int count = a.g.n_groups + a.b.n_seqs;
+  const int64_t prefix = a.units[count].start, suffix = a.units[count + 1].start - prefix;
   const int64_t stride = (int64_t)gridDim.x * kWaves;
   for (int64_t i = (int64_t)blockIdx.x * kWaves + wave_uniform(threadIdx.x / kWave); i < rows;
        i += stride) {
@@ -1021,14 +1063,10 @@ __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
     part[0].n = 0;
     if (su.group >= 0) {
       pu = a.units[su.group];
-      part[0] = part_of(a, pu, token, head % a.share, kvh, total);
+      part[0] = part_of(a, pu, 0, token, head % a.share, kvh);
     }
-    part[1] = part_of(a, su, token, head % a.share, kvh, total);
-    // Written whole by the first launch.
-    if (part[1].n > 0 && su.lo == 0 &&
-        tiles_before(su, part[1].start, begin_of(a, part[1].w0, total)) == 0 &&
-        tiles_before(su, part[1].start, begin_of(a, (int64_t)part[1].w0 + 1, total)) == su.tiles())
-      continue;
+    part[1] = part_of(a, su, 1, token, head % a.share, kvh);
+    if (part[1].whole) continue;
     const int most = part[0].n + part[1].n;
     float m = -__builtin_inff(), l = 0.0f, o[per] = {};
     for (int k0 = 0; k0 < most; k0 += kWave) {
@@ -1039,9 +1077,9 @@ __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
       const int w = p.w0 + (pre ? k : k - part[0].n);
       int64_t at = -1;
       float2 st = make_float2(-__builtin_inff(), 0.0f);
-      if (k < most && tiles_before(u, p.start, begin_of(a, w, total)) <
-                          tiles_before(u, p.start, begin_of(a, (int64_t)w + 1, total))) {
-        const int kind = pre ? 0 : 1;
+      const int kind = pre ? 0 : 1;
+      const Range r = range_of(a, kind, w, prefix, suffix);
+      if (k < most && tiles_before(u, p.start, r.begin) < tiles_before(u, p.start, r.end)) {
         const int64_t number = (int64_t)w + p.item;
         if (number < a.pieces[kind]) {
           at = number * a.rows[kind] + p.row;
@@ -1104,7 +1142,7 @@ struct Layout {
   int dim;  // padded head size
   int workers;
   int pieces[2], rows[2];
-  size_t units, stat[2], sum[2], bytes;
+  size_t units, span[2], stat[2], sum[2], bytes;
 };
 
 size_t up(size_t n) { return (n + 255) & ~(size_t)255; }
@@ -1128,8 +1166,10 @@ Layout layout(const ep_kv_cache& c, int n_seqs, int n_groups, int n_tokens, int 
   size_t at = 0;
   const int64_t units = (int64_t)n_seqs + n_groups;
   l.units = at;
-  at += up((size_t)(units + 1) * sizeof(Unit));
+  at += up((size_t)(units + 2) * sizeof(Unit));
   for (int k = 0; k < 2; ++k) {
+    l.span[k] = at;
+    at += up((size_t)l.pieces[k] * sizeof(int2));
     l.stat[k] = at;
     at += up((size_t)l.pieces[k] * l.rows[k] * 8);
     l.sum[k] = at;
@@ -1185,6 +1225,7 @@ hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                  max_new,
                  l.workers,
                  (Unit*)(p + l.units),
+                 {(int2*)(p + l.span[0]), (int2*)(p + l.span[1])},
                  {(float*)(p + l.sum[0]), (float*)(p + l.sum[1])},
                  {(float2*)(p + l.stat[0]), (float2*)(p + l.stat[1])},
                  {l.pieces[0], l.pieces[1]},
