@@ -47,6 +47,7 @@ constexpr int kBlock = 256;
 constexpr int kWaves = kBlock / kWave;
 constexpr int kTile = 128;       // keys of a tile
 constexpr int kNone = 0x7fffffff;
+constexpr int kMostKeys = 0x7fffffff - 1024;
 constexpr int kRowsSplit = 32;   // rows of an item whose keys the waves share out
 constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
 constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
@@ -87,6 +88,7 @@ struct Attend {
   float scale;
   int heads, share, max_new;  // share: query heads per KV head
   int workers;
+  uint32_t page_magic, page_shift;  // t / page_tokens = mulhi(t, magic) >> shift
   // Workspace: the units, with the lengths of the lines behind the last as the
   // starts of two more; per item the workgroups that hold its first and last
   // tile (the last as its complement where the item was written whole); and
@@ -119,9 +121,32 @@ __device__ __forceinline__ int clamp_int(int64_t v, int64_t lo, int64_t hi) {
   return (int)(v < lo ? lo : v > hi ? hi : v);
 }
 
+// Keys that a row of the table holds; positions stay under 2^31 with room for
+// two steps.
 __device__ __forceinline__ int key_cap(const Attend& a) {
   const int64_t cap = (int64_t)a.b.max_pages * a.c.page_tokens;
-  return cap < 0x7fffffff ? (int)cap : 0x7fffffff;
+  return cap < kMostKeys ? (int)cap : kMostKeys;
+}
+
+// A 64-bit value that is equal on all lanes, in scalar registers.
+__device__ __forceinline__ int64_t wave_uniform64(int64_t v) {
+  return (int64_t)((uint64_t)(uint32_t)wave_uniform((int)(uint32_t)v) |
+                   (uint64_t)(uint32_t)wave_uniform((int)(v >> 32)) << 32);
+}
+
+__device__ __forceinline__ Unit uniform_unit(const Unit& u) {
+  Unit t;
+  t.start = wave_uniform64(u.start);
+  t.item = wave_uniform(u.item);
+  t.row0 = wave_uniform(u.row0);
+  t.rows = wave_uniform(u.rows);
+  t.lo = wave_uniform(u.lo);
+  t.hi = wave_uniform(u.hi);
+  t.seq = wave_uniform(u.seq);
+  t.group = wave_uniform(u.group);
+  t.len = wave_uniform(u.len);
+  t.fresh = wave_uniform(u.fresh);
+  return t;
 }
 
 // New tokens between two offsets; 0 where the offsets are not those of a
@@ -268,6 +293,26 @@ __device__ __forceinline__ bool drop_special(u32x4& v) {
   return any;
 }
 
+// Which thread this is, opaque to the compiler at every call: what follows
+// from it is formed where it is used and not kept in registers across the
+// loops over items and tiles, which leave none to spare.
+struct Who {
+  int tid, lane, half, wave;  // half: of the wave; wave: scalar
+};
+
+__device__ __forceinline__ Who who() {
+  uint32_t t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return Who{(int)t, (int)(t % kWave), (int)(t % kWave / 32), wave_uniform((int)(t / kWave))};
+}
+
+__device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
+  const int at = lane * 4;
+  const int lo = __builtin_amdgcn_ds_bpermute(at, (int)(uint32_t)v);
+  const int hi = __builtin_amdgcn_ds_bpermute(at, (int)(v >> 32));
+  return (int64_t)((uint64_t)(uint32_t)lo | (uint64_t)(uint32_t)hi << 32);
+}
+
 // Source of the chunks that hold nothing: keys without a slot, and the part
 // of a padded row behind the head.
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
@@ -305,23 +350,33 @@ struct Stage {
   __device__ __forceinline__ void load(const uint8_t* kb, const uint8_t* vb, int64_t slot, int tid,
                                        int head_bytes, uint8_t* lk, uint8_t* lv) {
     const int c = tid % chunks;
+    int64_t at[n];
 #pragma unroll
-    for (int j = 0; j < n; ++j) {
-      const int t = tid / chunks + j * step;
-      const int64_t at = __shfl(slot, t);
-      if constexpr (direct) {
+    for (int j = 0; j < n; ++j) at[j] = from_lane(slot, tid / chunks % kWave + j * step);
+    if constexpr (direct) {
+      const uint8_t *pk[n], *pv[n];
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const int t = tid / chunks + j * step;
         const int ck = place_k<DP>(t, c) * 16, cv = place_v<DP>(t, c) * 16;
-        const int base = wave_uniform(tid / kWave) * (kWave / chunks) + j * step;  // wave's first row
-        const uint8_t *pk = kb + ck + at, *pv = vb + cv + at;
+        pk[j] = kb + ck + at[j];
+        pv[j] = vb + cv + at[j];
         if constexpr (!ALL) {
-          if (at < 0 || ck >= head_bytes) pk = (const uint8_t*)&kZeros;
-          if (at < 0 || cv >= head_bytes) pv = (const uint8_t*)&kZeros;
+          if (at[j] < 0 || ck >= head_bytes) pk[j] = (const uint8_t*)&kZeros;
+          if (at[j] < 0 || cv >= head_bytes) pv[j] = (const uint8_t*)&kZeros;
         }
-        copy_to_lds(pk, (const lds_u8*)lk + base * DP * 2);
-        copy_to_lds(pv, (const lds_u8*)lv + base * DP * 2);
-      } else {
-        // Nothing is read past a row; what does not exist is zeroed in store().
-        const int64_t off = ALL || (at >= 0 && c * 16 < head_bytes) ? at + c * 16 : 0;
+      }
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const int base = wave_uniform(tid / kWave) * (kWave / chunks) + j * step;  // wave's first row
+        copy_to_lds(pk[j], (const lds_u8*)lk + base * DP * 2);
+        copy_to_lds(pv[j], (const lds_u8*)lv + base * DP * 2);
+      }
+    } else {
+      // Nothing is read past a row; what does not exist is zeroed in store().
+#pragma unroll
+      for (int j = 0; j < n; ++j) {
+        const int64_t off = ALL || (at[j] >= 0 && c * 16 < head_bytes) ? at[j] + c * 16 : 0;
         k[j] = *(const u32x4*)(kb + off);
         v[j] = *(const u32x4*)(vb + off);
       }
@@ -411,33 +466,96 @@ struct Rows32 {
   }
 };
 
-__device__ __forceinline__ float other_half(float v) { return __shfl_xor(v, 32); }
+// Lanes l and l + 32 both get a function of their two values.
+__device__ __forceinline__ float max_halves(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return fmaxf(__uint_as_float(x[0]), __uint_as_float(x[1]));
+}
+__device__ __forceinline__ float add_halves(float v) {
+  const auto x = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(x[0]) + __uint_as_float(x[1]);
+}
 
 // Key of register i, among 32.
 __device__ __forceinline__ int key_of(int i, int half) { return 8 * (i / 4) + 4 * half + i % 4; }
 
-// NS * 32 keys in LDS at lk and lv. c > 0: the factor of the scores in powers
-// of two. masked: some row does not see some of the keys; bit t of `see` says
-// whether this lane's row sees key t.
+// Where a lane reads the tiles: the first chunk of its row of K, and its part
+// of the first four keys of V. The chunks of the other steps are an exclusive
+// or away, since place_k and place_v are one of the chunk's number.
+template <int DP>
+struct Reads {
+  uint32_t k, v;
+
+  __device__ __forceinline__ Reads(const uint8_t* lk, const uint8_t* lv) {
+    const Who me = who();
+    const int lane = me.lane, half = me.half, col = lane % 32, i16 = lane % 16;
+    const int t = 4 * half + i16 / 4, chunk = lane / 16 % 2 * 2 + i16 % 4 / 2;
+    k = (uint32_t)(uintptr_t)(const lds_u8*)lk + col * DP * 2 + place_k<DP>(col, half) * 16;
+    v = (uint32_t)(uintptr_t)(const lds_u8*)lv + t * DP * 2 + place_v<DP>(t, chunk) * 16 +
+        i16 % 2 * 8;
+  }
+};
+
+template <typename V>
+__device__ __forceinline__ V read_lds(uint32_t at) {
+  typedef V __attribute__((address_space(3))) lds_v;
+  return *(lds_v*)at;
+}
+
+// NS * 32 keys in LDS, `at` bytes behind the tiles of `rd`. c > 0: the factor
+// of the scores in powers of two. masked: some row does not see some of the
+// keys; bit t of `see` says whether this lane's row sees key t.
 template <int DP, int QT, int NS>
-__device__ __forceinline__ void step(Rows32<DP>& r, const uint8_t* lk, const uint8_t* lv, float c,
-                                     bool masked, uint64_t see) {
-  const int lane = lane_id(), half = lane / 32, col = lane % 32;
+__device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float c, bool masked,
+                                     uint64_t see) {
+  // Opaque, so that the few addresses are formed here and not kept.
+  asm volatile("" : "+v"(rd.k), "+v"(rd.v));
   f32x16 s[NS];
 #pragma unroll
-  for (int n = 0; n < NS; ++n) {
-    s[n] = f32x16{};
+  for (int n = 0; n < NS; ++n) s[n] = f32x16{};
+  // kAhead chunks stay on their way from LDS: read one at a time, each
+  // product would wait for its own.
+  constexpr int kReads = NS * DP / 16, kAhead = 4;
+  const auto k_at = [&](int m) {
+    return read_lds<s16x8>((rd.k ^ (m / NS << 5)) + at + 32 * (m % NS) * DP * 2);
+  };
+  s16x8 kf[kAhead];
 #pragma unroll
-    for (int i = 0; i < DP / 16; ++i) {
-      const int t = 32 * n + col;
-      const s16x8 k = *(const s16x8*)(lk + t * DP * 2 + place_k<DP>(t, 2 * i + half) * 16);
-      s[n] = product<QT>(k, r.q[i], s[n]);
-    }
+  for (int m = 0; m < kAhead; ++m) kf[m] = k_at(m);
+  __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+  for (int m = 0; m < kReads; ++m) {
+    s[m % NS] = product<QT>(kf[m % kAhead], r.q[m / NS], s[m % NS]);
+    if (m + kAhead < kReads) kf[m % kAhead] = k_at(m + kAhead);
+    __builtin_amdgcn_sched_barrier(0);
   }
+  // Product m is of 16 keys (m / (DP / 32)) and 32 elements (m % (DP / 32));
+  // V for the next ones is on its way, and between the products of one 16
+  // keys stands the arithmetic of the next's weights.
+  constexpr int kCols = DP / 32, kProducts = NS * 2 * kCols;
+  const auto v_at = [&](int m) {
+    typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
+    const int d = m % kCols, key = m / kCols * 16 * DP * 2;
+    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4*)((rd.v ^ (d << 6)) + at + key));
+    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+        (lds_s16x4*)((rd.v ^ (d << 6) ^ 32) + at + key + 8 * DP * 2));
+    s16x8 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      v[j] = lo[j];
+      v[4 + j] = hi[j];
+    }
+    return v;
+  };
+  s16x8 vf[kAhead];
+#pragma unroll
+  for (int m = 0; m < kAhead; ++m) vf[m] = v_at(m);
+  __builtin_amdgcn_sched_barrier(0);
   if (masked) {
 #pragma unroll
     for (int n = 0; n < NS; ++n) {
-      const int bits = (int)(uint32_t)(see >> (32 * n + 4 * half));
+      const int bits = (int)(uint32_t)(see >> (32 * n + 4 * who().half));
 #pragma unroll
       for (int i = 0; i < 16; ++i) {
         const uint32_t keep = (uint32_t)(bits << (31 - (8 * (i / 4) + i % 4)) >> 31);
@@ -450,7 +568,7 @@ __device__ __forceinline__ void step(Rows32<DP>& r, const uint8_t* lk, const uin
   for (int n = 0; n < NS; ++n)
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
-  top = fmaxf(top, other_half(top));
+  top = max_halves(top);
   // m need not be the maximum, only near it: it follows when a row's scores
   // pass it by 2^kSlack, which keeps every weight under 2^kSlack and spares
   // the rescale of the sums most of the time (with the maximum itself, some
@@ -470,57 +588,33 @@ __device__ __forceinline__ void step(Rows32<DP>& r, const uint8_t* lk, const uin
   }
   const float base = r.m == -__builtin_inff() ? 0.0f : r.m * c;
   float sum = 0.0f;
+  // The weights meet V in the rows' 16-bit type: half a step of it, relative,
+  // per weight; the sum of weights is taken before.
+  typename Fmt<QT>::vec8 w[2];
+  const auto weights = [&](int g, int j0, int j1) {
 #pragma unroll
-  for (int n = 0; n < NS; ++n)
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      s[n][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[n][i], c, -base));
-      sum += s[n][i];
+    for (int j = j0; j < j1; ++j) {
+      const float e =
+          __builtin_amdgcn_exp2f(__builtin_fmaf(s[g / 2][8 * (g % 2) + j], c, -base));
+      sum += e;
+      w[g % 2][j] = (typename Fmt<QT>::elem)e;
     }
+  };
+  weights(0, 0, 8);
+#pragma unroll
+  for (int m = 0; m < kProducts; ++m) {
+    const int g = m / kCols, d = m % kCols;
+    r.o[d] = product<QT>(vf[m % kAhead], as<s16x8>(w[g % 2]), r.o[d]);
+    if (m + kAhead < kProducts) vf[m % kAhead] = v_at(m + kAhead);
+    if (g + 1 < 2 * NS) weights(g + 1, d * 8 / kCols, (d + 1) * 8 / kCols);
+    __builtin_amdgcn_sched_barrier(0);
+  }
   r.l += sum;
-  const lds_u8* v0 = (const lds_u8*)lv;
-  const int i16 = lane % 16, part = (lane / 16) % 2;
-#pragma unroll
-  for (int n = 0; n < NS; ++n)
-#pragma unroll
-    for (int k = 0; k < 2; ++k) {
-      // The weights meet V in the rows' 16-bit type: half a step of it,
-      // relative, per weight; the sum of weights is taken before.
-      s16x8 p;
-      if constexpr (QT == EP_DTYPE_BF16) {
-        bf16x8 w;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = (__bf16)s[n][8 * k + j];
-        p = as<s16x8>(w);
-      } else {
-        f16x8 w;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) w[j] = (_Float16)s[n][8 * k + j];
-        p = as<s16x8>(w);
-      }
-      const int t = 32 * n + 16 * k + 4 * half + i16 / 4;
-#pragma unroll
-      for (int d = 0; d < DP / 32; ++d) {
-        const int ch = 4 * d + 2 * part + i16 % 4 / 2, in = i16 % 2 * 8;
-        typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
-        const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4*)(v0 + t * DP * 2 + place_v<DP>(t, ch) * 16 + in));
-        const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-            (lds_s16x4*)(v0 + (t + 8) * DP * 2 + place_v<DP>(t + 8, ch) * 16 + in));
-        s16x8 v;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          v[j] = lo[j];
-          v[4 + j] = hi[j];
-        }
-        r.o[d] = product<QT>(v, p, r.o[d]);
-      }
-    }
 }
 
 // Bits of the keys t0 .. t0 + 63 below `limit`.
-__device__ __forceinline__ uint64_t below(int limit, int64_t t0) {
-  const int64_t n = limit - t0;
+__device__ __forceinline__ uint64_t below(int limit, int t0) {
+  const int n = limit - t0;
   return n >= 64 ? ~0ull : n <= 0 ? 0 : (1ull << n) - 1;
 }
 
@@ -555,24 +649,22 @@ struct Body {
     uint32_t in;  // slot within the page; kNone: no key
   };
 
-  __device__ __forceinline__ Lookup look_up(int64_t t) const {
-    Lookup l{0, (uint32_t)kNone};
-    if (t < u.hi) {
-      const uint32_t page = (uint32_t)t / (uint32_t)a.c.page_tokens;
-      l.in = (uint32_t)t - page * (uint32_t)a.c.page_tokens;
-      l.page = a.b.tables[(int64_t)u.seq * a.b.max_pages + page];
-    }
-    return l;
+  __device__ __forceinline__ Lookup look_up(int t) const {
+    // Keys past the end read the last one's entry: no branch around the load.
+    const int last = t < u.hi ? t : u.hi - 1;
+    const uint32_t page = a.page_magic ? __umulhi((uint32_t)last, a.page_magic) >> a.page_shift
+                                       : (uint32_t)last;
+    const uint32_t in = (uint32_t)last - page * (uint32_t)a.c.page_tokens;
+    return Lookup{(a.b.tables + (int64_t)u.seq * a.b.max_pages)[page],
+                  t < u.hi ? in : (uint32_t)kNone};
   }
 
   // Byte offset of the slot, or -1.
   __device__ __forceinline__ int64_t slot_of(const Lookup& l, bool* bad) const {
-    if (l.in == (uint32_t)kNone) return -1;
-    if (l.page < 0 || l.page >= a.c.n_pages) {
-      *bad = true;
-      return -1;
-    }
-    return l.page * a.c.page_stride + (int64_t)l.in * a.c.token_stride;
+    const bool in = (uint32_t)l.page < (uint32_t)a.c.n_pages;
+    *bad |= !in && l.in != (uint32_t)kNone;
+    return in && l.in != (uint32_t)kNone
+               ? l.page * a.c.page_stride + (int64_t)l.in * a.c.token_stride : -1;
   }
 
   __device__ __forceinline__ int token_of(int row) const { return u.row0 + row / a.share; }
@@ -580,35 +672,46 @@ struct Body {
     return kvh * a.share + row % a.share;
   }
 
+  // The head size, opaque to the compiler: comparisons with it are not worth
+  // keeping in registers across the tiles.
+  __device__ __forceinline__ int dim() const {
+    int d = a.c.head_dim;
+    asm volatile("" : "+s"(d));
+    return d;
+  }
+
+  // Keys below it are seen by a row of the unit.
+  __device__ __forceinline__ int limit_of(int row) const {
+    const int token = token_of(row);
+    if (!prefix) return clamp_int((int64_t)u.len - u.fresh + (token - u.row0) + 1, 0, u.hi);
+    if (!sh.any_short) return u.hi;
+    int lo = u.seq, hi = a.g.group_off[u.group + 1];
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) / 2;
+      if ((a.b.q_off ? a.b.q_off[mid] : mid) <= token) lo = mid;
+      else hi = mid;
+    }
+    const int last = a.b.q_off ? a.b.q_off[lo + 1] : lo + 1;
+    return clamp_int((int64_t)a.b.lens[lo] - (last - token) + 1, 0, u.hi);
+  }
+
   __device__ __forceinline__ void load_rows(Rows32<DP>& r, int row0) const {
-    const int lane = lane_id(), half = lane / 32;
-    const int row = row0 + lane % 32;
+    const Who me = who();
+    const int half = me.half, row = row0 + me.lane % 32;
     r.clear();
     r.row = row < u.rows ? row : -1;
     const int have = row < u.rows ? row : u.rows - 1;
     const int token = token_of(have);
     // Rows past the unit's end see what the unit holds, so that they ask
     // for no masking.
-    r.limit = u.hi;
-    if (!prefix) {
-      r.limit = clamp_int((int64_t)u.len - u.fresh + (token - u.row0) + 1, 0, u.hi);
-    } else if (sh.any_short) {
-      int lo = u.seq, hi = a.g.group_off[u.group + 1];
-      while (hi - lo > 1) {
-        const int mid = (lo + hi) / 2;
-        if ((a.b.q_off ? a.b.q_off[mid] : mid) <= token) lo = mid;
-        else hi = mid;
-      }
-      const int last = a.b.q_off ? a.b.q_off[lo + 1] : lo + 1;
-      r.limit = clamp_int((int64_t)a.b.lens[lo] - (last - token) + 1, 0, u.hi);
-    }
+    r.limit = row < u.rows ? limit_of(row) : u.hi;
     const uint8_t* p = (const uint8_t*)a.q.p + (int64_t)token * a.q.token_stride +
                        (int64_t)head_of(have) * a.q.head_stride;
 #pragma unroll
     for (int i = 0; i < DP / 16; ++i) {
       const int d = 16 * i + 8 * half;
       u32x4 w = {0, 0, 0, 0};
-      if (d < a.c.head_dim) w = *(const u32x4*)(p + 2 * d);
+      if (d < dim()) w = *(const u32x4*)(p + 2 * d);
       if (negate) w ^= u32x4{0x80008000u, 0x80008000u, 0x80008000u, 0x80008000u};
       r.q[i] = as<s16x8>(w);
     }
@@ -626,24 +729,31 @@ struct Body {
   }
 
   // Infinities and NaN of V at keys that some rows may not see went to LDS as
-  // zeros, since 0 * inf would reach those rows. Here the rows that see such
-  // a key get them: a positive weight changes neither. Keys [t0, end).
-  __device__ __forceinline__ void add_special(Rows32<DP>& r, int64_t t0, int64_t end) const {
-    const int half = lane_id() / 32;
-    for (int64_t t = t0; t < end; ++t) {
+  // zeros, since 0 * inf would reach those rows. Here the rows of the piece
+  // that see such a key get them, after put() by the whole workgroup: a
+  // positive weight changes neither. Keys [t0, end).
+  __device__ __forceinline__ void add_special(int64_t number, bool whole, int t0, int end) const {
+    __syncthreads();
+    const int kind = prefix ? 0 : 1, rows = u.tile_rows();
+    if (!whole && number >= a.pieces[kind]) return;
+    for (int t = t0; t < end; ++t) {
       bool bad = false;
       const int64_t at = slot_of(look_up(t), &bad);
-      if (at < 0 || t >= r.limit) continue;
-#pragma unroll
-      for (int d = 0; d < DP / 32; ++d) {
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          const int e = 32 * d + key_of(i, half);
-          if (e >= a.c.head_dim) continue;
-          const float x = load1<CT>(vb + at + e * Fmt<CT>::bytes);
-          if (!(fabsf(x) < __builtin_inff())) r.o[d][i] += x;
+      if (at < 0) continue;
+#pragma unroll 1
+      for (int i = threadIdx.x; i < rows * DP; i += kBlock) {
+        const int in = i / DP, e = i % DP, row = index * rows + in;
+        if (e >= a.c.head_dim || row >= u.rows || t >= limit_of(row)) continue;
+        const float x = load1<CT>(vb + at + e * Fmt<CT>::bytes);
+        if (fabsf(x) < __builtin_inff()) continue;
+        if (whole) {
+          uint8_t* to = (uint8_t*)a.out.p + (int64_t)token_of(row) * a.out.token_stride +
+                        (int64_t)head_of(row) * a.out.head_stride + 2 * e;
+          store1<QT>(to, load1<QT>(to) + x);
+        } else {
+          float* to = a.sum[kind] + (number * a.rows[kind] + in) * DP + e;
+          *to += x;
         }
-        __builtin_amdgcn_sched_barrier(0);  // not all loads at once
       }
     }
   }
@@ -651,7 +761,8 @@ struct Body {
   // Rows to their place: the output where this piece is all there is, else
   // the piece's sums.
   __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole) const {
-    const int lane = lane_id(), half = lane / 32;
+    const Who me = who();
+    const int lane = me.lane, half = me.half;
     if (r.row < 0) return;
     const float m = r.m == -__builtin_inff() ? r.m : r.m * c;
     if (whole) {
@@ -665,7 +776,7 @@ struct Body {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int e = 32 * d + 8 * i + 4 * half;
-          if (e >= a.c.head_dim) continue;
+          if (e >= dim()) continue;
           typename Fmt<QT>::elem w[4];
 #pragma unroll
           for (int j = 0; j < 4; ++j) w[j] = (typename Fmt<QT>::elem)(r.o[d][4 * i + j] * inv);
@@ -696,15 +807,15 @@ struct Body {
 
   // Waves share out the rows: 32 each, all keys.
   __device__ __forceinline__ void block_rows(int64_t number, bool whole) {
-    const int tid = threadIdx.x, wave = wave_uniform(tid / kWave), lane = lane_id();
+    const Who me = who();
+    const int tid = me.tid, wave = me.wave, lane = me.lane;
     constexpr int keys = Lds<DP>::keys;
     constexpr uint64_t all = keys == 64 ? ~0ull : (1ull << keys) - 1;
     Stage<DP, QT, CT, keys, kBlock> st;
     Rows32<DP> r;
     bool bad = false;
-    int64_t t0 = u.lo + (int64_t)lo_tile * kTile;
-    const int64_t end = (int64_t)u.lo + (int64_t)hi_tile * kTile < u.hi
-                            ? (int64_t)u.lo + (int64_t)hi_tile * kTile : u.hi;
+    int t0 = u.lo + lo_tile * kTile;
+    const int end = hi_tile < u.tiles() ? u.lo + hi_tile * kTile : u.hi;
     int64_t slot = slot_of(look_up(t0 + lane % keys), &bad);
     Lookup next = look_up(t0 + keys + lane % keys);
     st.load(kb, vb, slot, tid, head_bytes, lds, lds + Lds<DP>::half);
@@ -717,6 +828,8 @@ struct Body {
     int fewest = sh.ipart[0];
 #pragma unroll
     for (int w = 1; w < kWaves; ++w) fewest = sh.ipart[w] < fewest ? sh.ipart[w] : fewest;
+    fewest = wave_uniform(fewest);
+    const Reads<DP> rd(lds, lds + Lds<DP>::half);
     const bool busy = index * kRowsBlock + wave * 32 < u.rows;
     // A step's tiles are complete once every wave has seen its own copies
     // land and met the others; they may be overwritten when all have met
@@ -732,7 +845,7 @@ struct Body {
       int special = kNone;
       if (edge) special = st.template store<true>(lk, lv, valid, tid, head_bytes);
       else st.template store<false>(lk, lv, valid, tid, head_bytes);
-      if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
+      if (special != kNone) atomicMin(&sh.special, t0 + special);
       __syncthreads();
       if (t0 + keys < end) {
         slot = slot_of(next, &bad);
@@ -741,7 +854,7 @@ struct Body {
         next = look_up(t0 + 2 * keys + lane % keys);
       }
       if (busy)
-        step<DP, QT, keys / 32>(r, lk, lv, c, t0 + keys > least || valid != all,
+        step<DP, QT, keys / 32>(r, rd, BUF * 2 * Lds<DP>::half, c, t0 + keys > least || valid != all,
                                 valid & below(r.limit, t0));
       t0 += keys;
     };
@@ -751,23 +864,24 @@ struct Body {
       one(std::integral_constant<int, 1>());
       if (t0 >= end) break;
     }
-    if (sh.special < end) add_special(r, sh.special, end);
     if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
-    r.l += other_half(r.l);
+    r.l = add_halves(r.l);
     put(r, number, whole);
+    const int special = wave_uniform(sh.special);
+    if (special < end) add_special(number, whole, special, end);
     __syncthreads();  // LDS is free for the next item
   }
 
   // Waves share out the keys: 32 of every 128 each, the same rows; their
   // sums are joined at the end.
   __device__ __forceinline__ void split_keys(int64_t number, bool whole) {
-    const int tid = threadIdx.x, wave = wave_uniform(tid / kWave), lane = lane_id();
+    const Who me = who();
+    const int tid = me.tid, wave = me.wave, lane = me.lane;
     Stage<DP, QT, CT, 32, kWave> st;
     Rows32<DP> r;
     bool bad = false;
-    int64_t t0 = u.lo + (int64_t)lo_tile * kTile + wave * 32;
-    const int64_t end = (int64_t)u.lo + (int64_t)hi_tile * kTile < u.hi
-                            ? (int64_t)u.lo + (int64_t)hi_tile * kTile : u.hi;
+    int t0 = u.lo + lo_tile * kTile + wave * 32;
+    const int end = hi_tile < u.tiles() ? u.lo + hi_tile * kTile : u.hi;
     uint8_t* lk = lds + wave * Lds<DP>::wave;
     uint8_t* lv = lk + Lds<DP>::wave / 2;
     int64_t slot = -1;
@@ -778,6 +892,7 @@ struct Body {
       st.load(kb, vb, slot, lane, head_bytes, lk, lv);
     }
     load_rows(r, index * kRowsSplit);
+    const Reads<DP> rd(lk, lv);
     const int least = least_limit(r);
     if (tid == 0) sh.special = kNone;
     __syncthreads();
@@ -788,7 +903,7 @@ struct Body {
       int special = kNone;
       if (edge) special = st.template store<true>(lk, lv, valid, lane, head_bytes);
       else st.template store<false>(lk, lv, valid, lane, head_bytes);
-      if (special != kNone) atomicMin(&sh.special, (int)(t0 + special));
+      if (special != kNone) atomicMin(&sh.special, t0 + special);
       if constexpr (!decltype(st)::direct) {
         if (t0 + kTile < end) {
           slot = slot_of(next, &bad);
@@ -796,7 +911,7 @@ struct Body {
           next = look_up(t0 + 2 * kTile + lane % 32);
         }
       }
-      step<DP, QT, 1>(r, lk, lv, c, edge, valid & below(r.limit, t0));
+      step<DP, QT, 1>(r, rd, 0, c, edge, valid & below(r.limit, t0));
       if constexpr (decltype(st)::direct) {
         if (t0 + kTile < end) {
           slot = slot_of(next, &bad);
@@ -808,7 +923,7 @@ struct Body {
       }
     }
     if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
-    r.l += other_half(r.l);
+    r.l = add_halves(r.l);
     // Join: the common maximum, then the sums of waves 2, 3 to 0, 1 and of 1
     // to 0 through LDS.
     if (lane < 32) sh.stat[0][wave][lane] = r.m;
@@ -852,10 +967,10 @@ struct Body {
       }
       __syncthreads();
     }
-    if (wave == 0) {
-      if (sh.special < end) add_special(r, sh.special, end);
-      put(r, number, whole);
-    }
+    if (wave == 0) put(r, number, whole);
+    const int special = wave_uniform(sh.special);
+    if (special < end) add_special(number, whole, special, end);
+    __syncthreads();  // everyone has read sh.special
   }
 
   // Tiles [lo_tile, hi_tile) of an item.
@@ -937,7 +1052,7 @@ __device__ __forceinline__ void place_units(const Attend& a, Shared& sh, int bas
 
 template <int DP, int QT, int CT>
 __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Attend a) {
-  __shared__ __attribute__((aligned(16))) uint8_t lds[Lds<DP>::bytes];
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[Lds<DP>::bytes];
   __shared__ Shared sh;
   const int tid = threadIdx.x;
   const int units = a.g.n_groups + a.b.n_seqs;
@@ -948,7 +1063,8 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
   int64_t total = 0;
   int32_t item[2] = {0, 0};
   for (int base = 0; base < units; base += kBlock) place_units(a, sh, base, total, item);
-  const int64_t prefix = sh.prefix;
+  total = wave_uniform64(total);
+  const int64_t prefix = wave_uniform64(sh.prefix);
   const bool scribe = blockIdx.x == 0;
   const int per_xcd = a.workers / kXcds;
   const int w = blockIdx.x % kXcds * per_xcd + blockIdx.x / kXcds;
@@ -962,8 +1078,12 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
     item[0] = item[1] = 0;
     for (int base = 0; base < units && (write || at < end); base += kBlock) {
       const int64_t from = at;
-      if (units > kBlock) place_units(a, sh, base, at, item);
-      else at = total;
+      if (units > kBlock) {
+        place_units(a, sh, base, at, item);
+        at = wave_uniform64(at);
+      } else {
+        at = total;
+      }
       const int count = units - base < kBlock ? units - base : kBlock;
       if (write && tid < count) a.units[base + tid] = sh.unit[tid];
       if (begin >= at || end <= from || begin == end) continue;
@@ -973,8 +1093,8 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
       __syncthreads();
       if (tid < count && sh.unit[tid].start <= begin && begin < stop) sh.first = tid;
       __syncthreads();
-      for (int k = sh.first; k < count; ++k) {
-        const Unit v = sh.unit[k];
+      for (int k = wave_uniform(sh.first); k < count; ++k) {
+        const Unit v = uniform_unit(sh.unit[k]);
         if (v.start >= end) break;
         const int64_t len = v.item_length();
         if (len == 0) continue;
@@ -1141,6 +1261,7 @@ __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
 struct Layout {
   int dim;  // padded head size
   int workers;
+  uint32_t page_magic, page_shift;  // t / page_tokens = mulhi(t, magic) >> shift
   int pieces[2], rows[2];
   size_t units, span[2], stat[2], sum[2], bytes;
 };
@@ -1213,6 +1334,14 @@ hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                             hipStream_t stream) {
   const Layout l = layout(c, b.n_seqs, g.n_groups, b.n_tokens, n_heads, max_new);
   char* p = (char*)ws;
+  // For d > 1 with 2^(l - 1) < d <= 2^l: magic = floor(2^(31 + l) / d) + 1 fits
+  // 32 bits, and mulhi(t, magic) >> (l - 1) = t / d for t < 2^31, since magic d
+  // is past 2^(31 + l) by at most d <= 2^l.
+  uint32_t magic = 0, shift = 0;
+  if (c.page_tokens > 1) {
+    while ((int64_t)1 << (shift + 1) < c.page_tokens) ++shift;
+    magic = (uint32_t)(((uint64_t)1 << (32 + shift)) / (uint64_t)c.page_tokens) + 1;
+  }
   const Attend a{c,
                  b,
                  g,
@@ -1224,6 +1353,8 @@ hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                  n_heads / c.n_heads,
                  max_new,
                  l.workers,
+                 magic,
+                 shift,
                  (Unit*)(p + l.units),
                  {(int2*)(p + l.span[0]), (int2*)(p + l.span[1])},
                  {(float*)(p + l.sum[0]), (float*)(p + l.sum[1])},
