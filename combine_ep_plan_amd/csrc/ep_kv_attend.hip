@@ -51,6 +51,7 @@ constexpr int kMostKeys = 0x7fffffff - 1024;
 constexpr int kRowsSplit = 32;   // rows of an item whose keys the waves share out
 constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
 constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
+constexpr int kSoloRows = 256;   // rows a sequence from which on it shares nothing
 // Costs in the line: of a tile of either kind, and of starting on an item.
 constexpr int kCostSplit = 4;
 constexpr int kCostBlock = 4;
@@ -155,11 +156,26 @@ __device__ __forceinline__ int fresh_of(const Attend& a, int lo, int hi) {
   return lo >= 0 && hi > lo && hi <= a.b.n_tokens ? hi - lo : 0;
 }
 
+// Shared tokens of the group of sequences s0 .. s1 - 1. A group whose
+// sequences bring kSoloRows rows or more on average fills its items without
+// sharing: each sequence then reads all its keys itself, which costs a part of
+// an item per sequence and spares the joining of two pieces per row (rows of
+// 12 prompts of 128 tokens behind an 8k prefix: XXX).
+__device__ __forceinline__ int shared_of(const Attend& a, int j, int s0, int s1) {
+  const int shared = a.g.shared[j];
+  if (s0 < 0 || s0 >= s1 || s1 > a.b.n_seqs) return shared;
+  const int64_t rows =
+      (int64_t)(a.b.q_off ? a.b.q_off[s1] - a.b.q_off[s0] : s1 - s0) * a.share;
+  return rows >= (int64_t)kSoloRows * (s1 - s0) ? 0 : shared;
+}
+
 // Reads the groups' ranges into LDS where they fit; a barrier must follow.
 __device__ __forceinline__ void load_groups(const Attend& a, Shared& sh) {
-  if (a.g.n_groups > kGroupTable) return;
-  if ((int)threadIdx.x <= a.g.n_groups) sh.group_off[threadIdx.x] = a.g.n_groups > 0 ? a.g.group_off[threadIdx.x] : 0;
-  if ((int)threadIdx.x < a.g.n_groups) sh.shared[threadIdx.x] = a.g.shared[threadIdx.x];
+  const int j = threadIdx.x;
+  if (a.g.n_groups > kGroupTable || j > a.g.n_groups || a.g.n_groups == 0) return;
+  const int s0 = a.g.group_off[j];
+  sh.group_off[j] = s0;
+  if (j < a.g.n_groups) sh.shared[j] = shared_of(a, j, s0, a.g.group_off[j + 1]);
 }
 
 // The group of sequence s, or -1: the last one that starts at or before it.
@@ -187,7 +203,10 @@ __device__ __forceinline__ Unit unit_of(const Attend& a, const Shared& sh, int u
     const int lo = a.b.q_off ? a.b.q_off[s] : s, hi = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
     t.len = a.b.lens[s];
     t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
-    const int shared = t.group < 0 ? 0 : kept ? sh.shared[t.group] : a.g.shared[t.group];
+    const int shared = t.group < 0 ? 0
+                       : kept ? sh.shared[t.group]
+                              : shared_of(a, t.group, a.g.group_off[t.group],
+                                          a.g.group_off[t.group + 1]);
     t.row0 = lo;
     t.fresh = fresh_of(a, lo, hi);
     t.rows = (t.fresh < a.max_new ? t.fresh : a.max_new) * a.share;
@@ -206,7 +225,7 @@ __device__ __forceinline__ Unit unit_of(const Attend& a, const Shared& sh, int u
       if (!a.b.q_off && hi > a.b.n_tokens) hi = a.b.n_tokens;
       t.row0 = lo;
       t.rows = fresh_of(a, lo, hi) * a.share;
-      t.hi = clamp_int(kept ? sh.shared[u] : a.g.shared[u], 0, key_cap(a));
+      t.hi = clamp_int(kept ? sh.shared[u] : shared_of(a, u, s0, s1), 0, key_cap(a));
     }
   }
   return t;
@@ -342,53 +361,40 @@ struct Stage {
   static constexpr int n = KEYS / step;
   static_assert(THREADS % chunks == 0 && KEYS % step == 0, "a pass takes whole rows");
   u32x4 k[direct ? 1 : n], v[direct ? 1 : n];
+  int64_t at[n];
 
   // slot: this lane's key's byte offset, lane i holding key i (mod KEYS);
-  // -1: none. lk, lv: where the tiles will be (written here if direct).
-  // ALL: every key has a slot and rows fill their place.
-  template <bool ALL>
-  __device__ __forceinline__ void load(const uint8_t* kb, const uint8_t* vb, int64_t slot, int tid,
-                                       int head_bytes, uint8_t* lk, uint8_t* lv) {
-    const int c = tid % chunks;
-    int64_t at[n];
+  // -1: none. Where each row of this thread's starts, or -1.
+  __device__ __forceinline__ void find(int64_t slot, int tid) {
 #pragma unroll
     for (int j = 0; j < n; ++j) at[j] = from_lane(slot, tid / chunks % kWave + j * step);
+  }
+
+  // Row j: to LDS at lk and lv where the tiles will be, or to registers.
+  __device__ __forceinline__ void copy(int j, const uint8_t* kb, const uint8_t* vb, int tid,
+                                       int head_bytes, uint8_t* lk, uint8_t* lv) {
+    const int c = tid % chunks;
     if constexpr (direct) {
-      const uint8_t *pk[n], *pv[n];
-#pragma unroll
-      for (int j = 0; j < n; ++j) {
-        const int t = tid / chunks + j * step;
-        const int ck = place_k<DP>(t, c) * 16, cv = place_v<DP>(t, c) * 16;
-        pk[j] = kb + ck + at[j];
-        pv[j] = vb + cv + at[j];
-        if constexpr (!ALL) {
-          if (at[j] < 0 || ck >= head_bytes) pk[j] = (const uint8_t*)&kZeros;
-          if (at[j] < 0 || cv >= head_bytes) pv[j] = (const uint8_t*)&kZeros;
-        }
-      }
-#pragma unroll
-      for (int j = 0; j < n; ++j) {
-        const int base = wave_uniform(tid / kWave) * (kWave / chunks) + j * step;  // wave's first row
-        copy_to_lds(pk[j], (const lds_u8*)lk + base * DP * 2);
-        copy_to_lds(pv[j], (const lds_u8*)lv + base * DP * 2);
-      }
+      const int t = tid / chunks + j * step;
+      const int ck = place_k<DP>(t, c) * 16, cv = place_v<DP>(t, c) * 16;
+      const int base = wave_uniform(tid / kWave) * (kWave / chunks) + j * step;  // wave's first row
+      copy_to_lds(at[j] >= 0 && ck < head_bytes ? kb + ck + at[j] : (const uint8_t*)&kZeros,
+                  (const lds_u8*)lk + base * DP * 2);
+      copy_to_lds(at[j] >= 0 && cv < head_bytes ? vb + cv + at[j] : (const uint8_t*)&kZeros,
+                  (const lds_u8*)lv + base * DP * 2);
     } else {
       // Nothing is read past a row; what does not exist is zeroed in store().
-#pragma unroll
-      for (int j = 0; j < n; ++j) {
-        const int64_t off = ALL || (at[j] >= 0 && c * 16 < head_bytes) ? at[j] + c * 16 : 0;
-        k[j] = *(const u32x4*)(kb + off);
-        v[j] = *(const u32x4*)(vb + off);
-      }
+      const int64_t off = at[j] >= 0 && c * 16 < head_bytes ? at[j] + c * 16 : 0;
+      k[j] = *(const u32x4*)(kb + off);
+      v[j] = *(const u32x4*)(vb + off);
     }
   }
 
   __device__ __forceinline__ void load(const uint8_t* kb, const uint8_t* vb, int64_t slot, int tid,
                                        int head_bytes, uint8_t* lk, uint8_t* lv) {
-    if (ballot(slot < 0) == 0 && head_bytes == DP * cb)
-      load<true>(kb, vb, slot, tid, head_bytes, lk, lv);
-    else
-      load<false>(kb, vb, slot, tid, head_bytes, lk, lv);
+    find(slot, tid);
+#pragma unroll
+    for (int j = 0; j < n; ++j) copy(j, kb, vb, tid, head_bytes, lk, lv);
   }
 
   // Finishes the tiles. CHECK: infinities and NaN of V are zeroed in LDS;
@@ -505,9 +511,15 @@ __device__ __forceinline__ V read_lds(uint32_t at) {
 // NS * 32 keys in LDS, `at` bytes behind the tiles of `rd`. c > 0: the factor
 // of the scores in powers of two. masked: some row does not see some of the
 // keys; bit t of `see` says whether this lane's row sees key t.
-template <int DP, int QT, int NS>
+// between(m) stands behind product m of the scores, m < kScoreProducts.
+template <int DP, int NS>
+constexpr int kScoreProducts = NS * DP / 16;
+
+template <int DP, int QT, int NS, typename F>
 __device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float c, bool masked,
-                                     uint64_t see) {
+                                     uint64_t see, F&& between) {
+  rd.k += at;
+  rd.v += at;
   // Opaque, so that the few addresses are formed here and not kept.
   asm volatile("" : "+v"(rd.k), "+v"(rd.v));
   f32x16 s[NS];
@@ -515,9 +527,9 @@ __device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float 
   for (int n = 0; n < NS; ++n) s[n] = f32x16{};
   // kAhead chunks stay on their way from LDS: read one at a time, each
   // product would wait for its own.
-  constexpr int kReads = NS * DP / 16, kAhead = 4;
+  constexpr int kReads = kScoreProducts<DP, NS>, kAhead = 4;
   const auto k_at = [&](int m) {
-    return read_lds<s16x8>((rd.k ^ (m / NS << 5)) + at + 32 * (m % NS) * DP * 2);
+    return read_lds<s16x8>((rd.k ^ (m / NS << 5)) + 32 * (m % NS) * DP * 2);
   };
   s16x8 kf[kAhead];
 #pragma unroll
@@ -527,6 +539,7 @@ __device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float 
   for (int m = 0; m < kReads; ++m) {
     s[m % NS] = product<QT>(kf[m % kAhead], r.q[m / NS], s[m % NS]);
     if (m + kAhead < kReads) kf[m % kAhead] = k_at(m + kAhead);
+    between(m);
     __builtin_amdgcn_sched_barrier(0);
   }
   // Product m is of 16 keys (m / (DP / 32)) and 32 elements (m % (DP / 32));
@@ -537,9 +550,9 @@ __device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float 
     typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
     const int d = m % kCols, key = m / kCols * 16 * DP * 2;
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_s16x4*)((rd.v ^ (d << 6)) + at + key));
+        (lds_s16x4*)((rd.v ^ (d << 6)) + key));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-        (lds_s16x4*)((rd.v ^ (d << 6) ^ 32) + at + key + 8 * DP * 2));
+        (lds_s16x4*)((rd.v ^ (d << 6) ^ 32) + key + 8 * DP * 2));
     s16x8 v;
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
@@ -626,7 +639,9 @@ struct Lds {
   static constexpr int half = keys * DP * 2;           // K or V of one
   static constexpr int block = 2 * half * 2;           // two steps
   static constexpr int wave = 2 * 32 * DP * 2;         // K and V of 32 keys
-  static constexpr int bytes = block > kWaves * wave ? block : kWaves * wave;
+  static constexpr int box = 32 * DP * 4;              // rows on their way out, of a wave
+  static constexpr int most = block > kWaves * wave ? block : kWaves * wave;
+  static constexpr int bytes = most > kWaves * box ? most : kWaves * box;
 };
 
 template <int DP, int QT, int CT>
@@ -759,50 +774,55 @@ struct Body {
   }
 
   // Rows to their place: the output where this piece is all there is, else
-  // the piece's sums.
-  __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole) const {
+  // the piece's sums. A lane holds pieces of 16 bytes of one row; they pass
+  // through the wave's `box` in LDS (32 rows of DP floats), so that whole rows
+  // are written at a time.
+  __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole,
+                                      uint8_t* box) const {
     const Who me = who();
-    const int lane = me.lane, half = me.half;
-    if (r.row < 0) return;
-    const float m = r.m == -__builtin_inff() ? r.m : r.m * c;
-    if (whole) {
-      const int token = token_of(r.row), head = head_of(r.row);
-      uint8_t* to = (uint8_t*)a.out.p + (int64_t)token * a.out.token_stride +
-                    (int64_t)head * a.out.head_stride;
-      const float vs = CT == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f;
-      const float inv = r.l == 0.0f ? 0.0f : vs / r.l;
-#pragma unroll
-      for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int e = 32 * d + 8 * i + 4 * half;
-          if (e >= dim()) continue;
-          typename Fmt<QT>::elem w[4];
-#pragma unroll
-          for (int j = 0; j < 4; ++j) w[j] = (typename Fmt<QT>::elem)(r.o[d][4 * i + j] * inv);
-          *(u32x2*)(to + 2 * e) = u32x2{
-              as<uint16_t>(w[0]) | (uint32_t)as<uint16_t>(w[1]) << 16,
-              as<uint16_t>(w[2]) | (uint32_t)as<uint16_t>(w[3]) << 16};
-        }
-      if (a.lse && half == 0)
-        a.lse[(int64_t)token * a.heads + head] =
-            r.l == 0.0f ? -__builtin_inff() : (m + log2f(r.l)) * 0.69314718055994531f;
-      return;
-    }
+    const int lane = me.lane, half = me.half, col = lane % 32;
     const int kind = prefix ? 0 : 1;
-    if (number >= a.pieces[kind]) {
+    if (!whole && number >= a.pieces[kind]) {
       if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
       return;
     }
-    const int64_t at = number * a.rows[kind] + r.row % u.tile_rows();
-    float* to = a.sum[kind] + at * DP;
+    constexpr int chunks = DP / 4;
+    float f = 1.0f;
+    if (whole) f = r.l == 0.0f ? 0.0f : (CT == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f) / r.l;
+    f32x4* lds_rows = (f32x4*)box;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        *(f32x4*)(to + 32 * d + 8 * i + 4 * half) = f32x4{
-            r.o[d][4 * i], r.o[d][4 * i + 1], r.o[d][4 * i + 2], r.o[d][4 * i + 3]};
-    if (half == 0) a.stat[kind][at] = make_float2(m, r.l);
+        lds_rows[col * chunks + ((8 * d + 2 * i + half) ^ (col % chunks))] =
+            f32x4{r.o[d][4 * i], r.o[d][4 * i + 1], r.o[d][4 * i + 2], r.o[d][4 * i + 3]} * f;
+    const int first = __builtin_amdgcn_readfirstlane(r.row);  // row of lane 0: always there
+    const float m = r.m == -__builtin_inff() ? r.m : r.m * c;
+    if (r.row >= 0 && half == 0) {
+      if (!whole)
+        a.stat[kind][number * a.rows[kind] + r.row % u.tile_rows()] = make_float2(m, r.l);
+      else if (a.lse)
+        a.lse[(int64_t)token_of(r.row) * a.heads + head_of(r.row)] =
+            r.l == 0.0f ? -__builtin_inff() : (m + log2f(r.l)) * 0.69314718055994531f;
+    }
+    const int e = lane % chunks * 4;
+#pragma unroll 4
+    for (int k = 0; k < 32 * chunks / kWave; ++k) {
+      const int in = k * (kWave / chunks) + lane / chunks, row = first + in;
+      const f32x4 x = lds_rows[in * chunks + ((lane % chunks) ^ (in % chunks))];
+      if (row >= u.rows) continue;
+      if (!whole) {
+        *(f32x4*)(a.sum[kind] + (number * a.rows[kind] + row % u.tile_rows()) * DP + e) = x;
+      } else if (e < a.c.head_dim) {
+        uint8_t* to = (uint8_t*)a.out.p + (int64_t)token_of(row) * a.out.token_stride +
+                      (int64_t)head_of(row) * a.out.head_stride + 2 * e;
+        typename Fmt<QT>::elem w[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) w[j] = (typename Fmt<QT>::elem)x[j];
+        *(u32x2*)to = u32x2{as<uint16_t>(w[0]) | (uint32_t)as<uint16_t>(w[1]) << 16,
+                            as<uint16_t>(w[2]) | (uint32_t)as<uint16_t>(w[3]) << 16};
+      }
+    }
   }
 
   // Waves share out the rows: 32 each, all keys.
@@ -833,11 +853,10 @@ struct Body {
     const bool busy = index * kRowsBlock + wave * 32 < u.rows;
     // A step's tiles are complete once every wave has seen its own copies
     // land and met the others; they may be overwritten when all have met
-    // again, in the next step. BUF is a constant, so that the tiles'
-    // addresses are too.
-    auto one = [&](auto buf) {
-      constexpr int BUF = decltype(buf)::value;
-      uint8_t* lk = lds + BUF * 2 * Lds<DP>::half;
+    // again, in the next step.
+    constexpr int kStep = 2 * Lds<DP>::half;
+    for (int buf = 0; t0 < end; t0 += keys, buf ^= kStep) {
+      uint8_t* lk = lds + buf;
       uint8_t* lv = lk + Lds<DP>::half;
       const uint64_t valid = ballot(slot >= 0) & all;
       const bool edge = t0 + keys > fewest || valid != all;
@@ -847,26 +866,40 @@ struct Body {
       else st.template store<false>(lk, lv, valid, tid, head_bytes);
       if (special != kNone) atomicMin(&sh.special, t0 + special);
       __syncthreads();
-      if (t0 + keys < end) {
-        slot = slot_of(next, &bad);
-        uint8_t* to = lds + (1 - BUF) * 2 * Lds<DP>::half;
-        st.load(kb, vb, slot, tid, head_bytes, to, to + Lds<DP>::half);
-        next = look_up(t0 + 2 * keys + lane % keys);
+      // The next step's copies are started one by one between the products
+      // of the scores: all at once they would hold the wave up, as the
+      // vector memory unit takes 64 bytes of a copy per cycle and CU.
+      const bool more = t0 + keys < end;
+      const bool masked = t0 + keys > least || valid != all;
+      const uint64_t see = valid & below(r.limit, t0);
+      uint8_t* to = lds + (buf ^ kStep);
+      const auto fetch = [&](int m, int of) {
+        if (!more) return;
+        if (m == 0) {
+          slot = slot_of(next, &bad);
+          st.find(slot, tid);
+        }
+        constexpr int n = decltype(st)::n;
+        // Copies spread over the products behind the first few.
+        const int from = of > n + 3 ? 3 : 0, gap = (of - from) / n > 0 ? (of - from) / n : 1;
+#pragma unroll
+        for (int j = 0; j < n; ++j)
+          if (m == (from + j * gap < of ? from + j * gap : of - 1))
+            st.copy(j, kb, vb, tid, head_bytes, to, to + Lds<DP>::half);
+        if (m == of - 1) next = look_up(t0 + 2 * keys + lane % keys);
+      };
+      if (busy) {
+        step<DP, QT, keys / 32>(r, rd, buf, c, masked, see, [&](int m) {
+          fetch(m, kScoreProducts<DP, keys / 32>);
+        });
+      } else {
+        fetch(0, 1);
       }
-      if (busy)
-        step<DP, QT, keys / 32>(r, rd, BUF * 2 * Lds<DP>::half, c, t0 + keys > least || valid != all,
-                                valid & below(r.limit, t0));
-      t0 += keys;
-    };
-    for (;;) {
-      one(std::integral_constant<int, 0>());
-      if (t0 >= end) break;
-      one(std::integral_constant<int, 1>());
-      if (t0 >= end) break;
     }
     if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
     r.l = add_halves(r.l);
-    put(r, number, whole);
+    __syncthreads();  // no wave reads tiles any more
+    if (busy) put(r, number, whole, lds + wave * 32 * DP * 4);
     const int special = wave_uniform(sh.special);
     if (special < end) add_special(number, whole, special, end);
     __syncthreads();  // LDS is free for the next item
@@ -911,7 +944,7 @@ struct Body {
           next = look_up(t0 + 2 * kTile + lane % 32);
         }
       }
-      step<DP, QT, 1>(r, rd, 0, c, edge, valid & below(r.limit, t0));
+      step<DP, QT, 1>(r, rd, 0, c, edge, valid & below(r.limit, t0), [](int) {});
       if constexpr (decltype(st)::direct) {
         if (t0 + kTile < end) {
           slot = slot_of(next, &bad);
@@ -967,7 +1000,7 @@ struct Body {
       }
       __syncthreads();
     }
-    if (wave == 0) put(r, number, whole);
+    if (wave == 0) put(r, number, whole, lds);
     const int special = wave_uniform(sh.special);
     if (special < end) add_special(number, whole, special, end);
     __syncthreads();  // everyone has read sh.special
