@@ -332,8 +332,8 @@ __device__ __forceinline__ int64_t from_lane(int64_t v, int lane) {
   return (int64_t)((uint64_t)(uint32_t)lo | (uint64_t)(uint32_t)hi << 32);
 }
 
-// Source of the chunks that hold nothing: keys without a slot, and the part
-// of a padded row behind the head.
+// Source of the chunks that hold nothing: the part of a padded row behind the
+// head.
 __device__ const u32x4 kZeros = {0, 0, 0, 0};
 
 // Starts the copy of 16 bytes per lane to LDS, lane l's to `to` + 16 l. It
@@ -351,8 +351,8 @@ __device__ __forceinline__ void settle_copies() { asm volatile("s_waitcnt vmcnt(
 // (whole waves). 16-bit rows of up to 128 elements are copied to LDS without
 // passing through registers: a copy fills 1024 bytes of LDS in order, so the
 // order of the chunks is made by what each lane reads. Others go through
-// registers: e4m3 rows are widened on the way.
-template <int DP, int QT, int CT, int KEYS, int THREADS>
+// registers: e4m3 rows are widened on the way. FULL: the head fills its place.
+template <int DP, int QT, int CT, bool FULL, int KEYS, int THREADS>
 struct Stage {
   static constexpr int cb = Fmt<CT>::bytes;
   static constexpr bool direct = cb == 2 && DP <= 128;
@@ -364,10 +364,12 @@ struct Stage {
   int64_t at[n];
 
   // slot: this lane's key's byte offset, lane i holding key i (mod KEYS);
-  // -1: none. Where each row of this thread's starts, or -1.
+  // -1: none, for which the cache's first row is read. Where each row of this
+  // thread's starts.
   __device__ __forceinline__ void find(int64_t slot, int tid) {
+    const int64_t from = slot >= 0 ? slot : 0;
 #pragma unroll
-    for (int j = 0; j < n; ++j) at[j] = from_lane(slot, tid / chunks % kWave + j * step);
+    for (int j = 0; j < n; ++j) at[j] = from_lane(from, tid / chunks % kWave + j * step);
   }
 
   // Row j: to LDS at lk and lv where the tiles will be, or to registers.
@@ -378,13 +380,15 @@ struct Stage {
       const int t = tid / chunks + j * step;
       const int ck = place_k<DP>(t, c) * 16, cv = place_v<DP>(t, c) * 16;
       const int base = wave_uniform(tid / kWave) * (kWave / chunks) + j * step;  // wave's first row
-      copy_to_lds(at[j] >= 0 && ck < head_bytes ? kb + ck + at[j] : (const uint8_t*)&kZeros,
-                  (const lds_u8*)lk + base * DP * 2);
-      copy_to_lds(at[j] >= 0 && cv < head_bytes ? vb + cv + at[j] : (const uint8_t*)&kZeros,
-                  (const lds_u8*)lv + base * DP * 2);
+      const uint8_t *pk = kb + ck + at[j], *pv = vb + cv + at[j];
+      if constexpr (!FULL) {  // nothing is read past a row
+        if (ck >= head_bytes) pk = (const uint8_t*)&kZeros;
+        if (cv >= head_bytes) pv = (const uint8_t*)&kZeros;
+      }
+      copy_to_lds(pk, (const lds_u8*)lk + base * DP * 2);
+      copy_to_lds(pv, (const lds_u8*)lv + base * DP * 2);
     } else {
-      // Nothing is read past a row; what does not exist is zeroed in store().
-      const int64_t off = at[j] >= 0 && c * 16 < head_bytes ? at[j] + c * 16 : 0;
+      const int64_t off = at[j] + (c * 16 < head_bytes ? c * 16 : 0);
       k[j] = *(const u32x4*)(kb + off);
       v[j] = *(const u32x4*)(vb + off);
     }
@@ -397,8 +401,10 @@ struct Stage {
     for (int j = 0; j < n; ++j) copy(j, kb, vb, tid, head_bytes, lk, lv);
   }
 
-  // Finishes the tiles. CHECK: infinities and NaN of V are zeroed in LDS;
-  // returns the lowest key (of this thread's) that holds one, else kNone.
+  // Finishes the tiles. CHECK: rows of V without a slot are zeroed in LDS, and
+  // infinities and NaN of the others; returns the lowest key (of this
+  // thread's) that holds one, else kNone. What K holds in rows without a slot
+  // does not matter: the scores are replaced.
   template <bool CHECK>
   __device__ __forceinline__ int store(uint8_t* lk, uint8_t* lv, uint64_t valid, int tid,
                                        int head_bytes) const {
@@ -411,7 +417,9 @@ struct Stage {
           const int t = tid / chunks + j * step;
           u32x4* at = (u32x4*)(lv + t * DP * 2 + c * 16);
           u32x4 x = *at;
-          if (drop_special<QT>(x)) {
+          if (!((valid >> t) & 1)) {
+            *at = u32x4{0, 0, 0, 0};
+          } else if (drop_special<QT>(x)) {
             *at = x;
             if (t < special) special = t;
           }
@@ -644,7 +652,7 @@ struct Lds {
   static constexpr int bytes = most > kWaves * box ? most : kWaves * box;
 };
 
-template <int DP, int QT, int CT>
+template <int DP, int QT, int CT, bool FULL>
 struct Body {
   const Attend& a;
   Shared& sh;
@@ -831,7 +839,7 @@ struct Body {
     const int tid = me.tid, wave = me.wave, lane = me.lane;
     constexpr int keys = Lds<DP>::keys;
     constexpr uint64_t all = keys == 64 ? ~0ull : (1ull << keys) - 1;
-    Stage<DP, QT, CT, keys, kBlock> st;
+    Stage<DP, QT, CT, FULL, keys, kBlock> st;
     Rows32<DP> r;
     bool bad = false;
     int t0 = u.lo + lo_tile * kTile;
@@ -910,7 +918,7 @@ struct Body {
   __device__ __forceinline__ void split_keys(int64_t number, bool whole) {
     const Who me = who();
     const int tid = me.tid, wave = me.wave, lane = me.lane;
-    Stage<DP, QT, CT, 32, kWave> st;
+    Stage<DP, QT, CT, FULL, 32, kWave> st;
     Rows32<DP> r;
     bool bad = false;
     int t0 = u.lo + lo_tile * kTile + wave * 32;
@@ -1083,7 +1091,7 @@ __device__ __forceinline__ void place_units(const Attend& a, Shared& sh, int bas
   __syncthreads();
 }
 
-template <int DP, int QT, int CT>
+template <int DP, int QT, int CT, bool FULL>
 __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Attend a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Lds<DP>::bytes];
   __shared__ Shared sh;
@@ -1120,23 +1128,28 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
       const int count = units - base < kBlock ? units - base : kBlock;
       if (write && tid < count) a.units[base + tid] = sh.unit[tid];
       if (begin >= at || end <= from || begin == end) continue;
-      // The unit that holds `begin`, or this round's first.
+      // From the last item backwards: workgroups that take the same keys for
+      // different rows then begin at the keys' start together, and stay in
+      // step for as long as they read the same item, so that each tile comes
+      // from memory to an XCD about once. The unit that holds the last point,
+      // or this round's last one.
       const int64_t stop = tid + 1 < count ? sh.unit[tid + 1].start : at;
-      if (tid == 0) sh.first = 0;
+      if (tid == 0) sh.first = count - 1;
       __syncthreads();
-      if (tid < count && sh.unit[tid].start <= begin && begin < stop) sh.first = tid;
+      if (tid < count && sh.unit[tid].start < end && end <= stop) sh.first = tid;
       __syncthreads();
-      for (int k = wave_uniform(sh.first); k < count; ++k) {
+      for (int k = wave_uniform(sh.first); k >= 0; --k) {
         const Unit v = uniform_unit(sh.unit[k]);
-        if (v.start >= end) break;
         const int64_t len = v.item_length();
         if (len == 0) continue;
         const int per = v.items(), n = per * a.c.n_heads, tiles = v.tiles();
-        const int64_t skip = begin > v.start ? begin - v.start : 0;
-        int i = ((skip | len) >> 32) == 0 ? (int)((uint32_t)skip / (uint32_t)len)
-                                          : (int)(skip / len);
-        for (; i < n && v.start + i * len < end; ++i) {
-          Body<DP, QT, CT> b{a, sh, lds};
+        if (v.start + n * len <= begin) break;
+        // The last item that starts before `end`.
+        const int64_t room = end - v.start < n * len ? end - v.start - 1 : n * len - 1;
+        int i = ((room | len) >> 32) == 0 ? (int)((uint32_t)room / (uint32_t)len)
+                                          : (int)(room / len);
+        for (; i >= 0 && v.start + (i + 1) * len > begin; --i) {
+          Body<DP, QT, CT, FULL> b{a, sh, lds};
           b.u = v;
           b.prefix = kind == 0;
           b.kvh = i / per;
@@ -1335,7 +1348,14 @@ Layout layout(const ep_kv_cache& c, int n_seqs, int n_groups, int n_tokens, int 
 
 template <int DP, int QT, int CT>
 hipError_t launch(const Attend& a, hipStream_t stream) {
-  hipLaunchKernelGGL((attend_kernel<DP, QT, CT>), dim3(a.workers), dim3(kBlock), 0, stream, a);
+  // FULL spares the copies of 16-bit rows a comparison per chunk.
+  constexpr bool direct = CT != EP_DTYPE_E4M3 && DP <= 128;
+  if (direct && a.c.head_dim == DP)
+    hipLaunchKernelGGL((attend_kernel<DP, QT, CT, direct>), dim3(a.workers), dim3(kBlock), 0,
+                       stream, a);
+  else
+    hipLaunchKernelGGL((attend_kernel<DP, QT, CT, false>), dim3(a.workers), dim3(kBlock), 0,
+                       stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int64_t rows = (int64_t)a.b.n_tokens * a.heads, blocks = (rows + kWaves - 1) / kWaves;
