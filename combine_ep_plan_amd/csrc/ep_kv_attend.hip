@@ -104,6 +104,16 @@ struct Attend {
 
 constexpr int kXcds = 8;
 
+// The arguments in the kernel's argument segment: read where they are used.
+// As values they would all be loaded at the start and spilled.
+typedef const Attend __attribute__((address_space(4))) Args;
+
+__device__ __forceinline__ Args& fresh(Args& a) {
+  Args* p = &a;
+  asm volatile("" : "+s"(p));
+  return *p;
+}
+
 
 struct Shared {
   Unit unit[kBlock];         // of a round
@@ -124,7 +134,8 @@ __device__ __forceinline__ int clamp_int(int64_t v, int64_t lo, int64_t hi) {
 
 // Keys that a row of the table holds; positions stay under 2^31 with room for
 // two steps.
-__device__ __forceinline__ int key_cap(const Attend& a) {
+template <typename A>
+__device__ __forceinline__ int key_cap(const A& a) {
   const int64_t cap = (int64_t)a.b.max_pages * a.c.page_tokens;
   return cap < kMostKeys ? (int)cap : kMostKeys;
 }
@@ -152,7 +163,7 @@ __device__ __forceinline__ Unit uniform_unit(const Unit& u) {
 
 // New tokens between two offsets; 0 where the offsets are not those of a
 // batch.
-__device__ __forceinline__ int fresh_of(const Attend& a, int lo, int hi) {
+__device__ __forceinline__ int fresh_of(Args& a, int lo, int hi) {
   return lo >= 0 && hi > lo && hi <= a.b.n_tokens ? hi - lo : 0;
 }
 
@@ -161,7 +172,7 @@ __device__ __forceinline__ int fresh_of(const Attend& a, int lo, int hi) {
 // sharing: each sequence then reads all its keys itself, which costs a part of
 // an item per sequence and spares the joining of two pieces per row (rows of
 // 12 prompts of 128 tokens behind an 8k prefix: XXX).
-__device__ __forceinline__ int shared_of(const Attend& a, int j, int s0, int s1) {
+__device__ __forceinline__ int shared_of(Args& a, int j, int s0, int s1) {
   const int shared = a.g.shared[j];
   if (s0 < 0 || s0 >= s1 || s1 > a.b.n_seqs) return shared;
   const int64_t rows =
@@ -170,7 +181,7 @@ __device__ __forceinline__ int shared_of(const Attend& a, int j, int s0, int s1)
 }
 
 // Reads the groups' ranges into LDS where they fit; a barrier must follow.
-__device__ __forceinline__ void load_groups(const Attend& a, Shared& sh) {
+__device__ __forceinline__ void load_groups(Args& a, Shared& sh) {
   const int j = threadIdx.x;
   if (a.g.n_groups > kGroupTable || j > a.g.n_groups || a.g.n_groups == 0) return;
   const int s0 = a.g.group_off[j];
@@ -179,7 +190,7 @@ __device__ __forceinline__ void load_groups(const Attend& a, Shared& sh) {
 }
 
 // The group of sequence s, or -1: the last one that starts at or before it.
-__device__ __forceinline__ int group_of(const Attend& a, const int32_t* off, int s) {
+__device__ __forceinline__ int group_of(Args& a, const int32_t* off, int s) {
   int lo = 0, hi = a.g.n_groups;
   while (hi - lo > 1) {
     const int mid = (lo + hi) / 2;
@@ -191,7 +202,7 @@ __device__ __forceinline__ int group_of(const Attend& a, const int32_t* off, int
 
 // Unit u but for its place; *late: the shared keys reach past the first new
 // token, so that rows of the group see different ones of them.
-__device__ __forceinline__ Unit unit_of(const Attend& a, const Shared& sh, int u, bool* late) {
+__device__ __forceinline__ Unit unit_of(Args& a, const Shared& sh, int u, bool* late) {
   const int s = u - a.g.n_groups;
   const bool kept = a.g.n_groups <= kGroupTable;
   Unit t;
@@ -238,7 +249,8 @@ struct Range {
   int64_t begin, end;
 };
 
-__device__ __forceinline__ Range range_of(const Attend& a, int kind, int w, int64_t p, int64_t s) {
+template <typename A>
+__device__ __forceinline__ Range range_of(const A& a, int kind, int w, int64_t p, int64_t s) {
   const int per = a.workers / kXcds, x = w / per, i = w % per;
   const int64_t p0 = p * x / kXcds, p1 = p * (x + 1) / kXcds;
   const int64_t s0 = s * x / kXcds, s1 = s * (x + 1) / kXcds;
@@ -654,7 +666,7 @@ struct Lds {
 
 template <int DP, int QT, int CT, bool FULL>
 struct Body {
-  const Attend& a;
+  Args& a;
   Shared& sh;
   uint8_t* lds;
   Unit u;
@@ -719,6 +731,7 @@ struct Body {
   }
 
   __device__ __forceinline__ void load_rows(Rows32<DP>& r, int row0) const {
+    Args& a = fresh(this->a);
     const Who me = who();
     const int half = me.half, row = row0 + me.lane % 32;
     r.clear();
@@ -756,6 +769,7 @@ struct Body {
   // that see such a key get them, after put() by the whole workgroup: a
   // positive weight changes neither. Keys [t0, end).
   __device__ __forceinline__ void add_special(int64_t number, bool whole, int t0, int end) const {
+    Args& a = fresh(this->a);
     __syncthreads();
     const int kind = prefix ? 0 : 1, rows = u.tile_rows();
     if (!whole && number >= a.pieces[kind]) return;
@@ -787,6 +801,7 @@ struct Body {
   // are written at a time.
   __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole,
                                       uint8_t* box) const {
+    Args& a = fresh(this->a);
     const Who me = who();
     const int lane = me.lane, half = me.half, col = lane % 32;
     const int kind = prefix ? 0 : 1;
@@ -1016,6 +1031,7 @@ struct Body {
 
   // Tiles [lo_tile, hi_tile) of an item.
   __device__ __forceinline__ void run(int64_t number, bool whole) {
+    Args& a = fresh(this->a);
     kb = (const uint8_t*)a.c.k + kvh * a.c.head_stride;
     vb = (const uint8_t*)a.c.v + kvh * a.c.head_stride;
     float f = a.scale * 1.44269504088896341f;
@@ -1031,7 +1047,7 @@ struct Body {
 
 // Units base .. base + kBlock - 1 into sh.unit, placed behind `at` in the
 // line and item[kind] of either kind, all of which move on by theirs.
-__device__ __forceinline__ void place_units(const Attend& a, Shared& sh, int base, int64_t& at,
+__device__ __forceinline__ void place_units(Args& a, Shared& sh, int base, int64_t& at,
                                             int32_t item[2]) {
   const int tid = threadIdx.x, lane = lane_id(), wave = tid / kWave, u = base + tid;
   const int count = a.g.n_groups + a.b.n_seqs;
@@ -1092,7 +1108,8 @@ __device__ __forceinline__ void place_units(const Attend& a, Shared& sh, int bas
 }
 
 template <int DP, int QT, int CT, bool FULL>
-__global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Attend a) {
+__global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Attend) {
+  Args& a = *(Args*)__builtin_amdgcn_kernarg_segment_ptr();
   __shared__ __attribute__((aligned(1024))) uint8_t lds[Lds<DP>::bytes];
   __shared__ Shared sh;
   const int tid = threadIdx.x;
@@ -1175,8 +1192,13 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
 }
 
 // ---------------------------------------------------------------------------
-// Joining the pieces: one wave per row and head.
+// Joining the pieces. 16 lanes take a row and head (the chain of loads from
+// the row to its pieces is most of the time, and a wave then has four on the
+// way), or SHARE times 16 lanes where there are few rows, with the pieces dealt
+// out among them.
 // ---------------------------------------------------------------------------
+constexpr int kJoin = 16;  // lanes
+
 struct Part {
   int64_t start;  // of the row's item, in the lines
   int item, row;  // number of the item, row of the piece
@@ -1203,103 +1225,189 @@ __device__ __forceinline__ Part part_of(const Attend& a, const Unit& u, int kind
   return p;
 }
 
-template <int DP, int QT>
+// seq_of_row() by the kJoin lanes that have the same i.
+__device__ __forceinline__ int seq_of_row16(const ep_kv_batch& b, int i) {
+  if (!b.q_off) return i < b.n_seqs ? i : -1;
+  const int lane = lane_id(), at = lane % kJoin;
+  int lo = 0, hi = b.n_seqs;  // the answer lies in [lo, hi)
+  while (hi - lo > 1) {
+    const int step = (hi - lo + kJoin - 1) / kJoin;
+    const int j = lo + at * step;
+    const uint64_t mask = ballot(j < hi && b.q_off[j < hi ? j : lo] <= i);
+    const uint32_t mine = (uint32_t)(mask >> (lane - at)) & ((1u << kJoin) - 1);
+    if (mine == 0) return -1;
+    lo += (31 - __builtin_clz(mine)) * step;
+    hi = hi < lo + step ? hi : lo + step;
+  }
+  return lo < b.n_seqs && b.q_off[lo] <= i && i < b.q_off[lo + 1] ? lo : -1;
+}
+
+template <int DP, int QT, int SHARE>
 __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
-  constexpr int per = DP / kWave;  // elements of a lane, consecutive
-  constexpr int kAhead = 4;        // pieces read at a time
-  const int lane = lane_id();
+  constexpr int kGroups = kBlock / kJoin;   // of a workgroup
+  constexpr int kQuads = DP / (4 * kJoin);  // elements 4 * (lane + kJoin q) .. + 3 of a lane
+  constexpr int kAhead = 4;                 // pieces read at a time
+  __shared__ float box[SHARE > 4 ? kWaves : 1][DP + 2];
+  const int at = threadIdx.x % kJoin, group = threadIdx.x / kJoin, part_no = group % SHARE;
   const int count = a.g.n_groups + a.b.n_seqs;
   const int64_t prefix = a.units[count].start, suffix = a.units[count + 1].start - prefix;
-  const int64_t stride = (int64_t)gridDim.x * kWaves;
-  for (int64_t i = (int64_t)blockIdx.x * kWaves + wave_uniform(threadIdx.x / kWave); i < rows;
+  const int64_t stride = (int64_t)gridDim.x * (kGroups / SHARE);
+  for (int64_t i = (int64_t)blockIdx.x * (kGroups / SHARE) + group / SHARE; i < rows;
        i += stride) {
-    const int token = (int)(i / a.heads), head = (int)(i % a.heads), kvh = head / a.share;
-    const int s = seq_of_row(a.b, token);
-    if (s < 0) continue;
-    const Unit su = a.units[a.g.n_groups + s];
-    const int64_t last = (int64_t)su.len - su.fresh + (token - su.row0);
-    if (token - su.row0 >= a.max_new || su.fresh == 0) {
-      if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
-      continue;
-    }
-    // Positions behind the table's end.
-    if (last >= key_cap(a) && lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+    const int token = (int)((uint32_t)i / (uint32_t)a.heads);  // rows < 2^31
+    const int head = (int)i - token * a.heads, kvh = head / a.share;
+    const int s = seq_of_row16(a.b, token);
+    bool done = s < 0;
+    Unit su;
     Part part[2];
-    Unit pu = su;
-    part[0].n = 0;
-    if (su.group >= 0) {
-      pu = a.units[su.group];
-      part[0] = part_of(a, pu, 0, token, head % a.share, kvh);
+    part[0].n = part[1].n = 0;
+    part[0].whole = part[1].whole = false;
+    Unit pu;
+    if (!done) {
+      su = a.units[a.g.n_groups + s];
+      pu = su;
+      const int64_t last = (int64_t)su.len - su.fresh + (token - su.row0);
+      const bool skip = token - su.row0 >= a.max_new || su.fresh == 0;
+      // Skipped rows, and positions behind the table's end.
+      if ((skip || last >= key_cap(a)) && at == 0 && part_no == 0)
+        atomicOr(a.status, EP_STATUS_BAD_PAGE);
+      done = skip;
     }
-    part[1] = part_of(a, su, 1, token, head % a.share, kvh);
-    if (part[1].whole) continue;
+    if (!done) {
+      if (su.group >= 0) {
+        pu = a.units[su.group];
+        part[0] = part_of(a, pu, 0, token, head % a.share, kvh);
+      }
+      part[1] = part_of(a, su, 1, token, head % a.share, kvh);
+      done = part[1].whole;
+    }
+    if (SHARE == 1 && done) continue;
+    if (SHARE > 1 && __all(done)) continue;  // all groups of a row agree
     const int most = part[0].n + part[1].n;
-    float m = -__builtin_inff(), l = 0.0f, o[per] = {};
-    for (int k0 = 0; k0 < most; k0 += kWave) {
-      const int k = k0 + lane;
+    float m = -__builtin_inff(), l = 0.0f;
+    f32x4 o[kQuads] = {};
+    for (int k0 = 0; k0 < most; k0 += kJoin * SHARE) {
+      const int k = k0 + at * SHARE + part_no;
       const bool pre = k < part[0].n;
       const Part& p = pre ? part[0] : part[1];
       const Unit& u = pre ? pu : su;
-      const int w = p.w0 + (pre ? k : k - part[0].n);
-      int64_t at = -1;
+      const int w = p.w0 + (pre ? k : k - part[0].n), kind = pre ? 0 : 1;
+      const float* x = nullptr;
       float2 st = make_float2(-__builtin_inff(), 0.0f);
-      const int kind = pre ? 0 : 1;
-      const Range r = range_of(a, kind, w, prefix, suffix);
-      if (k < most && tiles_before(u, p.start, r.begin) < tiles_before(u, p.start, r.end)) {
+      if (k < most) {
+        const Range r = range_of(a, kind, w, prefix, suffix);
         const int64_t number = (int64_t)w + p.item;
-        if (number < a.pieces[kind]) {
-          at = number * a.rows[kind] + p.row;
-          st = a.stat[kind][at];
-          if (st.x == -__builtin_inff()) at = -1;
+        if (tiles_before(u, p.start, r.begin) < tiles_before(u, p.start, r.end) &&
+            number < a.pieces[kind]) {
+          const int64_t row = number * a.rows[kind] + p.row;
+          st = a.stat[kind][row];
+          if (st.x != -__builtin_inff()) x = a.sum[kind] + row * DP;
         }
       }
       float top = st.x;
 #pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+      for (int d = 1; d < kJoin; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
       top = fmaxf(top, m);
       if (top == -__builtin_inff()) continue;
       const float scale = __builtin_amdgcn_exp2f(m - top);
-      const float wgt = at >= 0 ? __builtin_amdgcn_exp2f(st.x - top) : 0.0f;
+      const float wgt = x ? __builtin_amdgcn_exp2f(st.x - top) : 0.0f;
       float sum = wgt * st.y;
 #pragma unroll
-      for (int d = 1; d < kWave; d <<= 1) sum += __shfl_xor(sum, d);
+      for (int d = 1; d < kJoin; d <<= 1) sum += __shfl_xor(sum, d);
       l = l * scale + sum;
       m = top;
 #pragma unroll
-      for (int e = 0; e < per; ++e) o[e] *= scale;
-      const float* x = at < 0 ? nullptr : (pre ? a.sum[0] : a.sum[1]) + at * DP;
-      uint64_t mask = ballot(at >= 0);
+      for (int q = 0; q < kQuads; ++q) o[q] *= scale;
+      const int lane0 = lane_id() - at;
+      uint32_t mask = (uint32_t)(ballot(x != nullptr) >> lane0) & ((1u << kJoin) - 1);
       while (mask) {
-        float v[kAhead][per], f[kAhead];
+        f32x4 v[kAhead][kQuads];
+        float f[kAhead];
 #pragma unroll
         for (int j = 0; j < kAhead; ++j) {
-          f[j] = 0.0f;
-#pragma unroll
-          for (int e = 0; e < per; ++e) v[j][e] = 0.0f;
-          if (mask == 0) continue;
-          const int src = __builtin_ctzll(mask);
+          // Behind the last piece: the last one again, with no weight.
+          const int src = mask ? __builtin_ctz(mask) : -1;
           mask &= mask - 1;
-          f[j] = __shfl(wgt, src);
-          const float* y = (const float*)__shfl((uint64_t)x, src) + lane * per;
+          f[j] = src >= 0 ? __shfl(wgt, lane0 + (src >= 0 ? src : 0)) : 0.0f;
+          const float* y = (const float*)__shfl((uint64_t)x, lane0 + (src >= 0 ? src : 0));
 #pragma unroll
-          for (int e = 0; e < per; ++e) v[j][e] = y[e];
+          for (int q = 0; q < kQuads; ++q)
+            v[j][q] = src >= 0 ? *(const f32x4*)(y + 4 * (at + kJoin * q)) : f32x4{};
         }
 #pragma unroll
         for (int j = 0; j < kAhead; ++j)
 #pragma unroll
-          for (int e = 0; e < per; ++e) o[e] += f[j] * v[j][e];
+          for (int q = 0; q < kQuads; ++q) o[q] += v[j][q] * f[j];
       }
     }
+    if constexpr (SHARE > 1) {
+      // The groups of a wave, then the waves.
+      float top = m;
+#pragma unroll
+      for (int d = kJoin; d < kWave; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+      const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m - top);
+      m = top;
+      l *= f;
+#pragma unroll
+      for (int d = kJoin; d < kWave; d <<= 1) l += __shfl_xor(l, d);
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float y = o[q][e] * f;
+#pragma unroll
+          for (int d = kJoin; d < kWave; d <<= 1) y += __shfl_xor(y, d);
+          o[q][e] = y;
+        }
+    }
+    if constexpr (SHARE > 4) {
+      const int wave = threadIdx.x / kWave;
+      __syncthreads();  // the last row's reads
+      if (lane_id() < kJoin) {
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) box[wave][4 * (at + kJoin * q) + e] = o[q][e];
+        if (at == 0) {
+          box[wave][DP] = m;
+          box[wave][DP + 1] = l;
+        }
+      }
+      __syncthreads();
+      float top = box[0][DP];
+#pragma unroll
+      for (int w = 1; w < kWaves; ++w) top = fmaxf(top, box[w][DP]);
+      l = 0.0f;
+#pragma unroll
+      for (int q = 0; q < kQuads; ++q) o[q] = f32x4{};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float mw = box[w][DP];
+        const float f = mw == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(mw - top);
+        l += box[w][DP + 1] * f;
+#pragma unroll
+        for (int q = 0; q < kQuads; ++q)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) o[q][e] += box[w][4 * (at + kJoin * q) + e] * f;
+      }
+      m = top;
+    }
+    if (part_no != 0 || done) continue;
     uint8_t* to = (uint8_t*)a.out.p + (int64_t)token * a.out.token_stride +
                   (int64_t)head * a.out.head_stride;
     const float vs = a.c.dtype == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f;
     const float inv = l == 0.0f ? 0.0f : vs / l;
 #pragma unroll
-    for (int e = 0; e < per; ++e) {
-      const int d = lane * per + e;
-      if (d < a.c.head_dim) store1<QT>(to + 2 * d, o[e] * inv);
+    for (int q = 0; q < kQuads; ++q) {
+      const int d = 4 * (at + kJoin * q);
+      if (d >= a.c.head_dim) continue;
+      typename Fmt<QT>::elem w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = (typename Fmt<QT>::elem)(o[q][e] * inv);
+      *(u32x2*)(to + 2 * d) = u32x2{as<uint16_t>(w[0]) | (uint32_t)as<uint16_t>(w[1]) << 16,
+                                    as<uint16_t>(w[2]) | (uint32_t)as<uint16_t>(w[3]) << 16};
     }
-    if (a.lse && lane == 0)
+    if (a.lse && at == 0)
       a.lse[i] = l == 0.0f ? -__builtin_inff() : (m + log2f(l)) * 0.69314718055994531f;
   }
 }
@@ -1358,9 +1466,21 @@ hipError_t launch(const Attend& a, hipStream_t stream) {
                        stream, a);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t rows = (int64_t)a.b.n_tokens * a.heads, blocks = (rows + kWaves - 1) / kWaves;
-  const unsigned grid = (unsigned)(blocks < (1 << 20) ? blocks : 1 << 20);
-  hipLaunchKernelGGL((join_kernel<DP, QT>), dim3(grid), dim3(kBlock), 0, stream, a, rows);
+  // More lanes to a row where it has many pieces: where items are few, and
+  // each is cut for many workgroups (35 pieces per row, 160 rows: 7 against
+  // 13 us; 2 pieces, 1200 rows: 12 against 7 us).
+  const int64_t rows = (int64_t)a.b.n_tokens * a.heads;
+  const int64_t items = (int64_t)a.pieces[0] + a.pieces[1] - (a.pieces[0] > 0 ? 2 : 1) * a.workers;
+  const int share = a.workers >= 8 * items ? 16 : a.workers >= 3 * items ? 4 : 1;
+  const int per = kBlock / kJoin / share;
+  const int64_t blocks = (rows + per - 1) / per;
+  const dim3 grid((unsigned)(blocks < (1 << 20) ? blocks : 1 << 20));
+  if (share == 1)
+    hipLaunchKernelGGL((join_kernel<DP, QT, 1>), grid, dim3(kBlock), 0, stream, a, rows);
+  else if (share == 4)
+    hipLaunchKernelGGL((join_kernel<DP, QT, 4>), grid, dim3(kBlock), 0, stream, a, rows);
+  else
+    hipLaunchKernelGGL((join_kernel<DP, QT, 16>), grid, dim3(kBlock), 0, stream, a, rows);
   return hipGetLastError();
 }
 
