@@ -53,9 +53,9 @@ constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share o
 constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
 constexpr int kSoloRows = 256;   // rows a sequence from which on it shares nothing
 // Costs in the line: of a tile of either kind, and of starting on an item.
-constexpr int kCostSplit = 4;
+constexpr int kCostSplit = 3;
 constexpr int kCostBlock = 4;
-constexpr int kCostItem = 4;
+constexpr int kCostItem = 6;
 
 // A unit as the line of work has it.
 struct Unit {
@@ -795,56 +795,114 @@ struct Body {
     }
   }
 
-  // Rows to their place: the output where this piece is all there is, else
-  // the piece's sums. A lane holds pieces of 16 bytes of one row; they pass
-  // through the wave's `box` in LDS (32 rows of DP floats), so that whole rows
-  // are written at a time.
-  __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole,
-                                      uint8_t* box) const {
-    Args& a = fresh(this->a);
+  // Chunk q (of four floats) of row i of 32 in LDS: moved so that lanes that
+  // hold 32 rows and lanes that read whole ones both spread over the banks.
+  static constexpr int kChunks = DP / 4;
+  __device__ __forceinline__ static int chunk_at(int i, int q) {
+    return i * kChunks + (q ^ (i % kChunks));
+  }
+
+  // The wave's rows, times f, to LDS.
+  __device__ __forceinline__ static void lay_out(const Rows32<DP>& r, f32x4* to, float f) {
     const Who me = who();
-    const int lane = me.lane, half = me.half, col = lane % 32;
-    const int kind = prefix ? 0 : 1;
-    if (!whole && number >= a.pieces[kind]) {
-      if (lane == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
-      return;
-    }
-    constexpr int chunks = DP / 4;
-    float f = 1.0f;
-    if (whole) f = r.l == 0.0f ? 0.0f : (CT == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f) / r.l;
-    f32x4* lds_rows = (f32x4*)box;
 #pragma unroll
     for (int d = 0; d < DP / 32; ++d)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        lds_rows[col * chunks + ((8 * d + 2 * i + half) ^ (col % chunks))] =
+        to[chunk_at(me.lane % 32, 8 * d + 2 * i + me.half)] =
             f32x4{r.o[d][4 * i], r.o[d][4 * i + 1], r.o[d][4 * i + 2], r.o[d][4 * i + 3]} * f;
-    const int first = __builtin_amdgcn_readfirstlane(r.row);  // row of lane 0: always there
-    const float m = r.m == -__builtin_inff() ? r.m : r.m * c;
-    if (r.row >= 0 && half == 0) {
-      if (!whole)
-        a.stat[kind][number * a.rows[kind] + r.row % u.tile_rows()] = make_float2(m, r.l);
-      else if (a.lse)
-        a.lse[(int64_t)token_of(r.row) * a.heads + head_of(r.row)] =
-            r.l == 0.0f ? -__builtin_inff() : (m + log2f(r.l)) * 0.69314718055994531f;
-    }
-    const int e = lane % chunks * 4;
-#pragma unroll 4
-    for (int k = 0; k < 32 * chunks / kWave; ++k) {
-      const int in = k * (kWave / chunks) + lane / chunks, row = first + in;
-      const f32x4 x = lds_rows[in * chunks + ((lane % chunks) ^ (in % chunks))];
-      if (row >= u.rows) continue;
-      if (!whole) {
-        *(f32x4*)(a.sum[kind] + (number * a.rows[kind] + row % u.tile_rows()) * DP + e) = x;
-      } else if (e < a.c.head_dim) {
-        uint8_t* to = (uint8_t*)a.out.p + (int64_t)token_of(row) * a.out.token_stride +
-                      (int64_t)head_of(row) * a.out.head_stride + 2 * e;
-        typename Fmt<QT>::elem w[4];
+  }
+
+  // Four elements from e of a row of the unit, to the output or the piece.
+  __device__ __forceinline__ void put4(Args& a, int64_t number, bool whole, int row, int e,
+                                       const f32x4& x) const {
+    const int kind = prefix ? 0 : 1;
+    if (!whole) {
+      *(f32x4*)(a.sum[kind] + (number * a.rows[kind] + row % u.tile_rows()) * DP + e) = x;
+    } else if (e < a.c.head_dim) {
+      uint8_t* to = (uint8_t*)a.out.p + (int64_t)token_of(row) * a.out.token_stride +
+                    (int64_t)head_of(row) * a.out.head_stride + 2 * e;
+      typename Fmt<QT>::elem w[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) w[j] = (typename Fmt<QT>::elem)x[j];
-        *(u32x2*)to = u32x2{as<uint16_t>(w[0]) | (uint32_t)as<uint16_t>(w[1]) << 16,
-                            as<uint16_t>(w[2]) | (uint32_t)as<uint16_t>(w[3]) << 16};
+      for (int j = 0; j < 4; ++j) w[j] = (typename Fmt<QT>::elem)x[j];
+      *(u32x2*)to = u32x2{as<uint16_t>(w[0]) | (uint32_t)as<uint16_t>(w[1]) << 16,
+                          as<uint16_t>(w[2]) | (uint32_t)as<uint16_t>(w[3]) << 16};
+    }
+  }
+
+  // The statistics of a row; m of scores as the product gives them.
+  __device__ __forceinline__ void put_stat(Args& a, int64_t number, bool whole, int row, float m,
+                                           float l) const {
+    const int kind = prefix ? 0 : 1;
+    // Scores that are all NaN leave no maximum but a sum: the join has to
+    // see it.
+    const float n = m == -__builtin_inff() ? (l == 0.0f ? m : 0.0f) : m * c;
+    if (!whole)
+      a.stat[kind][number * a.rows[kind] + row % u.tile_rows()] = make_float2(n, l);
+    else if (a.lse)
+      a.lse[(int64_t)token_of(row) * a.heads + head_of(row)] =
+          l == 0.0f ? -__builtin_inff() : (n + log2f(l)) * 0.69314718055994531f;
+  }
+
+  // What the sums of a row are multiplied by where they are the output.
+  __device__ __forceinline__ float final_factor(Args& a, float l) const {
+    return l == 0.0f ? 0.0f : (CT == EP_DTYPE_E4M3 ? a.c.v_scale[kvh] : 1.0f) / l;
+  }
+
+  // Whether a piece of this number has a place (it has, but where the
+  // batch's offsets contradict each other).
+  __device__ __forceinline__ bool has_place(Args& a, int64_t number, bool whole) const {
+    if (whole || number < a.pieces[prefix ? 0 : 1]) return true;
+    if (threadIdx.x % kWave == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+    return false;
+  }
+
+  // A wave's rows to their place: the output where this piece is all there is,
+  // else the piece's sums. A lane holds parts of one row; they pass through
+  // `box` in LDS, so that whole rows are written at a time.
+  __device__ __forceinline__ void put(Rows32<DP>& r, int64_t number, bool whole,
+                                      uint8_t* box) const {
+    Args& a = fresh(this->a);
+    if (!has_place(a, number, whole)) return;
+    const Who me = who();
+    const int lane = me.lane;
+    lay_out(r, (f32x4*)box, whole ? final_factor(a, r.l) : 1.0f);
+    const int first = wave_uniform(r.row);  // row of lane 0: always there
+    if (r.row >= 0 && me.half == 0) put_stat(a, number, whole, r.row, r.m, r.l);
+#pragma unroll 4
+    for (int k = 0; k < 32 * kChunks / kWave; ++k) {
+      const int i = k * (kWave / kChunks) + lane / kChunks, q = lane % kChunks, row = first + i;
+      const f32x4 x = ((const f32x4*)box)[chunk_at(i, q)];
+      if (row < u.rows) put4(a, number, whole, row, 4 * q, x);
+    }
+  }
+
+  // The rows whose keys the waves shared out, from what each left in LDS: the
+  // common maximum, then the sums weighted to it.
+  __device__ __forceinline__ void put_split(int64_t number, bool whole) const {
+    Args& a = fresh(this->a);
+    if (!has_place(a, number, whole)) return;
+    const Who me = who();
+    const int row0 = index * kRowsSplit;
+    const int n = u.rows - row0 < kRowsSplit ? u.rows - row0 : kRowsSplit;
+    for (int j = me.tid; j < n * kChunks; j += kBlock) {
+      const int i = j / kChunks, q = j % kChunks;
+      float m[kWaves], top = -__builtin_inff(), l = 0.0f;
+      f32x4 x[kWaves], sum = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        m[w] = sh.stat[0][w][i];
+        x[w] = ((const f32x4*)(lds + w * Lds<DP>::box))[chunk_at(i, q)];
+        top = fmaxf(top, m[w]);
       }
+#pragma unroll
+      for (int w = 0; w < kWaves; ++w) {
+        const float f = m[w] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m[w] - top) * c);
+        l += sh.stat[1][w][i] * f;
+        sum += x[w] * f;
+      }
+      put4(a, number, whole, row0 + i, 4 * q, whole ? sum * final_factor(a, l) : sum);
+      if (q == 0) put_stat(a, number, whole, row0 + i, top, l);
     }
   }
 
@@ -866,7 +924,6 @@ struct Body {
     const int least = least_limit(r);
     // The block's least: keys from there on may be hidden from some row.
     if (lane == 0) sh.ipart[wave] = least;
-    if (tid == 0) sh.special = kNone;
     __syncthreads();
     int fewest = sh.ipart[0];
 #pragma unroll
@@ -926,6 +983,10 @@ struct Body {
     const int special = wave_uniform(sh.special);
     if (special < end) add_special(number, whole, special, end);
     __syncthreads();  // LDS is free for the next item
+    if (special != kNone) {
+      if (tid == 0) sh.special = kNone;
+      __syncthreads();
+    }
   }
 
   // Waves share out the keys: 32 of every 128 each, the same rows; their
@@ -950,8 +1011,6 @@ struct Body {
     load_rows(r, index * kRowsSplit);
     const Reads<DP> rd(lk, lv);
     const int least = least_limit(r);
-    if (tid == 0) sh.special = kNone;
-    __syncthreads();
     for (; t0 < end; t0 += kTile) {
       const uint64_t valid = ballot(slot >= 0) & 0xffffffffull;
       const bool edge = t0 + 32 > least || valid != 0xffffffffull;
@@ -980,53 +1039,24 @@ struct Body {
     }
     if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
     r.l = add_halves(r.l);
-    // Join: the common maximum, then the sums of waves 2, 3 to 0, 1 and of 1
-    // to 0 through LDS.
-    if (lane < 32) sh.stat[0][wave][lane] = r.m;
-    __syncthreads();  // also: no wave reads its tiles any more
-    const int col = lane % 32;
-    float top = sh.stat[0][0][col];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) top = fmaxf(top, sh.stat[0][w][col]);
-    const float w = r.m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((r.m - top) * c);
-    r.m = top;
-    r.l *= w;
-#pragma unroll
-    for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) r.o[d][i] *= w;
-    f32x4* box = (f32x4*)lds;
-#pragma unroll
-    for (int from = 2; from >= 1; from /= 2) {
-      if (wave >= from && wave < 2 * from) {
-        f32x4* to = box + (wave - from) * (DP / 8) * kWave + lane;
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i)
-            to[(4 * d + i) * kWave] = f32x4{r.o[d][4 * i], r.o[d][4 * i + 1], r.o[d][4 * i + 2],
-                                            r.o[d][4 * i + 3]};
-        if (lane < 32) sh.stat[1][wave][lane] = r.l;
-      }
-      __syncthreads();
-      if (wave < from) {
-        const f32x4* of = box + wave * (DP / 8) * kWave + lane;
-#pragma unroll
-        for (int d = 0; d < DP / 32; ++d)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const f32x4 x = of[(4 * d + i) * kWave];
-#pragma unroll
-            for (int j = 0; j < 4; ++j) r.o[d][4 * i + j] += x[j];
-          }
-        r.l += sh.stat[1][wave + from][col];
-      }
-      __syncthreads();
+    // Every wave leaves its sums where its tiles were, as put() does; then all
+    // threads join them, 16 bytes at a time.
+    f32x4* mine = (f32x4*)(lds + wave * Lds<DP>::box);
+    static_assert(Lds<DP>::box == Lds<DP>::wave, "a wave's sums take the place of its tiles");
+    lay_out(r, mine, 1.0f);
+    if (me.half == 0) {
+      sh.stat[0][wave][lane % 32] = r.m;
+      sh.stat[1][wave][lane % 32] = r.l;
     }
-    if (wave == 0) put(r, number, whole, lds);
+    __syncthreads();
+    put_split(number, whole);
     const int special = wave_uniform(sh.special);
     if (special < end) add_special(number, whole, special, end);
-    __syncthreads();  // everyone has read sh.special
+    __syncthreads();  // LDS is free for the next item
+    if (special != kNone) {
+      if (tid == 0) sh.special = kNone;
+      __syncthreads();
+    }
   }
 
   // Tiles [lo_tile, hi_tile) of an item.
@@ -1114,7 +1144,10 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
   __shared__ Shared sh;
   const int tid = threadIdx.x;
   const int units = a.g.n_groups + a.b.n_seqs;
-  if (tid == 0) sh.any_short = 0;
+  if (tid == 0) {
+    sh.any_short = 0;
+    sh.special = kNone;  // between items
+  }
   load_groups(a, sh);
   __syncthreads();
   // The line's length; a batch of up to kBlock units stays in LDS.

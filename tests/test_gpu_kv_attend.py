@@ -245,6 +245,29 @@ def test_masked_keys_may_hold_anything():
         assert torch.isnan(got[[3] + list(range(34, 44))]).all()
 
 
+def test_nan_queries_and_keys_reach_their_rows_and_no_others():
+    """A row whose query is NaN, or that sees a NaN key, is NaN, however many pieces its keys are cut
+    into; the others are as without it."""
+    for lens, new in (([3000, 40], [1, 1]), ([300, 700], [2, 40])):
+        c = Case(BF, BF, 4, 2, 64, 16, lens, new)
+        d = c.device()
+        c.call(d)
+        out, lse = d.out.cpu(), d.lse.cpu()
+        d.q[0, 1] = float("nan")
+        c.call(d)
+        bad = torch.zeros(out.shape[:2], dtype=torch.bool)
+        bad[0, 1] = True
+        assert torch.isnan(d.out.cpu()[bad]).all() and torch.isnan(d.lse.cpu()[bad]).all()
+        assert torch.equal(d.out.cpu()[~bad], out[~bad]) and torch.equal(d.lse.cpu()[~bad], lse[~bad])
+        e = c.device()
+        c.views(e.pool)[0][c.table[1][1], 5, 0] = float("nan")   # key 21 of sequence 1, KV head 0
+        c.call(e)
+        bad = torch.zeros(out.shape[:2], dtype=torch.bool)
+        bad[new[0]:, :2] = True
+        assert torch.isnan(e.out.cpu()[bad]).all() and torch.isnan(e.lse.cpu()[bad]).all()
+        assert torch.equal(e.out.cpu()[~bad], out[~bad]) and torch.equal(e.lse.cpu()[~bad], lse[~bad])
+
+
 def test_results_do_not_depend_on_the_run():
     c = Case(BF, BF, 8, 2, 128, 16, [530, 600, 513, 700], [1, 9, 1, 1], [0, 4], [512])
     d = c.device()
