@@ -132,7 +132,8 @@ def _load() -> ctypes.CDLL:
     # torch first: it loads its own HIP runtime, and the library's dependency
     # on libamdhip64.so.7 must resolve to that same, already-loaded copy
     # (two HIP runtimes in one process would not share devices or memory).
-    import torch  # noqa: F401
+    global _torch
+    import torch as _torch
 
     if not os.path.exists(LIB_PATH):
         raise ImportError(
@@ -237,8 +238,11 @@ def _planes(ts: Sequence) -> ctypes.Array:
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        # The handle alone: building a torch.cuda.Stream for it takes 3 us of a
+        # call's 10 to 17 on the host.
+        if not _torch.cuda.is_initialized():
+            _torch.cuda.init()
+        return _torch._C._cuda_getCurrentRawStream(_torch._C._cuda_getDevice())
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
@@ -451,9 +455,10 @@ def kv_push_staged_static(ranks: int, regions, n_regions: int, total_bytes: int,
 
 def _ints(t, shape, name: str):
     """Address of a contiguous int32 tensor of the given shape (None: any size)."""
-    if t.dim() != len(shape) or any(n is not None and n != m for n, m in zip(shape, t.shape)):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {shape}")
-    if str(t.dtype) != "torch.int32":
+    have = t.shape
+    if len(have) != len(shape) or any(n is not None and n != m for n, m in zip(shape, have)):
+        raise ValueError(f"{name} has shape {tuple(have)}, not {shape}")
+    if t.dtype != _torch.int32:
         raise ValueError(f"{name} must be int32, not {t.dtype}")
     return _addr(t)
 
@@ -508,33 +513,35 @@ def kv_copy_pages(g: KvPages, src, dst, ws, status, stream=None) -> None:
 
 
 def _dtype(t, name: str) -> int:
-    import torch
-    codes = {torch.bfloat16: EP_DTYPE_BF16, torch.float16: EP_DTYPE_F16,
-             torch.float8_e4m3fn: EP_DTYPE_E4M3}
+    codes = {_torch.bfloat16: EP_DTYPE_BF16, _torch.float16: EP_DTYPE_F16,
+             _torch.float8_e4m3fn: EP_DTYPE_E4M3}
     if t.dtype not in codes:
         raise ValueError(f"{name} has dtype {t.dtype}: bfloat16, float16 or float8_e4m3fn are taken")
     return codes[t.dtype]
 
 
-def _dense_rows(t, dims: int, name: str) -> None:
-    if t.dim() != dims or (t.shape[-1] > 1 and t.stride(-1) != 1):
-        raise ValueError(f"{name} of shape {tuple(t.shape)} and strides {t.stride()}: {dims} axes, "
-                         "the last one dense, are taken")
+def _row_strides(t, dims: int, name: str):
+    """Element strides of rows whose last axis is dense."""
+    st = t.stride()
+    if len(st) != dims or (st[-1] != 1 and t.shape[-1] > 1):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} and strides {st}: {dims} axes, the last "
+                         "one dense, are taken")
+    return st
 
 
 def make_kv_cache(k, v, k_scale=None, v_scale=None) -> KvCache:
     """One layer's cache from k and v [n_pages, page_tokens, n_heads, head_dim]: strided views of
     a pool, with equal strides. float8_e4m3fn ones take a float32 scale per head each."""
-    _dense_rows(k, 4, "k")
-    _dense_rows(v, 4, "v")
+    st = _row_strides(k, 4, "k")
+    _row_strides(v, 4, "v")
     if k.shape != v.shape or k.stride() != v.stride() or k.dtype != v.dtype:
         raise ValueError("k and v must have equal shapes, strides and dtypes")
     es = k.element_size()
     for s, name in ((k_scale, "k_scale"), (v_scale, "v_scale")):
-        if s is not None and (tuple(s.shape) != (k.shape[2],) or str(s.dtype) != "torch.float32"):
+        if s is not None and (tuple(s.shape) != (k.shape[2],) or s.dtype != _torch.float32):
             raise ValueError(f"{name} must be float32 [{k.shape[2]}]")
-    c = KvCache(k.data_ptr(), v.data_ptr(), _addr(k_scale), _addr(v_scale), k.stride(0) * es,
-                k.stride(1) * es, k.stride(2) * es, k.shape[0], k.shape[1], k.shape[2],
+    c = KvCache(k.data_ptr(), v.data_ptr(), _addr(k_scale), _addr(v_scale), st[0] * es,
+                st[1] * es, st[2] * es, k.shape[0], k.shape[1], k.shape[2],
                 k.shape[3], _dtype(k, "k"), 0)
     c.tensors = (k, v, k_scale, v_scale)
     return c
@@ -555,30 +562,26 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: int = EP_ROPE_NONE,
 
 def make_rope(inv_freq, rot_dim: int, layout: int = EP_ROPE_HALF, mscale: float = 1.0) -> Rope:
     """Rotary positions from a float32 tensor of rot_dim / 2 frequencies."""
-    if str(inv_freq.dtype) != "torch.float32" or inv_freq.numel() != int(rot_dim) // 2:
+    if inv_freq.dtype != _torch.float32 or inv_freq.numel() != int(rot_dim) // 2:
         raise ValueError(f"inv_freq must be float32 [{int(rot_dim) // 2}]")
     r = Rope(_addr(inv_freq), int(rot_dim), int(layout), float(mscale), 0)
     r.tensors = (inv_freq,)
     return r
 
 
-def _rows(t, name: str) -> Rows:
-    _dense_rows(t, 3, name)
-    es = t.element_size()
-    return Rows(t.data_ptr(), t.stride(0) * es, t.stride(1) * es)
+def _rows(t, name: str, dtype, shape) -> Rows:
+    """Rows of 16-bit elements of the given dtype and shape."""
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, not {dtype} {tuple(shape)}")
+    st = _row_strides(t, 3, name)
+    return Rows(t.data_ptr(), 2 * st[0], 2 * st[1])
 
 
-def _batch(cache: KvCache, tables, lens, q_off, rows, n_heads) -> KvBatch:
-    """The batch of `rows`, name: tensor, each [tokens, n_heads[name], head_dim] of one dtype."""
-    seqs = tables.shape[0]
-    first = next(iter(rows.values()))
-    for name, t in rows.items():
-        want = (first.shape[0], n_heads[name], cache.head_dim)
-        if tuple(t.shape) != want or t.dtype != first.dtype:
-            raise ValueError(f"{name} is {t.dtype} {tuple(t.shape)}, not {first.dtype} {want}")
-    return KvBatch(_ints(tables, (None, None), "tables"), _ints(lens, (seqs,), "lens"),
-                   None if q_off is None else _ints(q_off, (seqs + 1,), "q_off"), seqs,
-                   tables.shape[1], first.shape[0], _dtype(first, "rows"))
+def _batch(tables, lens, q_off, n_tokens: int, dtype: int) -> KvBatch:
+    seqs, max_pages = tables.shape
+    return KvBatch(_ints(tables, (seqs, max_pages), "tables"), _ints(lens, (seqs,), "lens"),
+                   None if q_off is None else _ints(q_off, (seqs + 1,), "q_off"), seqs, max_pages,
+                   n_tokens, dtype)
 
 
 def kv_append(cache: KvCache, tables, lens, q_off, q, k, v, q_out, rope, status,
@@ -586,18 +589,22 @@ def kv_append(cache: KvCache, tables, lens, q_off, q, k, v, q_out, rope, status,
     """Rotate the new tokens' q into q_out (which may be q) and write their rotated k, and v, to
     the pages. q and q_out None: only k and v. rope None: no rotation. q_off None: one new token
     per sequence."""
-    kv = cache.n_heads
-    rows, heads = {"k": k, "v": v}, {"k": kv, "v": kv}
+    shape, dtype = k.shape, k.dtype
+    if tuple(shape[1:]) != (cache.n_heads, cache.head_dim):
+        raise ValueError(f"k has shape {tuple(shape)}, not [tokens, {cache.n_heads}, "
+                         f"{cache.head_dim}]")
     if (q is None) != (q_out is None):
         raise ValueError("q and q_out must be given together")
+    b = _batch(tables, lens, q_off, shape[0], _dtype(k, "k"))
+    rq = ro = None
+    heads = 0
     if q is not None:
-        rows.update(q=q, q_out=q_out)
-        heads.update(q=q.shape[1], q_out=q.shape[1])
-    b = _batch(cache, tables, lens, q_off, rows, heads)
+        heads = q.shape[1]
+        wide = (shape[0], heads, shape[2])
+        rq, ro = _rows(q, "q", dtype, wide), _rows(q_out, "q_out", dtype, wide)
     _check(_lib.ep_kv_append(
-        ctypes.byref(cache), ctypes.byref(b), None if q is None else _rows(q, "q"),
-        0 if q is None else q.shape[1], _rows(k, "k"), _rows(v, "v"),
-        None if q is None else _rows(q_out, "q_out"), None if rope is None else ctypes.byref(rope),
+        ctypes.byref(cache), ctypes.byref(b), rq, heads, _rows(k, "k", dtype, shape),
+        _rows(v, "v", dtype, shape), ro, None if rope is None else ctypes.byref(rope),
         _addr(status), _stream(stream)), "ep_kv_append")
 
 
@@ -611,8 +618,10 @@ def kv_attend(cache: KvCache, tables, lens, q_off, max_new: int, group_off, shar
               sm_scale: float, ws, status, stream=None) -> None:
     """Attention of the new tokens' q over their pages into out, and lse (or None). group_off and
     shared (or both None): ranges of sequences that share their leading tokens."""
-    heads = q.shape[1]
-    b = _batch(cache, tables, lens, q_off, {"q": q, "out": out}, {"q": heads, "out": heads})
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3 or shape[2] != cache.head_dim:
+        raise ValueError(f"q has shape {tuple(shape)}, not [tokens, heads, {cache.head_dim}]")
+    b = _batch(tables, lens, q_off, shape[0], _dtype(q, "q"))
     if (group_off is None) != (shared is None):
         raise ValueError("group_off and shared must be given together")
     groups = None
@@ -620,12 +629,12 @@ def kv_attend(cache: KvCache, tables, lens, q_off, max_new: int, group_off, shar
         n = shared.numel()
         groups = KvGroups(_ints(group_off, (n + 1,), "group_off"), _ints(shared, (n,), "shared"),
                           n, 0)
-    if lse is not None and (tuple(lse.shape) != tuple(q.shape[:2]) or
-                            str(lse.dtype) != "torch.float32"):
-        raise ValueError(f"lse must be float32 {tuple(q.shape[:2])}")
+    if lse is not None and (lse.shape != shape[:2] or lse.dtype != _torch.float32):
+        raise ValueError(f"lse must be float32 {tuple(shape[:2])}")
     _check(_lib.ep_kv_attend(
         ctypes.byref(cache), ctypes.byref(b), None if groups is None else ctypes.byref(groups),
-        int(max_new), _rows(q, "q"), heads, _rows(out, "out"), _addr(lse), float(sm_scale),
+        int(max_new), _rows(q, "q", dtype, shape), shape[1], _rows(out, "out", dtype, shape),
+        _addr(lse), float(sm_scale),
         _addr(ws), _addr(status), _stream(stream)), "ep_kv_attend")
 
 

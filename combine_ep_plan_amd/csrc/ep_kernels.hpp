@@ -130,10 +130,11 @@ hipError_t launch_kv_push_staged(int ranks, const ep_kv_region* reg, int64_t m, 
                                  const void* src, int64_t src_rank_bytes, void* dst,
                                  int64_t dst_rank_bytes, void* bounce, int64_t round_bytes,
                                  int32_t* notify, int32_t* status, hipStream_t stream);
-// Pages of a KV cache. Workspace arrays (int32): pages [n_pages], src and dst
-// [n_pages / 2 + 1], first [n_seqs], start and len [m], counts [chunks + 1].
+// Pages of a KV cache. Workspace arrays (int32): pages and rank [n_pages], src
+// and dst [n_pages / 2 + 1], first [n_seqs], start and len [m], counts
+// [chunks + 1].
 struct PagesWs {
-  int32_t *pages, *src, *dst, *first, *start, *len, *counts;
+  int32_t *pages, *rank, *src, *dst, *first, *start, *len, *counts;
 };
 constexpr int kKvCompactChunk = 2048;  // pages per block of a compaction's passes
 int64_t kv_page_pieces(int64_t page_bytes);

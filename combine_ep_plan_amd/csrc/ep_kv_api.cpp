@@ -45,7 +45,7 @@ int check_pages(const ep_kv_pages* g, int64_t m) {
     return fail(EP_ERR_UNSUPPORTED, "page state: tables too large");
   // One grid row per rank and piece of a page.
   if (g->ranks > 65534 / ep::kv_page_pieces(g->page_bytes))
-    return fail(EP_ERR_UNSUPPORTED, "page state: ranks * (16 KB pieces per page) must be < 65535");
+    return fail(EP_ERR_UNSUPPORTED, "page state: ranks * (8 KB pieces per page) must be < 65535");
   if (m < 0) return fail(EP_ERR_INVALID_ARG, "number of requests must not be negative");
   if (m > EP_KV_MAX_REQUESTS)
     return fail(EP_ERR_UNSUPPORTED, "more than EP_KV_MAX_REQUESTS requests");
@@ -54,15 +54,15 @@ int check_pages(const ep_kv_pages* g, int64_t m) {
 
 size_t pages_layout(const ep_kv_pages& g, int64_t m, void* ws, ep::PagesWs* w) {
   const int64_t chunks = ((int64_t)g.n_pages + ep::kKvCompactChunk - 1) / ep::kKvCompactChunk;
-  const int64_t n[7] = {g.n_pages, g.n_pages / 2 + 1, g.n_pages / 2 + 1, g.n_seqs, m, m,
+  const int64_t n[8] = {g.n_pages, g.n_pages, g.n_pages / 2 + 1, g.n_pages / 2 + 1, g.n_seqs, m, m,
                         chunks + 1};
-  int32_t* p[7];
+  int32_t* p[8];
   size_t at = 0;
-  for (int i = 0; i < 7; ++i) {
+  for (int i = 0; i < 8; ++i) {
     p[i] = (int32_t*)((char*)ws + at);
     at += ((size_t)n[i] * 4 + 255) & ~(size_t)255;
   }
-  if (w) *w = ep::PagesWs{p[0], p[1], p[2], p[3], p[4], p[5], p[6]};
+  if (w) *w = ep::PagesWs{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
   return at;
 }
 

@@ -24,6 +24,9 @@ struct Append {
   ep_rows q, k, v, q_out;
   ep_rope rope;
   int heads, tokens;  // query heads; tokens per block
+  // Items of a row of q or k, and of v, and the powers of two they are laid
+  // out by: a thread finds its row and item by a shift.
+  int turned, turned_log, plain, plain_log;
   int32_t* status;
 };
 
@@ -39,16 +42,36 @@ __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
   y = b;
 }
 
+// x / scale, rounded once. With y = 1 / scale rounded once, q = x y and the
+// remainder r = x - scale q (exact), q + r y rounds correctly (Markstein, "Computation
+// of elementary functions on the IBM RISC System/6000 processor", 1990); an
+// infinite or NaN q stays. Scales whose reciprocals or remainders leave the
+// normal range are divided by.
+struct Divisor {
+  float scale, inv;
+  bool plain;
+
+  __device__ __forceinline__ explicit Divisor(float s) : scale(s), inv(1.0f / s) {
+    plain = !(fabsf(s) > 0x1p-60f && fabsf(s) < 0x1p60f);
+  }
+  __device__ __forceinline__ float operator()(float x) const {
+    const float q = x * inv;
+    const float c = __builtin_fmaf(__builtin_fmaf(-scale, q, x), inv, q);
+    return fabsf(q) < __builtin_inff() ? c : q;
+  }
+};
+
 // One row of a head: reads `from`, writes `to` (as type OUT, divided by
-// `scale` for an e4m3 cache). Item j of row_items().
+// the scale for an e4m3 cache). Item j of row_items().
 template <int IN, int OUT>
 __device__ __forceinline__ void row_item(const uint8_t* from, uint8_t* to, int j, int head_dim,
                                          const ep_rope& rope, const float2* cs, float scale) {
   constexpr int ib = Fmt<IN>::bytes, ob = Fmt<OUT>::bytes;
+  const Divisor by(scale);
   auto put8 = [&](int d, float* f) {
     if constexpr (OUT == EP_DTYPE_E4M3) {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = f[i] / scale;
+      for (int i = 0; i < 8; ++i) f[i] = by.plain ? f[i] / scale : by(f[i]);
     }
     store8<OUT>(to + (int64_t)d * ob, f);
   };
@@ -93,7 +116,7 @@ __device__ __forceinline__ void row_item(const uint8_t* from, uint8_t* to, int j
 
 // Items of a rotated row: chunks where the rotated part is whole chunks,
 // else pairs and single elements.
-__device__ __host__ __forceinline__ int row_items(const ep_rope& rope, int head_dim) {
+int row_items(const ep_rope& rope, int head_dim) {
   const bool split = rope.layout == EP_ROPE_HALF;
   const int rot = rope.rot_dim;
   if (rot % (split ? 16 : 8) == 0) return (split ? rot / 16 : rot / 8) + (head_dim - rot) / 8;
@@ -142,43 +165,44 @@ __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
     cs[t * kMaxPairs + pair] = make_float2(c * a.rope.mscale, s * a.rope.mscale);
   }
   __syncthreads();
-  const int turned = row_items(a.rope, a.c.head_dim), plain = a.c.head_dim / 8;
   const int heads = a.q.p ? a.heads : 0, kv = a.c.n_heads;
-  const int per = (heads + kv) * turned + kv * plain;
-  for (int i = threadIdx.x; i < a.tokens * per; i += kBlock) {
-    const int t = i / per;
-    int j = i - t * per;
+  const int qk = (heads + kv) << a.turned_log, per = qk + (kv << a.plain_log);
+  for (int t = 0; t < a.tokens; ++t) {
     const Token k = tok[t];
     if (k.row < 0) continue;
     const float2* sc = cs + t * kMaxPairs;
-    if (j < heads * turned) {
-      const int h = j / turned;
-      row_item<IN, IN>((const uint8_t*)a.q.p + k.row * a.q.token_stride + h * a.q.head_stride,
-                       (uint8_t*)a.q_out.p + k.row * a.q_out.token_stride + h * a.q_out.head_stride,
-                       j - h * turned, a.c.head_dim, a.rope, sc, 1.0f);
-      continue;
-    }
-    if (k.slot < 0) continue;
-    j -= heads * turned;
-    if (j < kv * turned) {
-      const int h = j / turned;
-      row_item<IN, OUT>((const uint8_t*)a.k.p + k.row * a.k.token_stride + h * a.k.head_stride,
-                        (uint8_t*)a.c.k + k.slot + h * a.c.head_stride, j - h * turned,
-                        a.c.head_dim, a.rope, sc, a.c.k_scale ? a.c.k_scale[h] : 1.0f);
-    } else {
-      j -= kv * turned;
-      const int h = j / plain, d = 8 * (j - h * plain);
-      float f[8];
-      load8<IN>((const uint8_t*)a.v.p + k.row * a.v.token_stride + h * a.v.head_stride +
-                    d * Fmt<IN>::bytes, f);
-      if constexpr (OUT == EP_DTYPE_E4M3) {
-        const float scale = a.c.v_scale[h];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) f[e] = f[e] / scale;
+    for (int i = threadIdx.x; i < per; i += kBlock) {
+      if (i < qk) {
+        const int h = i >> a.turned_log, j = i & ((1 << a.turned_log) - 1);
+        if (j >= a.turned) continue;
+        if (h < heads) {
+          row_item<IN, IN>((const uint8_t*)a.q.p + k.row * a.q.token_stride + h * a.q.head_stride,
+                           (uint8_t*)a.q_out.p + k.row * a.q_out.token_stride +
+                               h * a.q_out.head_stride,
+                           j, a.c.head_dim, a.rope, sc, 1.0f);
+        } else if (k.slot >= 0) {
+          const int g = h - heads;
+          row_item<IN, OUT>((const uint8_t*)a.k.p + k.row * a.k.token_stride + g * a.k.head_stride,
+                            (uint8_t*)a.c.k + k.slot + g * a.c.head_stride, j, a.c.head_dim,
+                            a.rope, sc, a.c.k_scale ? a.c.k_scale[g] : 1.0f);
+        }
+      } else if (k.slot >= 0) {
+        const int g = (i - qk) >> a.plain_log, j = (i - qk) & ((1 << a.plain_log) - 1);
+        if (j >= a.plain) continue;
+        ep_rope none = a.rope;
+        none.rot_dim = 0;
+        row_item<IN, OUT>((const uint8_t*)a.v.p + k.row * a.v.token_stride + g * a.v.head_stride,
+                          (uint8_t*)a.c.v + k.slot + g * a.c.head_stride, j, a.c.head_dim, none, sc,
+                          a.c.v_scale ? a.c.v_scale[g] : 1.0f);
       }
-      store8<OUT>((uint8_t*)a.c.v + k.slot + h * a.c.head_stride + d * Fmt<OUT>::bytes, f);
     }
   }
+}
+
+int log2_up(int n) {
+  int l = 0;
+  while (1 << l < n) ++l;
+  return l;
 }
 
 template <int IN, int OUT>
@@ -193,7 +217,9 @@ hipError_t launch(const Append& a, hipStream_t stream) {
 hipError_t launch_kv_append(const ep_kv_cache& c, const ep_kv_batch& b, const ep_rows& q,
                             int n_heads, const ep_rows& k, const ep_rows& v, const ep_rows& q_out,
                             const ep_rope& rope, int32_t* status, hipStream_t stream) {
-  Append a{c, b, q, k, v, q_out, rope, n_heads, b.n_tokens >= 2048 ? kMaxTokens : 1, status};
+  const int turned = row_items(rope, c.head_dim), plain = c.head_dim / 8;
+  const Append a{c,      b,     q, k, v, q_out, rope, n_heads, b.n_tokens >= 2048 ? kMaxTokens : 1,
+                 turned, log2_up(turned), plain, log2_up(plain), status};
   if (b.dtype == EP_DTYPE_BF16)
     return c.dtype == EP_DTYPE_E4M3 ? launch<EP_DTYPE_BF16, EP_DTYPE_E4M3>(a, stream)
                                     : launch<EP_DTYPE_BF16, EP_DTYPE_BF16>(a, stream);

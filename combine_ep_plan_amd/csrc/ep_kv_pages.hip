@@ -24,8 +24,11 @@ constexpr int kPlan = 1024;               // threads of the planning workgroup
 constexpr int kPlanWaves = kPlan / kWave;
 constexpr int kScan = 8;                  // refs per thread and pass
 constexpr int kBlock = 256;
-constexpr int kChunks = 4;                // 16-byte chunks per thread of a copy
-constexpr int64_t kPieceBytes = (int64_t)kBlock * kChunks * 16;
+// A copy's workgroup is one wave that has 8 KB on its way, page sizes being
+// mostly powers of two: 268 MB in 32 KB pages take 54 us, 5.0 TB/s, as with
+// pieces of 16 KB by four waves.
+constexpr int kChunks = 8;                // 16-byte chunks per lane
+constexpr int64_t kPieceBytes = (int64_t)kWave * kChunks * 16;
 constexpr int32_t kNone = 0x7fffffff;
 
 __device__ __forceinline__ void flag(int32_t* status, int32_t bits) {
@@ -71,20 +74,25 @@ __device__ __forceinline__ int64_t block_scan(int64_t v, int64_t* part, int64_t*
   return v + before;
 }
 
+__device__ __forceinline__ void load_refs(const int32_t* refs, int n_pages, int64_t base,
+                                          int32_t r[kScan]) {
+#pragma unroll
+  for (int j = 0; j < kScan; ++j) {
+    const int64_t p = base + j * kPlan + threadIdx.x;
+    r[j] = refs[p < n_pages ? p : n_pages - 1];
+  }
+}
+
 // The lowest free pages in ascending order into list[0, min(want, free));
-// returns how many were found. Whole workgroup.
+// returns how many were found. Whole workgroup. r: the counts of the first
+// pass, loaded ahead.
 __device__ __forceinline__ int64_t find_free(const int32_t* refs, int n_pages, int64_t want,
-                                             int32_t* list, int32_t* counts) {
+                                             int32_t r[kScan], int32_t* list, int32_t* counts) {
   const int lane = lane_id(), wave = threadIdx.x / kWave;
   int64_t found = 0;
   for (int64_t base = 0; base < n_pages && found < want; base += (int64_t)kPlan * kScan) {
     uint64_t mask[kScan];
-    int32_t r[kScan];
-#pragma unroll
-    for (int j = 0; j < kScan; ++j) {
-      const int64_t p = base + j * kPlan + threadIdx.x;
-      r[j] = refs[p < n_pages ? p : n_pages - 1];
-    }
+    if (base > 0) load_refs(refs, n_pages, base, r);
 #pragma unroll
     for (int j = 0; j < kScan; ++j) {
       const int64_t p = base + j * kPlan + threadIdx.x;
@@ -128,9 +136,16 @@ __device__ __forceinline__ int64_t find_free(const int32_t* refs, int n_pages, i
   return found < want ? found : want;
 }
 
+// What a call of few requests needs stays in LDS: the marks of up to kMarks
+// sequences, the starts of up to kPlan requests and kList pages. A trip
+// through memory and back is most of a microsecond, and the planning would
+// take four of them.
+constexpr int kMarks = 8192, kList = 4096;
+
 struct PagesShared {
   int64_t part[kPlanWaves];
   int32_t counts[kScan * kPlanWaves + 1];
+  int32_t first[kMarks], start[kPlan], list[kList];
 };
 
 // Pages that hold `n` tokens.
@@ -167,15 +182,21 @@ __device__ __forceinline__ int64_t need_of(const ep_kv_pages& g, int32_t seq, in
 template <bool ADD>
 __device__ __forceinline__ int64_t lay_out(const ep_kv_pages& g, const int32_t* seqs,
                                            const int32_t* args, int m, const PagesWs& ws,
-                                           PagesShared& sh, int32_t* status) {
+                                           PagesShared& sh, int32_t* start_of,
+                                           int32_t* status) {
+  const bool small = g.n_seqs <= kMarks;
   for (int i = threadIdx.x; i < m; i += kPlan) {
     const int32_t s = seqs[i];
-    if (s >= 0 && s < g.n_seqs) store_fresh(&ws.first[s], kNone);
+    if (s < 0 || s >= g.n_seqs) continue;
+    if (small) sh.first[s] = kNone;
+    else store_fresh(&ws.first[s], kNone);
   }
   settle();
   for (int i = threadIdx.x; i < m; i += kPlan) {
     const int32_t s = seqs[i];
-    if (s >= 0 && s < g.n_seqs) atomicMin(&ws.first[s], i);
+    if (s < 0 || s >= g.n_seqs) continue;
+    if (small) atomicMin(&sh.first[s], i);
+    else atomicMin(&ws.first[s], i);
   }
   settle();
   int64_t base = 0;
@@ -185,7 +206,8 @@ __device__ __forceinline__ int64_t lay_out(const ep_kv_pages& g, const int32_t* 
     int64_t need = -1;
     if (i < m) {
       need = need_of<ADD>(g, seqs[i], args[i]);
-      if (need >= 0 && load_fresh(&ws.first[seqs[i]]) != i) need = -1;
+      if (need >= 0 && (small ? sh.first[seqs[i]] : load_fresh(&ws.first[seqs[i]])) != i)
+        need = -1;
       bad |= need < 0;
     }
     const int64_t n = need > 0 ? need : 0;
@@ -193,7 +215,7 @@ __device__ __forceinline__ int64_t lay_out(const ep_kv_pages& g, const int32_t* 
     const int64_t incl = base + block_scan(n, sh.part, &sum);
     // Starts past the pool's size are never granted: they saturate.
     const int64_t start = incl - n;
-    if (i < m) ws.start[i] = need < 0 ? -1 : (int32_t)(start < kNone ? start : kNone);
+    if (i < m) start_of[i] = need < 0 ? -1 : (int32_t)(start < kNone ? start : kNone);
     base += sum;
   }
   if (bad) flag(status, EP_STATUS_BAD_PAGE);
@@ -204,11 +226,15 @@ __global__ __launch_bounds__(kPlan) void extend_kernel(ep_kv_pages g, const int3
                                                        const int32_t* add, int m, PagesWs ws,
                                                        int32_t* status) {
   __shared__ PagesShared sh;
-  const int64_t total = lay_out<true>(g, seqs, add, m, ws, sh, status);
-  const int64_t found = find_free(g.refs, g.n_pages, total, ws.pages, sh.counts);
+  int32_t r[kScan];
+  load_refs(g.refs, g.n_pages, 0, r);
+  int32_t* start_of = m <= kPlan ? sh.start : ws.start;
+  const int64_t total = lay_out<true>(g, seqs, add, m, ws, sh, start_of, status);
+  int32_t* list = total <= kList ? sh.list : ws.pages;
+  const int64_t found = find_free(g.refs, g.n_pages, total, r, list, sh.counts);
   settle();
   for (int i = threadIdx.x / kWave; i < m; i += kPlanWaves) {
-    const int64_t start = ws.start[i];
+    const int64_t start = start_of[i];
     if (start < 0) continue;
     const int32_t s = seqs[i], len = g.lens[s], n = add[i];
     const int64_t have = pages_of(len, g.page_tokens);
@@ -219,7 +245,7 @@ __global__ __launch_bounds__(kPlan) void extend_kernel(ep_kv_pages g, const int3
     }
     int32_t* row = g.tables + (int64_t)s * g.max_pages + have;
     for (int64_t k = lane_id(); k < need; k += kWave) {
-      const int32_t p = ws.pages[start + k];
+      const int32_t p = list[start + k];
       row[k] = p;
       g.refs[p] = 1;
     }
@@ -234,8 +260,11 @@ __global__ __launch_bounds__(kPlan) void fork_plan_kernel(ep_kv_pages g, const i
                                                           const int32_t* children, int m,
                                                           PagesWs ws, int32_t* status) {
   __shared__ PagesShared sh;
-  const int64_t total = lay_out<false>(g, children, parents, m, ws, sh, status);
-  const int64_t found = find_free(g.refs, g.n_pages, total, ws.pages, sh.counts);
+  int32_t r[kScan];
+  load_refs(g.refs, g.n_pages, 0, r);
+  const int64_t total = lay_out<false>(g, children, parents, m, ws, sh, ws.start, status);
+  int32_t* list = total <= kList ? sh.list : ws.pages;
+  const int64_t found = find_free(g.refs, g.n_pages, total, r, list, sh.counts);
   settle();
   for (int i = threadIdx.x; i < m; i += kPlan) {
     const int64_t start = ws.start[i];
@@ -244,33 +273,25 @@ __global__ __launch_bounds__(kPlan) void fork_plan_kernel(ep_kv_pages g, const i
     ws.len[i] = len;
     int32_t page = -2;
     if (len % g.page_tokens != 0) {
-      page = start < found ? ws.pages[start] : -1;
+      page = start < found ? list[start] : -1;
       if (page < 0) flag(status, EP_STATUS_CAPACITY);
     }
     ws.start[i] = page;
   }
 }
 
-// 16-byte chunks [c0, c0 + kBlock * kChunks) of a page, clamped to its end.
-__device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, int64_t c0,
-                                           int64_t n16) {
-  u32x4 v[kChunks];
-#pragma unroll
-  for (int j = 0; j < kChunks; ++j) {
-    const int64_t c = c0 + j * kBlock + threadIdx.x;
-    v[j] = load_stream((const u32x4*)src + (c < n16 ? c : n16 - 1));
-  }
-  asm volatile("" ::: "memory");
-#pragma unroll
-  for (int j = 0; j < kChunks; ++j) {
-    const int64_t c = c0 + j * kBlock + threadIdx.x;
-    if (c < n16) store_stream((u32x4*)dst + c, v[j]);
-  }
+// Piece q of a page, by one wave.
+__device__ __forceinline__ void copy_piece(const uint8_t* src, uint8_t* dst, int q, int64_t n16) {
+  RowRegs<kChunks> r;
+  const int64_t c0 = (int64_t)q * kWave * kChunks;
+  const int n = (int)(n16 - c0 < kWave * kChunks ? n16 - c0 : kWave * kChunks);
+  load_row16(r, (const u32x4*)src + c0, 0, n);
+  store_row16(r, (u32x4*)dst + c0, 0, n);
 }
 
 // Block (i, 0): the child's row, counts and length. Block (i, 1 + r * pieces
 // + q): piece q of the partly filled page, in rank r.
-__global__ __launch_bounds__(kBlock) void fork_apply_kernel(ep_kv_pages g, const int32_t* parents,
+__global__ __launch_bounds__(kWave) void fork_apply_kernel(ep_kv_pages g, const int32_t* parents,
                                                             const int32_t* children, PagesWs ws,
                                                             int pieces, int32_t* status) {
   const int i = blockIdx.x;
@@ -281,7 +302,7 @@ __global__ __launch_bounds__(kBlock) void fork_apply_kernel(ep_kv_pages g, const
   if (blockIdx.y == 0) {
     int32_t* to = g.tables + (int64_t)children[i] * g.max_pages;
     bool bad = false;
-    for (int k = threadIdx.x; k < g.max_pages; k += kBlock) {
+    for (int k = threadIdx.x; k < g.max_pages; k += kWave) {
       int32_t p = -1;
       if (k < full) {
         p = from[k];
@@ -305,8 +326,7 @@ __global__ __launch_bounds__(kBlock) void fork_apply_kernel(ep_kv_pages g, const
   }
   const int r = (blockIdx.y - 1) / pieces, q = (blockIdx.y - 1) % pieces;
   uint8_t* base = (uint8_t*)g.pool + r * g.rank_bytes;
-  copy_piece(base + src * g.page_bytes, base + page * g.page_bytes,
-             (int64_t)q * kBlock * kChunks, g.page_bytes / 16);
+  copy_piece(base + src * g.page_bytes, base + page * g.page_bytes, q, g.page_bytes / 16);
 }
 
 // One block per request. The first request of a sequence is the one that no
@@ -348,6 +368,9 @@ __global__ __launch_bounds__(kBlock) void free_kernel(ep_kv_pages g, const int32
 // ---------------------------------------------------------------------------
 constexpr int kCompact = kKvCompactChunk;
 constexpr int kPer = kCompact / kBlock;
+// Up to so many chunks every block counts all pages itself, which spares a
+// launch (4.5 us for 2048 pages).
+constexpr int kCompactAlone = 4;
 
 __device__ __forceinline__ int block_sum(int v, int* part) {
 #pragma unroll
@@ -382,17 +405,25 @@ __global__ __launch_bounds__(kBlock) void compact_rank_kernel(ep_kv_pages g, Pag
   __shared__ int part[kBlock / kWave];
   const int c = blockIdx.x;
   int before = 0, all = 0;
-  for (int j = threadIdx.x; j < chunks; j += kBlock) {
-    const int n = ws.counts[j];
-    all += n;
-    if (j < c) before += n;
+  if (chunks <= kCompactAlone) {
+    for (int64_t p = threadIdx.x; p < g.n_pages; p += kBlock) {
+      const int used = g.refs[p] > 0;
+      all += used;
+      if (p < (int64_t)c * kCompact) before += used;
+    }
+  } else {
+    for (int j = threadIdx.x; j < chunks; j += kBlock) {
+      const int n = ws.counts[j];
+      all += n;
+      if (j < c) before += n;
+    }
   }
   before = block_sum(before, part);
   const int live = block_sum(all, part);
   // used(L): the chunks before L's, and the part of its own chunk.
-  const int lc = live / kCompact;
+  const int lc = chunks <= kCompactAlone ? 0 : live / kCompact;
   int below = 0;
-  for (int j = threadIdx.x; j < chunks; j += kBlock) below += j < lc ? ws.counts[j] : 0;
+  for (int j = threadIdx.x; j < lc; j += kBlock) below += ws.counts[j];
   for (int64_t p = (int64_t)lc * kCompact + threadIdx.x; p < live; p += kBlock)
     below += g.refs[p] > 0;
   below = block_sum(below, part);
@@ -424,27 +455,28 @@ __global__ __launch_bounds__(kBlock) void compact_rank_kernel(ep_kv_pages g, Pag
     } else if (!used && p < live) {
       ws.dst[p - mine] = (int32_t)p;
     }
-    ws.pages[p] = rank;  // the mover's number; its new page follows
+    ws.rank[p] = rank;
+    ws.pages[p] = -1;  // a mover's new page follows with its copy
   }
 }
 
-// New page ids in place of the movers' numbers, tables and counts.
-__global__ __launch_bounds__(kBlock) void compact_apply_kernel(ep_kv_pages g, PagesWs ws,
-                                                               int chunks, int row_blocks,
-                                                               int pieces, int32_t* status) {
+// Tables (by the first row_blocks waves), pages and counts.
+__global__ __launch_bounds__(kWave) void compact_apply_kernel(ep_kv_pages g, PagesWs ws,
+                                                              int chunks, int row_blocks,
+                                                              int pieces, int32_t* status) {
   const int moves = ws.counts[chunks];
   if ((int)blockIdx.x < row_blocks) {
     bool bad = false;
     for (int s = blockIdx.x; s < g.n_seqs; s += row_blocks) {
       const int64_t n = used_pages(g.lens[s], g);
       int32_t* row = g.tables + (int64_t)s * g.max_pages;
-      for (int64_t k = threadIdx.x; k < n; k += kBlock) {
+      for (int64_t k = threadIdx.x; k < n; k += kWave) {
         const int32_t p = row[k];
         if (p < 0 || p >= g.n_pages) {
           bad = true;
           continue;
         }
-        const int32_t rank = ws.pages[p];
+        const int32_t rank = ws.rank[p];
         if (rank >= 0) row[k] = ws.dst[rank];
       }
     }
@@ -457,20 +489,13 @@ __global__ __launch_bounds__(kBlock) void compact_apply_kernel(ep_kv_pages g, Pa
     const int rest = (int)(u - j * g.ranks * pieces), r = rest / pieces, q = rest % pieces;
     const int32_t src = ws.src[j], dst = ws.dst[j];
     uint8_t* base = (uint8_t*)g.pool + r * g.rank_bytes;
-    copy_piece(base + src * g.page_bytes, base + dst * g.page_bytes,
-               (int64_t)q * kBlock * kChunks, g.page_bytes / 16);
+    copy_piece(base + src * g.page_bytes, base + dst * g.page_bytes, q, g.page_bytes / 16);
     if (rest == 0 && threadIdx.x == 0) {
       g.refs[dst] = g.refs[src];
       g.refs[src] = 0;
+      ws.pages[src] = dst;
     }
   }
-}
-
-__global__ __launch_bounds__(kBlock) void compact_map_kernel(ep_kv_pages g, PagesWs ws) {
-  const int64_t p = (int64_t)blockIdx.x * kBlock + threadIdx.x;
-  if (p >= g.n_pages) return;
-  const int32_t rank = ws.pages[p];
-  if (rank >= 0) ws.pages[p] = ws.dst[rank];
 }
 
 // ---------------------------------------------------------------------------
@@ -496,7 +521,7 @@ __global__ __launch_bounds__(kBlock) void copy_own_kernel(ep_kv_pages g, const i
   atomicMin(&ws.pages[dst[i]], i);
 }
 
-__global__ __launch_bounds__(kBlock) void copy_pages_kernel(ep_kv_pages g, const int32_t* src,
+__global__ __launch_bounds__(kWave) void copy_pages_kernel(ep_kv_pages g, const int32_t* src,
                                                             const int32_t* dst, PagesWs ws,
                                                             int pieces, int32_t* status) {
   const int i = blockIdx.x;
@@ -509,8 +534,7 @@ __global__ __launch_bounds__(kBlock) void copy_pages_kernel(ep_kv_pages g, const
   }
   const int r = blockIdx.y / pieces, q = blockIdx.y % pieces;
   uint8_t* base = (uint8_t*)g.pool + r * g.rank_bytes;
-  copy_piece(base + s * g.page_bytes, base + d * g.page_bytes, (int64_t)q * kBlock * kChunks,
-             g.page_bytes / 16);
+  copy_piece(base + s * g.page_bytes, base + d * g.page_bytes, q, g.page_bytes / 16);
 }
 
 }  // namespace
@@ -530,7 +554,7 @@ hipError_t launch_kv_fork(const ep_kv_pages& g, const int32_t* parents, const in
                      ws, status);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(fork_apply_kernel, dim3(m, 1 + g.ranks * pieces), dim3(kBlock), 0, stream, g,
+  hipLaunchKernelGGL(fork_apply_kernel, dim3(m, 1 + g.ranks * pieces), dim3(kWave), 0, stream, g,
                      parents, children, ws, pieces, status);
   return hipGetLastError();
 }
@@ -545,20 +569,23 @@ hipError_t launch_kv_compact(const ep_kv_pages& g, int32_t* n_live, const PagesW
                              int32_t* status, hipStream_t stream) {
   const int chunks = (g.n_pages + kCompact - 1) / kCompact;
   const int pieces = (int)kv_page_pieces(g.page_bytes);
-  hipLaunchKernelGGL(compact_count_kernel, dim3(chunks), dim3(kBlock), 0, stream, g, ws);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
+  hipError_t e = hipSuccess;
+  if (chunks > kCompactAlone) {
+    hipLaunchKernelGGL(compact_count_kernel, dim3(chunks), dim3(kBlock), 0, stream, g, ws);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   hipLaunchKernelGGL(compact_rank_kernel, dim3(chunks), dim3(kBlock), 0, stream, g, ws, chunks,
                      n_live);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
   const int row_blocks = g.n_seqs < 256 ? g.n_seqs : 256;
-  hipLaunchKernelGGL(compact_apply_kernel, dim3(row_blocks + 2048), dim3(kBlock), 0, stream, g, ws,
-                     chunks, row_blocks, pieces, status);
-  e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(compact_map_kernel, dim3((g.n_pages + kBlock - 1) / kBlock), dim3(kBlock), 0,
-                     stream, g, ws);
+  // How many pages move is known on the device only: enough waves to fill the
+  // chip several times over, and no more than the moves there can be.
+  const int64_t most = ((int64_t)g.n_pages + 1) / 2 * g.ranks * pieces;
+  const int waves = (int)(most < 16384 ? most : 16384);
+  hipLaunchKernelGGL(compact_apply_kernel, dim3(row_blocks + (waves > 0 ? waves : 1)), dim3(kWave),
+                     0, stream, g, ws, chunks, row_blocks, pieces, status);
   return hipGetLastError();
 }
 
@@ -572,7 +599,7 @@ hipError_t launch_kv_copy_pages(const ep_kv_pages& g, const int32_t* src, const 
   hipLaunchKernelGGL(copy_own_kernel, flat, dim3(kBlock), 0, stream, g, src, dst, m, ws);
   e = hipGetLastError();
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(copy_pages_kernel, dim3(m, g.ranks * pieces), dim3(kBlock), 0, stream, g, src,
+  hipLaunchKernelGGL(copy_pages_kernel, dim3(m, g.ranks * pieces), dim3(kWave), 0, stream, g, src,
                      dst, ws, pieces, status);
   return hipGetLastError();
 }
