@@ -15,7 +15,7 @@ namespace ep {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kMaxTokens = 4;  // tokens of a block
+constexpr int kAhead = 2;  // tokens whose loads are on their way together
 constexpr int kMaxPairs = 128;
 
 struct Append {
@@ -61,48 +61,83 @@ struct Divisor {
   }
 };
 
-// One row of a head: reads `from`, writes `to` (as type OUT, divided by
-// the scale for an e4m3 cache). Item j of row_items().
-template <int IN, int OUT>
-__device__ __forceinline__ void row_item(const uint8_t* from, uint8_t* to, int j, int head_dim,
-                                         const ep_rope& rope, const float2* cs, float scale) {
-  constexpr int ib = Fmt<IN>::bytes, ob = Fmt<OUT>::bytes;
-  const Divisor by(scale);
-  auto put8 = [&](int d, float* f) {
-    if constexpr (OUT == EP_DTYPE_E4M3) {
+// Items of a row of chunks: 16 bytes of it, or the two halves' 16 bytes that
+// turn together.
+struct Chunk {
+  u32x4 x, y;
+};
+
+__device__ __forceinline__ bool by_chunks(const ep_rope& rope) {
+  return rope.rot_dim % (rope.layout == EP_ROPE_HALF ? 16 : 8) == 0;
+}
+
+// Whether item j of a row turns, and where it starts.
+struct Place {
+  int d;
+  bool turns;
+};
+__device__ __forceinline__ Place place_of(const ep_rope& rope, int j) {
+  const int turned = rope.layout == EP_ROPE_HALF ? rope.rot_dim / 16 : rope.rot_dim / 8;
+  return j < turned ? Place{8 * j, true} : Place{rope.rot_dim + 8 * (j - turned), false};
+}
+
+template <int IN>
+__device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* from, int j,
+                                           const ep_rope& rope) {
+  const Place p = place_of(rope, j);
+  c.x = *(const u32x4*)(from + p.d * Fmt<IN>::bytes);
+  if (p.turns && rope.layout == EP_ROPE_HALF)
+    c.y = *(const u32x4*)(from + (p.d + rope.rot_dim / 2) * Fmt<IN>::bytes);
+}
+
+template <int IN>
+__device__ __forceinline__ void widen8(const u32x4& w, float* f) {
+  const auto v = as<typename Fmt<IN>::vec8>(w);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) f[i] = by.plain ? f[i] / scale : by(f[i]);
-    }
-    store8<OUT>(to + (int64_t)d * ob, f);
-  };
+  for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
+}
+
+template <int OUT>
+__device__ __forceinline__ void divide8(const Divisor& by, float* f) {
+  if constexpr (OUT == EP_DTYPE_E4M3) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = by.plain ? f[i] / by.scale : by(f[i]);
+  }
+}
+
+template <int IN, int OUT>
+__device__ __forceinline__ void put_chunk(const Chunk& c, uint8_t* to, int j, const ep_rope& rope,
+                                          const float2* cs, const Divisor& by) {
+  const Place p = place_of(rope, j);
+  float f[8], g[8];
+  widen8<IN>(c.x, f);
+  if (p.turns && rope.layout == EP_ROPE_HALF) {
+    widen8<IN>(c.y, g);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) turn(f[i], g[i], cs[8 * j + i].x, cs[8 * j + i].y);
+    divide8<OUT>(by, g);
+    store8<OUT>(to + (p.d + rope.rot_dim / 2) * Fmt<OUT>::bytes, g);
+  } else if (p.turns) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) turn(f[2 * i], f[2 * i + 1], cs[4 * j + i].x, cs[4 * j + i].y);
+  }
+  divide8<OUT>(by, f);
+  store8<OUT>(to + p.d * Fmt<OUT>::bytes, f);
+}
+
+// Item j of a row whose rotated part is no whole chunks: a pair, or a single
+// element.
+template <int IN, int OUT>
+__device__ __forceinline__ void small_item(const uint8_t* from, uint8_t* to, int j,
+                                           const ep_rope& rope, const float2* cs, float scale) {
+  constexpr int ib = Fmt<IN>::bytes, ob = Fmt<OUT>::bytes;
   auto put1 = [&](int d, float f) {
     if constexpr (OUT == EP_DTYPE_E4M3) f = f / scale;
     store1<OUT>(to + (int64_t)d * ob, f);
   };
   const int rot = rope.rot_dim, half = rot / 2;
-  const bool split = rope.layout == EP_ROPE_HALF;
-  if (rot % (split ? 16 : 8) == 0) {
-    const int turned = split ? rot / 16 : rot / 8;
-    float f[8];
-    if (j >= turned) {
-      const int d = rot + 8 * (j - turned);
-      load8<IN>(from + (int64_t)d * ib, f);
-      put8(d, f);
-    } else if (split) {
-      float g[8];
-      load8<IN>(from + (int64_t)8 * j * ib, f);
-      load8<IN>(from + (int64_t)(8 * j + half) * ib, g);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) turn(f[i], g[i], cs[8 * j + i].x, cs[8 * j + i].y);
-      put8(8 * j, f);
-      put8(8 * j + half, g);
-    } else {
-      load8<IN>(from + (int64_t)8 * j * ib, f);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) turn(f[2 * i], f[2 * i + 1], cs[4 * j + i].x, cs[4 * j + i].y);
-      put8(8 * j, f);
-    }
-  } else if (j < half) {
+  if (j < half) {
+    const bool split = rope.layout == EP_ROPE_HALF;
     const int d = split ? j : 2 * j, e = split ? j + half : 2 * j + 1;
     float x = load1<IN>(from + (int64_t)d * ib), y = load1<IN>(from + (int64_t)e * ib);
     turn(x, y, cs[j].x, cs[j].y);
@@ -123,23 +158,46 @@ int row_items(const ep_rope& rope, int head_dim) {
   return rot / 2 + head_dim - rot;
 }
 
-template <int IN, int OUT>
+template <int IN, int OUT, int TOKENS>
 __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
-  __shared__ float2 cs[kMaxTokens * kMaxPairs];
-  __shared__ Token tok[kMaxTokens];
-  __shared__ int64_t at[kMaxTokens];
-  const int wave = wave_uniform(threadIdx.x / kWave);
+  __shared__ float2 cs[TOKENS * kMaxPairs];
+  __shared__ Token tok[TOKENS];
+  __shared__ int64_t at[TOKENS];
   const int half = a.rope.rot_dim / 2, bt = a.c.page_tokens;
-  for (int t = wave; t < a.tokens; t += kBlock / kWave) {
-    const int64_t row = (int64_t)blockIdx.x * a.tokens + t;
+  // Token t of the block by lane t of the first wave: the first one's
+  // sequence is searched for, the others' lie among the next 64 offsets.
+  if (threadIdx.x < kWave) {
+    const int lane = threadIdx.x, row0 = wave_uniform(blockIdx.x) * TOKENS, row = row0 + lane;
+    const bool have = lane < TOKENS && row < a.b.n_tokens;
+    int s = have && row < a.b.n_seqs ? row : -1, first = row, end = row + 1;
+    if (a.b.q_off) {
+      const int s0 = seq_of_row(a.b, row0);
+      s = -1;
+      if (s0 >= 0) {
+        const int last = a.b.n_seqs - s0;  // offsets s0 .. s0 + last
+        const int next = a.b.q_off[s0 + (lane + 1 < last ? lane + 1 : last)];
+        int skip = 0;
+#pragma unroll
+        for (int t = 0; t < TOKENS; ++t) {
+          const uint64_t mask = ballot(next <= row0 + t);
+          if (lane == t) skip = mask + 1 == 0 ? kWave : __builtin_ctzll(~mask);
+        }
+        int lo = s0 + skip;
+        if (have && skip == kWave)  // more empty sequences than lanes: walk on
+          while (lo < a.b.n_seqs && a.b.q_off[lo + 1] <= row) ++lo;
+        if (have && lo < a.b.n_seqs) {
+          first = a.b.q_off[lo];
+          end = a.b.q_off[lo + 1];
+          if (first <= row && row < end) s = lo;
+        }
+      }
+    }
     Token k{-1, -1};
     int64_t pos = 0;
     bool bad = false;
-    const int s = row < a.b.n_tokens ? seq_of_row(a.b, (int)row) : -1;
     if (s >= 0) {
-      const int first = first_row(a.b, s), end = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
       pos = (int64_t)a.b.lens[s] - (end - first) + (row - first);
-      k.row = (int)row;
+      k.row = row;
       bad = true;
       if (pos >= 0 && pos / bt < a.b.max_pages) {
         const int32_t p = a.b.tables[(int64_t)s * a.b.max_pages + pos / bt];
@@ -149,14 +207,14 @@ __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
         }
       }
     }
-    if (lane_id() == 0) {
-      tok[t] = k;
-      at[t] = pos;
-      if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+    if (lane < TOKENS) {
+      tok[lane] = k;
+      at[lane] = pos;
     }
+    if (bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
   }
   __syncthreads();
-  for (int i = threadIdx.x; i < a.tokens * half; i += kBlock) {
+  for (int i = threadIdx.x; i < TOKENS * half; i += kBlock) {
     const int t = i / half, pair = i - t * half;
     const double turns = (double)at[t] * (double)a.rope.inv_freq[pair] * 0.15915494309189533577;
     const float f = (float)(turns - rint(turns));
@@ -167,33 +225,49 @@ __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
   __syncthreads();
   const int heads = a.q.p ? a.heads : 0, kv = a.c.n_heads;
   const int qk = (heads + kv) << a.turned_log, per = qk + (kv << a.plain_log);
-  for (int t = 0; t < a.tokens; ++t) {
-    const Token k = tok[t];
-    if (k.row < 0) continue;
-    const float2* sc = cs + t * kMaxPairs;
-    for (int i = threadIdx.x; i < per; i += kBlock) {
-      if (i < qk) {
-        const int h = i >> a.turned_log, j = i & ((1 << a.turned_log) - 1);
-        if (j >= a.turned) continue;
-        if (h < heads) {
-          row_item<IN, IN>((const uint8_t*)a.q.p + k.row * a.q.token_stride + h * a.q.head_stride,
-                           (uint8_t*)a.q_out.p + k.row * a.q_out.token_stride +
-                               h * a.q_out.head_stride,
-                           j, a.c.head_dim, a.rope, sc, 1.0f);
-        } else if (k.slot >= 0) {
-          const int g = h - heads;
-          row_item<IN, OUT>((const uint8_t*)a.k.p + k.row * a.k.token_stride + g * a.k.head_stride,
-                            (uint8_t*)a.c.k + k.slot + g * a.c.head_stride, j, a.c.head_dim,
-                            a.rope, sc, a.c.k_scale ? a.c.k_scale[g] : 1.0f);
+  for (int i = threadIdx.x; i < per; i += kBlock) {
+    // The item: of head h of q, k or v; the same one of every token.
+    const bool is_v = i >= qk;
+    const int log = is_v ? a.plain_log : a.turned_log, at_row = is_v ? i - qk : i;
+    const int h = at_row >> log, j = at_row & ((1 << log) - 1);
+    if (j >= (is_v ? a.plain : a.turned)) continue;
+    const bool is_q = !is_v && h < heads;
+    const int g = is_v || is_q ? h : h - heads;
+    const ep_rows& in = is_v ? a.v : is_q ? a.q : a.k;
+    const uint8_t* from = (const uint8_t*)in.p + g * in.head_stride;
+    uint8_t* to = is_q ? (uint8_t*)a.q_out.p + g * a.q_out.head_stride
+                       : (uint8_t*)(is_v ? a.c.v : a.c.k) + g * a.c.head_stride;
+    const float* scales = is_v ? a.c.v_scale : a.c.k_scale;
+    const float scale = OUT == EP_DTYPE_E4M3 && !is_q ? scales[g] : 1.0f;
+    ep_rope rope = a.rope;
+    if (is_v) rope.rot_dim = 0;
+    const Divisor by(scale);
+    if (by_chunks(rope)) {
+      constexpr int n = TOKENS < kAhead ? TOKENS : kAhead;
+#pragma unroll 1
+      for (int t0 = 0; t0 < TOKENS; t0 += n) {
+        Chunk c[n];
+#pragma unroll
+        for (int t = 0; t < n; ++t)
+          if (tok[t0 + t].row >= 0)
+            load_chunk<IN>(c[t], from + tok[t0 + t].row * in.token_stride, j, rope);
+#pragma unroll
+        for (int t = 0; t < n; ++t) {
+          const Token k = tok[t0 + t];
+          if (k.row < 0 || (!is_q && k.slot < 0)) continue;
+          const float2* sc = cs + (t0 + t) * kMaxPairs;
+          if (is_q) put_chunk<IN, IN>(c[t], to + k.row * a.q_out.token_stride, j, rope, sc, by);
+          else put_chunk<IN, OUT>(c[t], to + k.slot, j, rope, sc, by);
         }
-      } else if (k.slot >= 0) {
-        const int g = (i - qk) >> a.plain_log, j = (i - qk) & ((1 << a.plain_log) - 1);
-        if (j >= a.plain) continue;
-        ep_rope none = a.rope;
-        none.rot_dim = 0;
-        row_item<IN, OUT>((const uint8_t*)a.v.p + k.row * a.v.token_stride + g * a.v.head_stride,
-                          (uint8_t*)a.c.v + k.slot + g * a.c.head_stride, j, a.c.head_dim, none, sc,
-                          a.c.v_scale ? a.c.v_scale[g] : 1.0f);
+      }
+    } else {
+      for (int t = 0; t < TOKENS; ++t) {
+        const Token k = tok[t];
+        if (k.row < 0 || (!is_q && k.slot < 0)) continue;
+        const float2* sc = cs + t * kMaxPairs;
+        const uint8_t* x = from + k.row * in.token_stride;
+        if (is_q) small_item<IN, IN>(x, to + k.row * a.q_out.token_stride, j, rope, sc, 1.0f);
+        else small_item<IN, OUT>(x, to + k.slot, j, rope, sc, scale);
       }
     }
   }
@@ -207,8 +281,13 @@ int log2_up(int n) {
 
 template <int IN, int OUT>
 hipError_t launch(const Append& a, hipStream_t stream) {
-  const unsigned grid = (unsigned)(((int64_t)a.b.n_tokens + a.tokens - 1) / a.tokens);
-  hipLaunchKernelGGL((append_kernel<IN, OUT>), dim3(grid), dim3(kBlock), 0, stream, a);
+  const dim3 grid((unsigned)(((int64_t)a.b.n_tokens + a.tokens - 1) / a.tokens));
+  if (a.tokens == 1)
+    hipLaunchKernelGGL((append_kernel<IN, OUT, 1>), grid, dim3(kBlock), 0, stream, a);
+  else if (a.tokens == 4)
+    hipLaunchKernelGGL((append_kernel<IN, OUT, 4>), grid, dim3(kBlock), 0, stream, a);
+  else
+    hipLaunchKernelGGL((append_kernel<IN, OUT, 16>), grid, dim3(kBlock), 0, stream, a);
   return hipGetLastError();
 }
 
@@ -218,7 +297,9 @@ hipError_t launch_kv_append(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                             int n_heads, const ep_rows& k, const ep_rows& v, const ep_rows& q_out,
                             const ep_rope& rope, int32_t* status, hipStream_t stream) {
   const int turned = row_items(rope, c.head_dim), plain = c.head_dim / 8;
-  const Append a{c,      b,     q, k, v, q_out, rope, n_heads, b.n_tokens >= 2048 ? kMaxTokens : 1,
+  // Tokens of a block: as many as leave four blocks or so to a CU.
+  const int tokens = b.n_tokens >= 8192 ? 16 : b.n_tokens >= 2048 ? 4 : 1;
+  const Append a{c,      b,     q, k, v, q_out, rope, n_heads, tokens,
                  turned, log2_up(turned), plain, log2_up(plain), status};
   if (b.dtype == EP_DTYPE_BF16)
     return c.dtype == EP_DTYPE_E4M3 ? launch<EP_DTYPE_BF16, EP_DTYPE_E4M3>(a, stream)

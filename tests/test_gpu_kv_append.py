@@ -127,6 +127,11 @@ CASES = [
 ]
 
 
+# Many sequences to a block of tokens, more empty ones in a row than a wave has lanes, long ones.
+MANY = [1] * 100 + [0] * 90 + [2900] + [0] * 70 + [5, 0, 2600, 2700, 0]
+CASES.append((BF, BF, 1, 1, 16, 16, 1, 1.0, MANY, MANY, 16))
+
+
 @pytest.mark.parametrize("case", CASES, ids=[str(i) for i in range(len(CASES))])
 def test_append_matches_64_bits(case):
     note(f"kv append {case}")
