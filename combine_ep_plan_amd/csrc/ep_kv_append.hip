@@ -15,7 +15,7 @@ namespace ep {
 namespace {
 
 constexpr int kBlock = 256;
-constexpr int kAhead = 2;  // tokens whose loads are on their way together
+constexpr int kAhead = 4;  // tokens whose loads are on their way together
 constexpr int kMaxPairs = 128;
 
 struct Append {
@@ -30,10 +30,11 @@ struct Append {
   int32_t* status;
 };
 
-// Where one token's K and V go: byte offset of its slot, or -1.
+// Where one token's rows are, in bytes.
 struct Token {
-  int64_t slot;
-  int row;  // -1: no sequence has it
+  int64_t slot;     // of the cache; -1: none
+  int64_t from[3];  // q, k, v
+  int64_t to;       // q_out; -1: no sequence has the token
 };
 
 __device__ __forceinline__ void turn(float& x, float& y, float c, float s) {
@@ -85,9 +86,9 @@ template <int IN>
 __device__ __forceinline__ void load_chunk(Chunk& c, const uint8_t* from, int j,
                                            const ep_rope& rope) {
   const Place p = place_of(rope, j);
-  c.x = *(const u32x4*)(from + p.d * Fmt<IN>::bytes);
+  c.x = load_stream((const u32x4*)(from + p.d * Fmt<IN>::bytes));
   if (p.turns && rope.layout == EP_ROPE_HALF)
-    c.y = *(const u32x4*)(from + (p.d + rope.rot_dim / 2) * Fmt<IN>::bytes);
+    c.y = load_stream((const u32x4*)(from + (p.d + rope.rot_dim / 2) * Fmt<IN>::bytes));
 }
 
 template <int IN>
@@ -109,6 +110,10 @@ template <int IN, int OUT>
 __device__ __forceinline__ void put_chunk(const Chunk& c, uint8_t* to, int j, const ep_rope& rope,
                                           const float2* cs, const Divisor& by) {
   const Place p = place_of(rope, j);
+  if (IN == OUT && !p.turns) {
+    *(u32x4*)(to + p.d * Fmt<OUT>::bytes) = c.x;
+    return;
+  }
   float f[8], g[8];
   widen8<IN>(c.x, f);
   if (p.turns && rope.layout == EP_ROPE_HALF) {
@@ -192,12 +197,15 @@ __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
         }
       }
     }
-    Token k{-1, -1};
+    Token k{-1, {0, 0, 0}, -1};
     int64_t pos = 0;
     bool bad = false;
     if (s >= 0) {
       pos = (int64_t)a.b.lens[s] - (end - first) + (row - first);
-      k.row = row;
+      k.from[0] = row * a.q.token_stride;
+      k.from[1] = row * a.k.token_stride;
+      k.from[2] = row * a.v.token_stride;
+      k.to = row * a.q_out.token_stride;
       bad = true;
       if (pos >= 0 && pos / bt < a.b.max_pages) {
         const int32_t p = a.b.tables[(int64_t)s * a.b.max_pages + pos / bt];
@@ -233,8 +241,10 @@ __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
     if (j >= (is_v ? a.plain : a.turned)) continue;
     const bool is_q = !is_v && h < heads;
     const int g = is_v || is_q ? h : h - heads;
-    const ep_rows& in = is_v ? a.v : is_q ? a.q : a.k;
-    const uint8_t* from = (const uint8_t*)in.p + g * in.head_stride;
+    const int side = is_v ? 2 : is_q ? 0 : 1;
+    const uint8_t* from = is_v   ? (const uint8_t*)a.v.p + g * a.v.head_stride
+                          : is_q ? (const uint8_t*)a.q.p + g * a.q.head_stride
+                                 : (const uint8_t*)a.k.p + g * a.k.head_stride;
     uint8_t* to = is_q ? (uint8_t*)a.q_out.p + g * a.q_out.head_stride
                        : (uint8_t*)(is_v ? a.c.v : a.c.k) + g * a.c.head_stride;
     const float* scales = is_v ? a.c.v_scale : a.c.k_scale;
@@ -248,26 +258,25 @@ __global__ __launch_bounds__(kBlock) void append_kernel(Append a) {
       for (int t0 = 0; t0 < TOKENS; t0 += n) {
         Chunk c[n];
 #pragma unroll
-        for (int t = 0; t < n; ++t)
-          if (tok[t0 + t].row >= 0)
-            load_chunk<IN>(c[t], from + tok[t0 + t].row * in.token_stride, j, rope);
+        for (int t = 0; t < n; ++t)  // a token that no sequence has reads row 0
+          load_chunk<IN>(c[t], from + tok[t0 + t].from[side], j, rope);
 #pragma unroll
         for (int t = 0; t < n; ++t) {
-          const Token k = tok[t0 + t];
-          if (k.row < 0 || (!is_q && k.slot < 0)) continue;
+          const int64_t at_to = is_q ? tok[t0 + t].to : tok[t0 + t].slot;
+          if (at_to < 0) continue;
           const float2* sc = cs + (t0 + t) * kMaxPairs;
-          if (is_q) put_chunk<IN, IN>(c[t], to + k.row * a.q_out.token_stride, j, rope, sc, by);
-          else put_chunk<IN, OUT>(c[t], to + k.slot, j, rope, sc, by);
+          if (is_q) put_chunk<IN, IN>(c[t], to + at_to, j, rope, sc, by);
+          else put_chunk<IN, OUT>(c[t], to + at_to, j, rope, sc, by);
         }
       }
     } else {
       for (int t = 0; t < TOKENS; ++t) {
-        const Token k = tok[t];
-        if (k.row < 0 || (!is_q && k.slot < 0)) continue;
+        const int64_t at_to = is_q ? tok[t].to : tok[t].slot;
+        if (at_to < 0) continue;
         const float2* sc = cs + t * kMaxPairs;
-        const uint8_t* x = from + k.row * in.token_stride;
-        if (is_q) small_item<IN, IN>(x, to + k.row * a.q_out.token_stride, j, rope, sc, 1.0f);
-        else small_item<IN, OUT>(x, to + k.slot, j, rope, sc, scale);
+        const uint8_t* x = from + tok[t].from[side];
+        if (is_q) small_item<IN, IN>(x, to + at_to, j, rope, sc, 1.0f);
+        else small_item<IN, OUT>(x, to + at_to, j, rope, sc, scale);
       }
     }
   }

@@ -61,7 +61,7 @@ __device__ __forceinline__ void load8(const uint8_t* p, float* f) {
 
 // The nearest e4m3 code of f, saturating at 448; a NaN stays one.
 __device__ __forceinline__ float e4m3_range(float f) {
-  return f != f ? f : fminf(fmaxf(f, -448.0f), 448.0f);
+  return f != f ? f : __builtin_amdgcn_fmed3f(f, -448.0f, 448.0f);
 }
 
 template <int DT>
