@@ -397,6 +397,8 @@ int ep_kv_attend(const ep_kv_cache* c, const ep_kv_batch* b, const ep_kv_groups*
   EP_CHECK(check_rows(q, n_heads, *b, c->head_dim, "q", dev));
   EP_CHECK(check_rows(out, n_heads, *b, c->head_dim, "out", dev));
   EP_CHECK(check_apart(*out, n_heads, *b, c->head_dim, "out"));
+  // Rows of q are read again after others were written.
+  if (out->p == q->p) return fail(EP_ERR_INVALID_ARG, "out may not be q");
   if (lse) EP_CHECK(check_ptr(lse, dev, "lse", (int64_t)b->n_tokens * n_heads * 4));
   EP_CHECK(check_ptr(ws, dev, "ws",
                      (int64_t)ep::kv_attend_bytes(*c, b->n_seqs, g.n_groups, b->n_tokens, n_heads,

@@ -51,11 +51,12 @@ constexpr int kMostKeys = 0x7fffffff - 1024;
 constexpr int kRowsSplit = 32;   // rows of an item whose keys the waves share out
 constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
 constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
-constexpr int kSoloRows = 256;   // rows a sequence from which on it shares nothing
-// Costs in the line: of a tile of either kind, and of starting on an item.
-constexpr int kCostSplit = 3;
+// Costs in the line: of a tile of either kind, and of starting on an item. The
+// times hardly follow them (338 MB of keys: 131 to 140 us for all that were
+// tried); an item's start is worth two tiles, which short batches show.
+constexpr int kCostSplit = 4;
 constexpr int kCostBlock = 4;
-constexpr int kCostItem = 6;
+constexpr int kCostItem = 8;
 
 // A unit as the line of work has it.
 struct Unit {
@@ -114,7 +115,6 @@ __device__ __forceinline__ Args& fresh(Args& a) {
   return *p;
 }
 
-
 struct Shared {
   Unit unit[kBlock];         // of a round
   int64_t part[kWaves];
@@ -139,6 +139,10 @@ __device__ __forceinline__ int key_cap(const A& a) {
   const int64_t cap = (int64_t)a.b.max_pages * a.c.page_tokens;
   return cap < kMostKeys ? (int)cap : kMostKeys;
 }
+
+// Whether number n has a place among `places`. Offsets that contradict each
+// other name more items than a batch can have, and may wrap their numbers.
+__device__ __forceinline__ bool fits(int64_t n, int places) { return n >= 0 && n < places; }
 
 // A 64-bit value that is equal on all lanes, in scalar registers.
 __device__ __forceinline__ int64_t wave_uniform64(int64_t v) {
@@ -167,26 +171,12 @@ __device__ __forceinline__ int fresh_of(Args& a, int lo, int hi) {
   return lo >= 0 && hi > lo && hi <= a.b.n_tokens ? hi - lo : 0;
 }
 
-// Shared tokens of the group of sequences s0 .. s1 - 1. A group whose
-// sequences bring kSoloRows rows or more on average fills its items without
-// sharing: each sequence then reads all its keys itself, which costs a part of
-// an item per sequence and spares the joining of two pieces per row (rows of
-// 12 prompts of 128 tokens behind an 8k prefix: XXX).
-__device__ __forceinline__ int shared_of(Args& a, int j, int s0, int s1) {
-  const int shared = a.g.shared[j];
-  if (s0 < 0 || s0 >= s1 || s1 > a.b.n_seqs) return shared;
-  const int64_t rows =
-      (int64_t)(a.b.q_off ? a.b.q_off[s1] - a.b.q_off[s0] : s1 - s0) * a.share;
-  return rows >= (int64_t)kSoloRows * (s1 - s0) ? 0 : shared;
-}
-
 // Reads the groups' ranges into LDS where they fit; a barrier must follow.
 __device__ __forceinline__ void load_groups(Args& a, Shared& sh) {
   const int j = threadIdx.x;
   if (a.g.n_groups > kGroupTable || j > a.g.n_groups || a.g.n_groups == 0) return;
-  const int s0 = a.g.group_off[j];
-  sh.group_off[j] = s0;
-  if (j < a.g.n_groups) sh.shared[j] = shared_of(a, j, s0, a.g.group_off[j + 1]);
+  sh.group_off[j] = a.g.group_off[j];
+  if (j < a.g.n_groups) sh.shared[j] = a.g.shared[j];
 }
 
 // The group of sequence s, or -1: the last one that starts at or before it.
@@ -214,10 +204,7 @@ __device__ __forceinline__ Unit unit_of(Args& a, const Shared& sh, int u, bool* 
     const int lo = a.b.q_off ? a.b.q_off[s] : s, hi = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
     t.len = a.b.lens[s];
     t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
-    const int shared = t.group < 0 ? 0
-                       : kept ? sh.shared[t.group]
-                              : shared_of(a, t.group, a.g.group_off[t.group],
-                                          a.g.group_off[t.group + 1]);
+    const int shared = t.group < 0 ? 0 : kept ? sh.shared[t.group] : a.g.shared[t.group];
     t.row0 = lo;
     t.fresh = fresh_of(a, lo, hi);
     t.rows = (t.fresh < a.max_new ? t.fresh : a.max_new) * a.share;
@@ -236,7 +223,7 @@ __device__ __forceinline__ Unit unit_of(Args& a, const Shared& sh, int u, bool* 
       if (!a.b.q_off && hi > a.b.n_tokens) hi = a.b.n_tokens;
       t.row0 = lo;
       t.rows = fresh_of(a, lo, hi) * a.share;
-      t.hi = clamp_int(kept ? sh.shared[u] : shared_of(a, u, s0, s1), 0, key_cap(a));
+      t.hi = clamp_int(kept ? sh.shared[u] : a.g.shared[u], 0, key_cap(a));
     }
   }
   return t;
@@ -772,7 +759,7 @@ struct Body {
     Args& a = fresh(this->a);
     __syncthreads();
     const int kind = prefix ? 0 : 1, rows = u.tile_rows();
-    if (!whole && number >= a.pieces[kind]) return;
+    if (!whole && !fits(number, a.pieces[kind])) return;
     for (int t = t0; t < end; ++t) {
       bool bad = false;
       const int64_t at = slot_of(look_up(t), &bad);
@@ -852,7 +839,7 @@ struct Body {
   // Whether a piece of this number has a place (it has, but where the
   // batch's offsets contradict each other).
   __device__ __forceinline__ bool has_place(Args& a, int64_t number, bool whole) const {
-    if (whole || number < a.pieces[prefix ? 0 : 1]) return true;
+    if (whole || fits(number, a.pieces[prefix ? 0 : 1])) return true;
     if (threadIdx.x % kWave == 0) atomicOr(a.status, EP_STATUS_BAD_PAGE);
     return false;
   }
@@ -1184,6 +1171,7 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
       // from memory to an XCD about once. The unit that holds the last point,
       // or this round's last one.
       const int64_t stop = tid + 1 < count ? sh.unit[tid + 1].start : at;
+      __syncthreads();  // the other line's reads of it
       if (tid == 0) sh.first = count - 1;
       __syncthreads();
       if (tid < count && sh.unit[tid].start < end && end <= stop) sh.first = tid;
@@ -1209,7 +1197,7 @@ __global__ __launch_bounds__(kBlock, DP <= 128 ? 2 : 1) void attend_kernel(Atten
           b.hi_tile = tiles_before(v, start, end);
           if (b.lo_tile >= b.hi_tile) continue;
           const bool whole = kind == 1 && v.lo == 0 && b.lo_tile == 0 && b.hi_tile == tiles;
-          if (tid == 0 && v.item + i < a.pieces[kind] - a.workers) {
+          if (tid == 0 && fits(v.item + i, a.pieces[kind] - a.workers)) {
             if (b.lo_tile == 0) a.span[kind][v.item + i].x = w;
             if (b.hi_tile == tiles) a.span[kind][v.item + i].y = whole ? ~w : w;
           }
@@ -1250,7 +1238,7 @@ __device__ __forceinline__ Part part_of(const Attend& a, const Unit& u, int kind
   p.start = u.start + i * u.item_length();
   p.item = u.item + i;
   p.row = row % u.tile_rows();
-  if (p.item >= a.pieces[kind] - a.workers) return p;
+  if (!fits(p.item, a.pieces[kind] - a.workers)) return p;
   const int2 span = a.span[kind][p.item];
   p.w0 = span.x;
   p.whole = span.y < 0;
@@ -1331,7 +1319,7 @@ __global__ __launch_bounds__(kBlock) void join_kernel(Attend a, int64_t rows) {
         const Range r = range_of(a, kind, w, prefix, suffix);
         const int64_t number = (int64_t)w + p.item;
         if (tiles_before(u, p.start, r.begin) < tiles_before(u, p.start, r.end) &&
-            number < a.pieces[kind]) {
+            fits(number, a.pieces[kind])) {
           const int64_t row = number * a.rows[kind] + p.row;
           st = a.stat[kind][row];
           if (st.x != -__builtin_inff()) x = a.sum[kind] + row * DP;

@@ -38,27 +38,6 @@ __device__ __forceinline__ V as(const S& s) {
   return __builtin_bit_cast(V, s);
 }
 
-// Eight consecutive elements as floats.
-template <int DT>
-__device__ __forceinline__ void load8(const uint8_t* p, float* f) {
-  if constexpr (DT == EP_DTYPE_E4M3) {
-    const u32x2 w = *(const u32x2*)p;
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      const auto lo = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], false);
-      const auto hi = __builtin_amdgcn_cvt_pk_f32_fp8(w[i], true);
-      f[4 * i] = lo[0];
-      f[4 * i + 1] = lo[1];
-      f[4 * i + 2] = hi[0];
-      f[4 * i + 3] = hi[1];
-    }
-  } else {
-    const auto v = as<typename Fmt<DT>::vec8>(*(const u32x4*)p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
-  }
-}
-
 // The nearest e4m3 code of f, saturating at 448; a NaN stays one.
 __device__ __forceinline__ float e4m3_range(float f) {
   return f != f ? f : __builtin_amdgcn_fmed3f(f, -448.0f, 448.0f);
@@ -99,11 +78,6 @@ __device__ __forceinline__ void store1(uint8_t* p, float f) {
     *p = (uint8_t)__builtin_amdgcn_cvt_pk_fp8_f32(e4m3_range(f), 0.0f, 0, false);
   else
     *(typename Fmt<DT>::elem*)p = (typename Fmt<DT>::elem)f;
-}
-
-// First row of sequence b among the new tokens.
-__device__ __forceinline__ int first_row(const ep_kv_batch& b, int s) {
-  return b.q_off ? b.q_off[s] : s;
 }
 
 // The sequence of row i < n_tokens (every lane of the wave has the same i):
