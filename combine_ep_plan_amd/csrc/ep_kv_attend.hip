@@ -29,6 +29,23 @@
 // both sides take it: slot (half h, j) of its step s is key 16 s + 8 (j / 4)
 // + 4 h + j % 4, the order the scores come out in. V is read from LDS through
 // the transposing read, four keys of one column per lane.
+//
+// What bounds it (bf16, heads of 128):
+// - Many rows over shared pages (12 sequences of up to 256 new tokens, 40
+//   heads over 8, 8192 shared keys; 232 GFLOP): 320 us with the join, 0.73
+//   PFLOP/s, where a large matrix product reaches 1.35 to 1.6. The matrix
+//   units are busy 36 % of the time and the other vector arithmetic 46 %: two
+//   waves on a SIMD cover each other only in part. The exponentials, the reads
+//   of LDS and the copies to it each account for 5, 5 and 15 % when left out.
+// - Few rows (128 samples of a prompt of 16,384 tokens, 512 keys of their own
+//   on average; 339 MB): 124 us with the join, 2.7 TB/s of the 5.7 that a
+//   copy reaches, the prefix's arithmetic and the waits of short sequences
+//   beside each other. What was tried and did not pay: K straight to
+//   registers with V in two tiles (138 us), workgroups brought into step over
+//   the prefix, which fetches 347 instead of 543 MB (120 us, but 1 % more
+//   elsewhere).
+// - One token over 300 keys: 18.5 us, two launches and some ten dependent
+//   loads.
 #include <type_traits>
 
 #include "ep_kernels.hpp"
@@ -48,7 +65,12 @@ constexpr int kWaves = kBlock / kWave;
 constexpr int kTile = 128;       // keys of a tile
 constexpr int kNone = 0x7fffffff;
 constexpr int kMostKeys = 0x7fffffff - 1024;
-constexpr int kRowsSplit = 32;   // rows of an item whose keys the waves share out
+// Rows of an item whose keys the waves share out. With few rows that ends an
+// item sooner (4 rows over one-byte keys: 31.5 us, 36.5 with the rows shared
+// out and three waves idle; 5 rows, 16 bits: 136 and 137; 24 rows: 78 both).
+// Items of 32 rows read the keys of 33 to 96 rows two or three times: 124
+// against 91 us for up to 96 rows a sequence.
+constexpr int kRowsSplit = 32;
 constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
 constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
 // Costs in the line: of a tile of either kind, and of starting on an item. The
