@@ -73,9 +73,10 @@ extern "C" {
 #define EP_ERR_DEVICE_MISMATCH (-3) /* a buffer is not on the stream's GPU */
 #define EP_ERR_HIP (-4)             /* a HIP runtime call failed */
 
-/* Device status bits, OR-ed into *status by ep_plan. */
+/* Device status bits, OR-ed into *status by the calls that take one. */
 #define EP_STATUS_BAD_EXPERT 1 /* an expert id outside [0, E): slot dropped */
-#define EP_STATUS_CAPACITY 2   /* a rank would receive more than cap rows */
+#define EP_STATUS_CAPACITY 2   /* a rank would receive more than cap rows, or
+                                  the KV pool has too few free pages */
 #define EP_STATUS_BAD_REGION 4 /* a KV region outside its pools: skipped */
 #define EP_STATUS_BAD_PAGE 8   /* a page, sequence or length outside its range */
 
