@@ -59,7 +59,7 @@ size_t pages_layout(const ep_kv_pages& g, int64_t m, void* ws, ep::PagesWs* w) {
   int32_t* p[8];
   size_t at = 0;
   for (int i = 0; i < 8; ++i) {
-    p[i] = (int32_t*)((char*)ws + at);
+    p[i] = ws ? (int32_t*)((char*)ws + at) : nullptr;
     at += ((size_t)n[i] * 4 + 255) & ~(size_t)255;
   }
   if (w) *w = ep::PagesWs{p[0], p[1], p[2], p[3], p[4], p[5], p[6], p[7]};
