@@ -142,6 +142,7 @@ struct Shared {
   int64_t part[kWaves];
   int32_t ipart[kWaves], spart[kWaves];
   int32_t group_off[kGroupTable + 1], shared[kGroupTable];
+  uint64_t refused;          // bit j: of the first kGroupTable groups
   int32_t any_short, special, first;
   int64_t prefix;  // length of the prefix line
   float stat[2][kWaves][32];
@@ -212,42 +213,71 @@ __device__ __forceinline__ int group_of(Args& a, const int32_t* off, int s) {
   return lo < a.g.n_groups && off[lo] <= s && s < off[lo + 1] ? lo : -1;
 }
 
+// The new tokens of sequences s0 .. s1 - 1.
+struct Span {
+  int lo, hi;  // the first, and behind the last
+  bool bad;    // the offsets name no such sequences or rows
+};
+
+// Offsets out of range are not followed. Without a branch, so that groups' and
+// sequences' loads are on their way together.
+__device__ __forceinline__ Span span_of(Args& a, int s0, int s1) {
+  const bool in = s0 >= 0 && s0 <= s1 && s1 <= a.b.n_seqs;
+  const int i0 = in ? s0 : 0, i1 = in ? s1 : 0;
+  Span r;
+  if (a.b.q_off) {
+    r.lo = a.b.q_off[i0];
+    r.hi = a.b.q_off[i1];
+    r.bad = !in || r.lo < 0 || r.hi < r.lo || r.hi > a.b.n_tokens;
+  } else {
+    r.lo = i0;
+    r.hi = i1 < a.b.n_tokens ? i1 : a.b.n_tokens;
+    r.bad = !in;
+  }
+  return r;
+}
+
 // Unit u but for its place; *late: the shared keys reach past the first new
-// token, so that rows of the group see different ones of them.
-__device__ __forceinline__ Unit unit_of(Args& a, const Shared& sh, int u, bool* late) {
+// token, so that rows of the group see different ones of them; *bad: its
+// offsets are not those of a batch. Such a unit has no rows. A group that has
+// none for that reason shares nothing: its sequences read all their keys
+// through their own rows of the table (place_units() sees to that where the
+// groups are in LDS).
+__device__ __forceinline__ Unit unit_of(Args& a, const Shared& sh, int u, bool* late, bool* bad) {
   const int s = u - a.g.n_groups;
   const bool kept = a.g.n_groups <= kGroupTable;
+  int s0 = s, s1 = s + 1;
+  if (s < 0) {
+    s0 = kept ? sh.group_off[u] : a.g.group_off[u];
+    s1 = kept ? sh.group_off[u + 1] : a.g.group_off[u + 1];
+  }
+  const int len = a.b.lens[s < 0 ? 0 : s];
+  const Span rows = span_of(a, s0, s1);
+  // An empty group has nobody to share with, wherever it lies.
+  *bad = rows.bad && s0 != s1;
+  *late = false;
   Unit t;
   t.start = t.item = 0;
-  t.row0 = t.rows = t.lo = t.hi = t.len = t.fresh = 0;
-  t.group = -1;
-  t.seq = s;
-  if (s >= 0) {
-    const int lo = a.b.q_off ? a.b.q_off[s] : s, hi = a.b.q_off ? a.b.q_off[s + 1] : s + 1;
-    t.len = a.b.lens[s];
-    t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
-    const int shared = t.group < 0 ? 0 : kept ? sh.shared[t.group] : a.g.shared[t.group];
-    t.row0 = lo;
-    t.fresh = fresh_of(a, lo, hi);
-    t.rows = (t.fresh < a.max_new ? t.fresh : a.max_new) * a.share;
-    t.lo = clamp_int(shared, 0, key_cap(a));
-    t.hi = clamp_int(t.len, t.lo, key_cap(a));
-    *late = (int64_t)t.len - t.fresh + 1 < shared;
-  } else {
-    const int s0 = kept ? sh.group_off[u] : a.g.group_off[u];
-    const int s1 = kept ? sh.group_off[u + 1] : a.g.group_off[u + 1];
+  t.row0 = rows.lo;
+  t.seq = s0;
+  t.fresh = *bad ? 0 : fresh_of(a, rows.lo, rows.hi);
+  if (s < 0) {
     t.group = u;
-    t.seq = s0;
-    *late = false;
-    if (s0 >= 0 && s0 < s1 && s1 <= a.b.n_seqs) {
-      const int lo = a.b.q_off ? a.b.q_off[s0] : s0;
-      int hi = a.b.q_off ? a.b.q_off[s1] : s1;
-      if (!a.b.q_off && hi > a.b.n_tokens) hi = a.b.n_tokens;
-      t.row0 = lo;
-      t.rows = fresh_of(a, lo, hi) * a.share;
-      t.hi = clamp_int(kept ? sh.shared[u] : a.g.shared[u], 0, key_cap(a));
-    }
+    t.rows = t.fresh * a.share;
+    t.lo = t.len = t.fresh = 0;
+    t.hi = t.rows > 0 ? clamp_int(kept ? sh.shared[u] : a.g.shared[u], 0, key_cap(a)) : 0;
+    return t;
   }
+  t.len = len;
+  t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
+  if (!kept && t.group >= 0 &&
+      span_of(a, a.g.group_off[t.group], a.g.group_off[t.group + 1]).bad)
+    t.group = -1;
+  const int shared = t.group < 0 ? 0 : kept ? sh.shared[t.group] : a.g.shared[t.group];
+  t.rows = (t.fresh < a.max_new ? t.fresh : a.max_new) * a.share;
+  t.lo = clamp_int(shared, 0, key_cap(a));
+  t.hi = clamp_int(t.len, t.lo, key_cap(a));
+  *late = (int64_t)t.len - t.fresh + 1 < shared;
   return t;
 }
 
@@ -1094,9 +1124,26 @@ __device__ __forceinline__ void place_units(Args& a, Shared& sh, int base, int64
   Unit t;
   int64_t x = 0;
   int32_t y[2] = {0, 0};
+  bool late = false, bad = false;
+  if (u < count) t = unit_of(a, sh, u, &late, &bad);
+  if (blockIdx.x == 0 && bad) atomicOr(a.status, EP_STATUS_BAD_PAGE);
+  // Groups in LDS are the first wave's in the first round; where it has the
+  // sequences too, nobody waits for it.
+  if (a.g.n_groups > 0 && a.g.n_groups <= kGroupTable) {
+    uint64_t refused = ballot(!suffix && bad);
+    if (count > kWave) {
+      if (base == 0 && tid == 0) sh.refused = refused;
+      __syncthreads();
+      refused = sh.refused;
+    }
+    if (u < count && suffix && t.group >= 0 && ((refused >> t.group) & 1)) {
+      t.group = -1;
+      t.lo = 0;
+      t.hi = clamp_int(t.len, 0, key_cap(a));
+      late = false;
+    }
+  }
   if (u < count) {
-    bool late;
-    t = unit_of(a, sh, u, &late);
     if (late) sh.any_short = 1;
     if (t.tiles() > 0) {
       y[suffix] = t.items() * a.c.n_heads;

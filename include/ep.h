@@ -605,7 +605,9 @@ EP_API int ep_kv_append(const ep_kv_cache *c, const ep_kv_batch *b,
  * their first shared[j] tokens. Those are read through the row of the
  * group's first sequence, once for all its rows. n_groups 0: nothing is
  * shared. Sequences outside group_off[0] .. group_off[n_groups] - 1 share
- * nothing. */
+ * nothing. A group whose offsets descend, name sequences that the batch does
+ * not have, or rows outside [0, n_tokens) sets EP_STATUS_BAD_PAGE, and its
+ * sequences share nothing. */
 typedef struct ep_kv_groups {
   const int32_t *group_off; /* [n_groups + 1], ascending */
   const int32_t *shared;    /* [n_groups] */
@@ -626,7 +628,8 @@ EP_API size_t ep_kv_attend_bytes(const ep_kv_cache *c, int32_t n_seqs,
  * rounded once from 32-bit sums. A row that sees nothing gets zeros and -inf.
  * out may not overlap q or the cache.
  * lse: float [n_tokens][n_heads], or NULL. Tokens of a sequence behind its
- * first max_new ones are skipped and set EP_STATUS_BAD_PAGE.
+ * first max_new ones are skipped and set EP_STATUS_BAD_PAGE, as are those of
+ * a sequence whose offsets descend or lie outside [0, n_tokens].
  * The workspace (16-byte aligned) holds nothing between calls; calls that
  * may overlap, graphs among them, need one each. */
 EP_API int ep_kv_attend(const ep_kv_cache *c, const ep_kv_batch *b,
