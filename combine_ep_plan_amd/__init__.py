@@ -11,6 +11,7 @@ PyTorch is used for device memory and streams only.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence
 
@@ -202,6 +203,7 @@ def _load() -> ctypes.CDLL:
 
 
 _lib = _load()
+_INT32 = _torch.int32
 
 
 def lib() -> ctypes.CDLL:
@@ -456,11 +458,44 @@ def kv_push_staged_static(ranks: int, regions, n_regions: int, total_bytes: int,
 def _ints(t, shape, name: str):
     """Address of a contiguous int32 tensor of the given shape (None: any size)."""
     have = t.shape
-    if len(have) != len(shape) or any(n is not None and n != m for n, m in zip(shape, have)):
+    if have != shape and (len(have) != len(shape) or
+                          any(n is not None and n != m for n, m in zip(shape, have))):
         raise ValueError(f"{name} has shape {tuple(have)}, not {shape}")
-    if t.dtype != _torch.int32:
+    if t.dtype is not _INT32:
         raise ValueError(f"{name} must be int32, not {t.dtype}")
-    return _addr(t)
+    return t.data_ptr() if t.is_contiguous() else _addr(t)
+
+
+def _word(t, name: str):
+    """Address of a tensor of at least one int32, or None."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype is not _INT32 or t.numel() < 1:
+        raise ValueError(f"{name} must be int32 with at least one element, not {t.dtype} "
+                         f"{tuple(t.shape)}")
+    return t.data_ptr() if t.is_contiguous() else _addr(t)
+
+
+def _room(ws, need: int):
+    """Address of a workspace of at least `need` bytes (0: sizes that the library refuses). The
+    library sees no more than the allocation around it, which may hold other tensors."""
+    if ws is None or isinstance(ws, int):
+        return ws
+    if ws.nbytes < need:
+        raise ValueError(f"ws holds {ws.nbytes} bytes, the call needs {need}")
+    return ws.data_ptr() if ws.is_contiguous() else _addr(ws)
+
+
+@functools.lru_cache(maxsize=4096)
+def _pages_bytes(n_seqs: int, n_pages: int, m: int) -> int:
+    """ep_kv_pages_bytes by what it depends on: a call to the library takes 1 us of the 5 that a
+    page operation takes on the host."""
+    g = KvPages(None, None, None, None, n_seqs, 1, n_pages, 1, 1, 0, 16, 16 * n_pages)
+    return _lib.ep_kv_pages_bytes(ctypes.byref(g), m)
+
+
+def _page_room(g: KvPages, m: int, ws):
+    return _room(ws, _pages_bytes(g.n_seqs, g.n_pages, m))
 
 
 def make_kv_pages(tables, lens, refs, pool, page_tokens: int) -> KvPages:
@@ -484,32 +519,33 @@ def kv_pages_bytes(g: KvPages, m: int) -> int:
 def kv_extend(g: KvPages, seqs, add, ws, status, stream=None) -> None:
     m = seqs.numel()
     _check(_lib.ep_kv_extend(ctypes.byref(g), _ints(seqs, (m,), "seqs"), _ints(add, (m,), "add"),
-                             m, _addr(ws), _addr(status), _stream(stream)), "ep_kv_extend")
+                             m, _page_room(g, m, ws), _word(status, "status"), _stream(stream)),
+           "ep_kv_extend")
 
 
 def kv_fork(g: KvPages, parents, children, ws, status, stream=None) -> None:
     m = parents.numel()
     _check(_lib.ep_kv_fork(ctypes.byref(g), _ints(parents, (m,), "parents"),
-                           _ints(children, (m,), "children"), m, _addr(ws), _addr(status),
-                           _stream(stream)), "ep_kv_fork")
+                           _ints(children, (m,), "children"), m, _page_room(g, m, ws),
+                           _word(status, "status"), _stream(stream)), "ep_kv_fork")
 
 
 def kv_free(g: KvPages, seqs, ws, status, stream=None) -> None:
     m = seqs.numel()
-    _check(_lib.ep_kv_free(ctypes.byref(g), _ints(seqs, (m,), "seqs"), m, _addr(ws),
-                           _addr(status), _stream(stream)), "ep_kv_free")
+    _check(_lib.ep_kv_free(ctypes.byref(g), _ints(seqs, (m,), "seqs"), m, _page_room(g, m, ws),
+                           _word(status, "status"), _stream(stream)), "ep_kv_free")
 
 
 def kv_compact(g: KvPages, ws, status, n_live=None, stream=None) -> None:
-    _check(_lib.ep_kv_compact(ctypes.byref(g), _addr(n_live), _addr(ws), _addr(status),
-                              _stream(stream)), "ep_kv_compact")
+    _check(_lib.ep_kv_compact(ctypes.byref(g), _word(n_live, "n_live"), _page_room(g, 0, ws),
+                              _word(status, "status"), _stream(stream)), "ep_kv_compact")
 
 
 def kv_copy_pages(g: KvPages, src, dst, ws, status, stream=None) -> None:
     m = src.numel()
     _check(_lib.ep_kv_copy_pages(ctypes.byref(g), _ints(src, (m,), "src"), _ints(dst, (m,), "dst"),
-                                 m, _addr(ws), _addr(status), _stream(stream)),
-           "ep_kv_copy_pages")
+                                 m, _page_room(g, m, ws), _word(status, "status"),
+                                 _stream(stream)), "ep_kv_copy_pages")
 
 
 def _dtype(t, name: str) -> int:
@@ -605,7 +641,7 @@ def kv_append(cache: KvCache, tables, lens, q_off, q, k, v, q_out, rope, status,
     _check(_lib.ep_kv_append(
         ctypes.byref(cache), ctypes.byref(b), rq, heads, _rows(k, "k", dtype, shape),
         _rows(v, "v", dtype, shape), ro, None if rope is None else ctypes.byref(rope),
-        _addr(status), _stream(stream)), "ep_kv_append")
+        _word(status, "status"), _stream(stream)), "ep_kv_append")
 
 
 def kv_attend_bytes(cache: KvCache, n_seqs: int, n_groups: int, n_tokens: int, n_heads: int,
@@ -624,18 +660,22 @@ def kv_attend(cache: KvCache, tables, lens, q_off, max_new: int, group_off, shar
     b = _batch(tables, lens, q_off, shape[0], _dtype(q, "q"))
     if (group_off is None) != (shared is None):
         raise ValueError("group_off and shared must be given together")
-    groups = None
+    groups, n = None, 0
     if shared is not None:
         n = shared.numel()
         groups = KvGroups(_ints(group_off, (n + 1,), "group_off"), _ints(shared, (n,), "shared"),
                           n, 0)
     if lse is not None and (lse.shape != shape[:2] or lse.dtype != _torch.float32):
         raise ValueError(f"lse must be float32 {tuple(shape[:2])}")
+    need = 0   # an empty batch needs no workspace
+    if shape[0] > 0 and b.n_seqs > 0:
+        need = _lib.ep_kv_attend_bytes(ctypes.byref(cache), b.n_seqs, n, shape[0], shape[1],
+                                       int(max_new))
     _check(_lib.ep_kv_attend(
         ctypes.byref(cache), ctypes.byref(b), None if groups is None else ctypes.byref(groups),
         int(max_new), _rows(q, "q", dtype, shape), shape[1], _rows(out, "out", dtype, shape),
         _addr(lse), float(sm_scale),
-        _addr(ws), _addr(status), _stream(stream)), "ep_kv_attend")
+        _room(ws, need), _word(status, "status"), _stream(stream)), "ep_kv_attend")
 
 
 def probe_copy(dst, src, nbytes: int, stream=None) -> None:
