@@ -567,6 +567,25 @@ __device__ __forceinline__ V read_lds(uint32_t at) {
   return *(lds_v*)at;
 }
 
+// m need not be the maximum of a row's scores, only near it: it follows when
+// they pass it by 2^kSlack, which keeps every weight under 2^kSlack and spares
+// the rescale of the sums most of the time (with the maximum itself, some row
+// of 32 has a new one in almost every step).
+constexpr float kSlack = 8.0f;
+// Weights and sums are 2^kRaise times what m alone would make them. In fp16 a
+// weight under 2^-14 loses bits and one under 2^-25 is lost, and a thousand
+// such keys beside one of large weight and small V are the row's output. The
+// type holds 2^15, so 7 powers of two are free above those of the slack.
+template <int QT>
+constexpr float kRaise = QT == EP_DTYPE_F16 ? 7.0f : 0.0f;
+
+// What the exponents of a row's weights are taken off; nothing seen yet: any
+// finite value.
+template <int QT>
+__device__ __forceinline__ float base_of(float m, float c) {
+  return m == -__builtin_inff() ? 0.0f : m * c - kRaise<QT>;
+}
+
 // NS * 32 keys in LDS, `at` bytes behind the tiles of `rd`. c > 0: the factor
 // of the scores in powers of two. masked: some row does not see some of the
 // keys; bit t of `see` says whether this lane's row sees key t.
@@ -641,11 +660,6 @@ __device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float 
 #pragma unroll
     for (int i = 0; i < 16; ++i) top = fmaxf(top, s[n][i]);
   top = max_halves(top);
-  // m need not be the maximum, only near it: it follows when a row's scores
-  // pass it by 2^kSlack, which keeps every weight under 2^kSlack and spares
-  // the rescale of the sums most of the time (with the maximum itself, some
-  // row of 32 has a new one in almost every step).
-  constexpr float kSlack = 8.0f;
   if (ballot((top - r.m) * c > kSlack)) {
     const float m = fmaxf(r.m, top);
     // exp2(-inf) = 0 where nothing was seen before; rows that still see
@@ -658,10 +672,11 @@ __device__ __forceinline__ void step(Rows32<DP>& r, Reads<DP> rd, int at, float 
       for (int i = 0; i < 16; ++i) r.o[d][i] *= w;
     r.m = m;
   }
-  const float base = r.m == -__builtin_inff() ? 0.0f : r.m * c;
+  const float base = base_of<QT>(r.m, c);
   float sum = 0.0f;
   // The weights meet V in the rows' 16-bit type: half a step of it, relative,
-  // per weight; the sum of weights is taken before.
+  // per weight; the sum of weights is taken before. kRaise keeps small fp16
+  // weights from it for longer.
   typename Fmt<QT>::vec8 w[2];
   const auto weights = [&](int g, int j0, int j1) {
 #pragma unroll
@@ -875,7 +890,7 @@ struct Body {
     const int kind = prefix ? 0 : 1;
     // Scores that are all NaN leave no maximum but a sum: the join has to
     // see it.
-    const float n = m == -__builtin_inff() ? (l == 0.0f ? m : 0.0f) : m * c;
+    const float n = m == -__builtin_inff() && l == 0.0f ? m : base_of<QT>(m, c);
     if (!whole)
       a.stat[kind][number * a.rows[kind] + row % u.tile_rows()] = make_float2(n, l);
     else if (a.lse)

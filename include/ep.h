@@ -625,7 +625,9 @@ EP_API size_t ep_kv_attend_bytes(const ep_kv_cache *c, int32_t n_seqs,
  * tokens' own K and V are there: append first). Head h reads KV head
  * h / (n_heads / c->n_heads). With s_i = sm_scale * q . k_i over positions
  * i <= the row's own: lse = log sum exp s_i, out = sum exp(s_i - lse) v_i,
- * rounded once from 32-bit sums. A row that sees nothing gets zeros and -inf.
+ * rounded once from 32-bit sums. Each weight meets v_i rounded to the rows'
+ * type (half a step of it; in fp16 also half of 2^-31 of the largest weight).
+ * A row that sees nothing gets zeros and -inf.
  * out may not overlap q or the cache.
  * lse: float [n_tokens][n_heads], or NULL. Tokens of a sequence behind its
  * first max_new ones are skipped and set EP_STATUS_BAD_PAGE, as are those of
