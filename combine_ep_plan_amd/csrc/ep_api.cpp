@@ -684,19 +684,37 @@ int ep_probe_pattern(void* dst, const void* src, const int32_t* table, int64_t r
 }
 
 const char* ep_status_string(int code) {
+#define EP_TEXT_EXPERT "expert id out of range (slot dropped)"
+#define EP_TEXT_CAPACITY "capacity exceeded (receive rows dropped, or too few free KV pages: refused)"
+#define EP_TEXT_REGION "KV region outside its pools (skipped)"
+#define EP_TEXT_PAGE "page, sequence or length out of range (skipped)"
+  // By the sum of the bits: the calls that share a status word may set any.
+  static const char* const kBits[16] = {
+      "ok",
+      EP_TEXT_EXPERT,
+      EP_TEXT_CAPACITY,
+      EP_TEXT_EXPERT "; " EP_TEXT_CAPACITY,
+      EP_TEXT_REGION,
+      EP_TEXT_EXPERT "; " EP_TEXT_REGION,
+      EP_TEXT_CAPACITY "; " EP_TEXT_REGION,
+      EP_TEXT_EXPERT "; " EP_TEXT_CAPACITY "; " EP_TEXT_REGION,
+      EP_TEXT_PAGE,
+      EP_TEXT_EXPERT "; " EP_TEXT_PAGE,
+      EP_TEXT_CAPACITY "; " EP_TEXT_PAGE,
+      EP_TEXT_EXPERT "; " EP_TEXT_CAPACITY "; " EP_TEXT_PAGE,
+      EP_TEXT_REGION "; " EP_TEXT_PAGE,
+      EP_TEXT_EXPERT "; " EP_TEXT_REGION "; " EP_TEXT_PAGE,
+      EP_TEXT_CAPACITY "; " EP_TEXT_REGION "; " EP_TEXT_PAGE,
+      EP_TEXT_EXPERT "; " EP_TEXT_CAPACITY "; " EP_TEXT_REGION "; " EP_TEXT_PAGE,
+  };
+  static_assert(EP_OK == 0 && EP_STATUS_BAD_EXPERT == 1 && EP_STATUS_CAPACITY == 2 &&
+                EP_STATUS_BAD_REGION == 4 && EP_STATUS_BAD_PAGE == 8, "kBits goes by the bits");
   switch (code) {
-    case EP_OK: return "ok";
     case EP_ERR_INVALID_ARG: return "invalid argument";
     case EP_ERR_UNSUPPORTED: return "unsupported size";
     case EP_ERR_DEVICE_MISMATCH: return "buffer on another device";
     case EP_ERR_HIP: return "HIP runtime error";
-    case EP_STATUS_BAD_EXPERT: return "expert id out of range (slot dropped)";
-    case EP_STATUS_CAPACITY: return "receive capacity exceeded (rows dropped)";
-    case EP_STATUS_BAD_EXPERT | EP_STATUS_CAPACITY:
-      return "expert id out of range and receive capacity exceeded";
-    case EP_STATUS_BAD_REGION: return "KV region outside its pools (skipped)";
-    case EP_STATUS_BAD_PAGE: return "page, sequence or length out of range (skipped)";
-    default: return "unknown code";
+    default: return code >= 0 && code < 16 ? kBits[code] : "unknown code";
   }
 }
 

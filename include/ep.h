@@ -728,7 +728,7 @@ EP_API int ep_probe_pattern(void *dst, const void *src, const int32_t *table,
                             int64_t piece_bytes, int fan_in, int in_flight, int mode,
                             int flags, int64_t waves, hipStream_t stream);
 
-/* Text for a return code or status bit set; never NULL. */
+/* Text for a return code or any set of status bits; never NULL. */
 EP_API const char *ep_status_string(int code);
 
 /* Last host-side error message of the calling thread ("" if none). */
