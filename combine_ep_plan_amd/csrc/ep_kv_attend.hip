@@ -213,29 +213,28 @@ __device__ __forceinline__ int group_of(Args& a, const int32_t* off, int s) {
   return lo < a.g.n_groups && off[lo] <= s && s < off[lo + 1] ? lo : -1;
 }
 
-// The new tokens of sequences s0 .. s1 - 1.
+// The new tokens of sequences s0 .. s1 - 1: the first, and behind the last.
+// Offsets out of range are not followed.
 struct Span {
-  int lo, hi;  // the first, and behind the last
-  bool bad;    // the offsets name no such sequences or rows
-};
+  int lo, hi;
+  bool in;
 
-// Offsets out of range are not followed. Without a branch, so that groups' and
-// sequences' loads are on their way together.
-__device__ __forceinline__ Span span_of(Args& a, int s0, int s1) {
-  const bool in = s0 >= 0 && s0 <= s1 && s1 <= a.b.n_seqs;
-  const int i0 = in ? s0 : 0, i1 = in ? s1 : 0;
-  Span r;
-  if (a.b.q_off) {
-    r.lo = a.b.q_off[i0];
-    r.hi = a.b.q_off[i1];
-    r.bad = !in || r.lo < 0 || r.hi < r.lo || r.hi > a.b.n_tokens;
-  } else {
-    r.lo = i0;
-    r.hi = i1 < a.b.n_tokens ? i1 : a.b.n_tokens;
-    r.bad = !in;
+  __device__ __forceinline__ Span(Args& a, int s0, int s1)
+      : in(s0 >= 0 && s0 <= s1 && s1 <= a.b.n_seqs) {
+    lo = in ? s0 : 0;
+    hi = in ? s1 : 0;
+    if (a.b.q_off) {
+      lo = a.b.q_off[lo];
+      hi = a.b.q_off[hi];
+    } else if (hi > a.b.n_tokens) {
+      hi = a.b.n_tokens;
+    }
   }
-  return r;
-}
+  // Whether the offsets name no such sequences or rows.
+  __device__ __forceinline__ bool bad(Args& a) const {
+    return !in || (a.b.q_off && (lo < 0 || hi < lo || hi > a.b.n_tokens));
+  }
+};
 
 // Unit u but for its place; *late: the shared keys reach past the first new
 // token, so that rows of the group see different ones of them; *bad: its
@@ -251,33 +250,37 @@ __device__ __forceinline__ Unit unit_of(Args& a, const Shared& sh, int u, bool* 
     s0 = kept ? sh.group_off[u] : a.g.group_off[u];
     s1 = kept ? sh.group_off[u + 1] : a.g.group_off[u + 1];
   }
+  // On their way for both kinds of unit while the group is searched for.
   const int len = a.b.lens[s < 0 ? 0 : s];
-  const Span rows = span_of(a, s0, s1);
-  // An empty group has nobody to share with, wherever it lies.
-  *bad = rows.bad && s0 != s1;
-  *late = false;
+  const Span rows(a, s0, s1);
   Unit t;
   t.start = t.item = 0;
-  t.row0 = rows.lo;
   t.seq = s0;
-  t.fresh = *bad ? 0 : fresh_of(a, rows.lo, rows.hi);
-  if (s < 0) {
-    t.group = u;
-    t.rows = t.fresh * a.share;
-    t.lo = t.len = t.fresh = 0;
-    t.hi = t.rows > 0 ? clamp_int(kept ? sh.shared[u] : a.g.shared[u], 0, key_cap(a)) : 0;
-    return t;
+  t.group = u;
+  if (s >= 0) {
+    t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
+    if (!kept && t.group >= 0 &&
+        Span(a, a.g.group_off[t.group], a.g.group_off[t.group + 1]).bad(a))
+      t.group = -1;
   }
-  t.len = len;
-  t.group = kept ? group_of(a, sh.group_off, s) : group_of(a, a.g.group_off, s);
-  if (!kept && t.group >= 0 &&
-      span_of(a, a.g.group_off[t.group], a.g.group_off[t.group + 1]).bad)
-    t.group = -1;
   const int shared = t.group < 0 ? 0 : kept ? sh.shared[t.group] : a.g.shared[t.group];
-  t.rows = (t.fresh < a.max_new ? t.fresh : a.max_new) * a.share;
-  t.lo = clamp_int(shared, 0, key_cap(a));
-  t.hi = clamp_int(t.len, t.lo, key_cap(a));
-  *late = (int64_t)t.len - t.fresh + 1 < shared;
+  // An empty group has nobody to share with, wherever it lies.
+  *bad = s0 != s1 && rows.bad(a);
+  t.row0 = rows.lo;
+  const int fresh = *bad ? 0 : fresh_of(a, rows.lo, rows.hi);
+  if (s < 0) {
+    t.rows = fresh * a.share;
+    t.lo = t.len = t.fresh = 0;
+    t.hi = t.rows > 0 ? clamp_int(shared, 0, key_cap(a)) : 0;
+    *late = false;
+  } else {
+    t.len = len;
+    t.fresh = fresh;
+    t.rows = (fresh < a.max_new ? fresh : a.max_new) * a.share;
+    t.lo = clamp_int(shared, 0, key_cap(a));
+    t.hi = clamp_int(len, t.lo, key_cap(a));
+    *late = (int64_t)len - fresh + 1 < shared;
+  }
   return t;
 }
 
