@@ -6,9 +6,11 @@
 //
 // Bytes bound it: q is read and written once, k and v are read once and
 // written once. 14,900 tokens of 32 + 8 + 8 heads of 128, bf16 to e4m3 (335
-// MB), take 70 us: 4.8 TB/s, against 5.7 that a large copy reaches. A step of
-// 128 tokens takes 5.5 us, most of it the chain from the offsets over the
-// table to the slot, and the launch.
+// MB), take 67 us: 5.0 TB/s, against 5.7 that a large copy reaches; 10,000 to a
+// bf16 cache take 43 us, 5.7 TB/s. With the 5 + 1 + 1 heads of one rank a token
+// has items for one wave of a block's four, and 14,900 tokens (53 MB) take 21
+// us, 2.6 TB/s. A step of 128 tokens takes 5.5 us, most of it the chain from
+// the offsets over the table to the slot, and the launch.
 //
 // A block takes one token or a few and forms their sines and cosines once, in
 // LDS, for all heads; a work item is a pair of 16-byte chunks (or one chunk,
@@ -312,11 +314,12 @@ hipError_t launch_kv_append(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                             const ep_rope& rope, int32_t* status, hipStream_t stream) {
   const int turned = row_items(rope, c.head_dim), plain = c.head_dim / 8;
   // Four tokens of a block have their loads on the way together and share the
-  // block's start, which pays once every CU has blocks enough (32 + 8 heads of
-  // 128: 90 against 70 us at 15,000 tokens, 56 against 48 at 10,000, 26
-  // against 24 at 4,000; as fast at 2,400). Few tokens finish sooner in blocks
-  // of their own (12.5 against 14.5 us at 1,000). 16 gain nothing over 4 (69
-  // us at 15,000) and lose where blocks get few (61 us at 10,000).
+  // block's start, which pays once every CU has blocks enough; few tokens
+  // finish sooner in blocks of their own. One and four tokens, us, with 32 + 8
+  // heads of 128 in bf16: 13.1 and 14.2 at 2,000 tokens, 16.5 and 16.1 at
+  // 2,400, 48.0 and 43.4 at 10,000 (an e4m3 cache: 75.4 and 67.7 at 14,900).
+  // With 5 + 1 heads: 5.1 and 6.6 at 2,000, 6.7 and 6.9 at 2,400, 8.8 and 7.6 at
+  // 4,000, 30.2 and 20.8 at 14,900.
   const int tokens = b.n_tokens >= 2048 ? kAhead : 1;
   const Append a{c,      b,     q, k, v, q_out, rope, n_heads, tokens,
                  turned, log2_up(turned), plain, log2_up(plain), status};

@@ -32,19 +32,22 @@
 //
 // What bounds it (bf16, heads of 128):
 // - Many rows over shared pages (12 sequences of up to 256 new tokens, 40
-//   heads over 8, 8192 shared keys; 232 GFLOP): 320 us with the join, 0.73
+//   heads over 8, 8192 shared keys; 232 GFLOP): 323 us with the join, 0.72
 //   PFLOP/s, where a large matrix product reaches 1.35 to 1.6. The matrix
 //   units are busy 36 % of the time and the other vector arithmetic 46 %: two
 //   waves on a SIMD cover each other only in part. The exponentials, the reads
 //   of LDS and the copies to it each account for 5, 5 and 15 % when left out.
-// - Few rows (128 samples of a prompt of 16,384 tokens, 512 keys of their own
-//   on average; 339 MB): 124 us with the join, 2.7 TB/s of the 5.7 that a
-//   copy reaches, the prefix's arithmetic and the waits of short sequences
-//   beside each other. What was tried and did not pay: K straight to
-//   registers with V in two tiles (138 us), workgroups brought into step over
-//   the prefix, which fetches 347 instead of 543 MB (120 us, but 1 % more
-//   elsewhere).
-// - One token over 300 keys: 18.5 us, two launches and some ten dependent
+// - Many rows over their own keys: a row tile takes all keys of its sequence,
+//   those that are hidden from all its rows as well, which is twice the needed
+//   operations for a prompt with nothing before it (4096 tokens, 172 GFLOP
+//   visible: 474 us).
+// - Few rows over a prefix (128 samples of a prompt of 16,384 tokens, 512 keys
+//   of their own on average; 339 MB): 124 us with the join, 2.7 TB/s of the 5.7
+//   that a copy reaches, the prefix's arithmetic and the waits of short
+//   sequences beside each other.
+// - Few rows over their own keys (32 to 128 sequences, 4096 to 32,768 keys, 40
+//   heads over 8): 4.4 to 5.4 TB/s, 3.4 to 4.7 over one-byte caches.
+// - One token over 300 keys: 18.6 us, two launches and some ten dependent
 //   loads.
 #include <type_traits>
 
@@ -66,16 +69,20 @@ constexpr int kTile = 128;       // keys of a tile
 constexpr int kNone = 0x7fffffff;
 constexpr int kMostKeys = 0x7fffffff - 1024;
 // Rows of an item whose keys the waves share out. With few rows that ends an
-// item sooner (4 rows over one-byte keys: 31.5 us, 36.5 with the rows shared
-// out and three waves idle; 5 rows, 16 bits: 136 and 137; 24 rows: 78 both).
-// Items of 32 rows read the keys of 33 to 96 rows two or three times: 124
-// against 91 us for up to 96 rows a sequence.
+// item sooner (4 rows of 64 over one-byte keys in pages of one token: 40 us, 52
+// with the rows shared out and three waves idle; 4 rows of 128 over one-byte
+// keys: 73 and 81; 5 rows over 16 bits: 113 both). Items of 32 rows would read
+// the keys of 33 to 96 rows two or three times: 214 against 120 us for 48 rows,
+// 322 against 128 for 96.
 constexpr int kRowsSplit = 32;
 constexpr int kRowsBlock = 128;  // rows of an item whose rows the waves share out
 constexpr int kGroupTable = 64;  // groups whose ranges are kept in LDS
-// Costs in the line: of a tile of either kind, and of starting on an item. The
-// times hardly follow them (338 MB of keys: 131 to 140 us for all that were
-// tried); an item's start is worth two tiles, which short batches show.
+// Costs in the line: of a tile of either kind, and of starting on an item. A
+// split tile at half of a block's tile costs short batches 5 to 11 % (25.4
+// against 22.9 us for one rank's decode, 34.6 and 31.7 for drafts) and others
+// nothing; at one and a half times it drafts 11 %, others 2 to 5 %. An item's
+// start at half a tile leaves prompts uneven (500 and 361 us), at four tiles it
+// costs 128 samples 5 % (143 and 135).
 constexpr int kCostSplit = 4;
 constexpr int kCostBlock = 4;
 constexpr int kCostItem = 8;
@@ -1575,8 +1582,9 @@ hipError_t launch(const Attend& a, hipStream_t stream) {
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   // More lanes to a row where it has many pieces: where items are few, and
-  // each is cut for many workgroups (35 pieces per row, 160 rows: 7 against
-  // 13 us; 2 pieces, 1200 rows: 12 against 7 us).
+  // each is cut for many workgroups (16 pieces per row, 160 rows: 40.6 us with
+  // 16 groups, 42.3 with one; 3 pieces, 1200 rows: 110.2 with one, 113.8 with
+  // 16; one piece, 5120 rows: 397 and 407).
   const int64_t rows = (int64_t)a.b.n_tokens * a.heads;
   const int64_t items = (int64_t)a.pieces[0] + a.pieces[1] - (a.pieces[0] > 0 ? 2 : 1) * a.workers;
   const int share = a.workers >= 8 * items ? 16 : a.workers >= 3 * items ? 4 : 1;

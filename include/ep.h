@@ -443,6 +443,10 @@ EP_API int ep_kv_push_staged_static(int32_t ranks, const ep_kv_region *regions,
  * that names a sequence or a page out of range, or a length that the table
  * cannot hold, is skipped and sets EP_STATUS_BAD_PAGE. Of several requests
  * for one sequence the first counts, the others are skipped and flagged.
+ * Broken state is flagged as well and nothing out of range is touched: a fork
+ * copies an entry outside the pool as it is, a compaction leaves it, and
+ * ep_kv_free empties a sequence whose length its table cannot hold too (with
+ * every page of its row, or with none if the length is negative).
  * ---------------------------------------------------------------------- */
 typedef struct ep_kv_pages {
   int32_t *tables;     /* [n_seqs][max_pages] */
@@ -518,7 +522,9 @@ EP_API int ep_kv_copy_pages(const ep_kv_pages *g, const int32_t *src,
  * q_off[n_seqs] belong to no sequence: nothing reads them and they are left
  * as they were. A table entry outside [0, n_pages), or a position behind
  * max_pages * page_tokens, sets EP_STATUS_BAD_PAGE; its token is neither
- * written nor attended to.
+ * written nor attended to. A position below 0 (lens[b] is less than the new
+ * tokens) has no slot either: ep_kv_append flags it, ep_kv_attend gives its
+ * row what a row that sees nothing gets.
  * ---------------------------------------------------------------------- */
 #define EP_DTYPE_BF16 0
 #define EP_DTYPE_F16 1
@@ -626,8 +632,8 @@ EP_API size_t ep_kv_attend_bytes(const ep_kv_cache *c, int32_t n_seqs,
  * h / (n_heads / c->n_heads). With s_i = sm_scale * q . k_i over positions
  * i <= the row's own: lse = log sum exp s_i, out = sum exp(s_i - lse) v_i,
  * rounded once from 32-bit sums. Each weight meets v_i rounded to the rows'
- * type (half a step of it; in fp16 also half of 2^-31 of the largest weight).
- * A row that sees nothing gets zeros and -inf.
+ * type (half a step of it, in fp16 at least 2^-32 of the largest weight). A
+ * row that sees nothing gets zeros and -inf.
  * out may not overlap q or the cache.
  * lse: float [n_tokens][n_heads], or NULL. Tokens of a sequence behind its
  * first max_new ones are skipped and set EP_STATUS_BAD_PAGE, as are those of
