@@ -36,6 +36,8 @@ EP_DTYPE_BF16, EP_DTYPE_F16, EP_DTYPE_E4M3 = range(3)
 EP_ROPE_HALF, EP_ROPE_INTERLEAVED = range(2)
 EP_ROPE_NONE, EP_ROPE_LINEAR, EP_ROPE_NTK, EP_ROPE_YARN = range(4)
 EP_PROBE_NT_LOADS, EP_PROBE_XCD, EP_PROBE_ONE_WAVE = 1, 2, 4
+EP_NORM_MAX_HIDDEN = 32768
+EP_ACT_NONE, EP_ACT_SILU, EP_ACT_GELU, EP_ACT_SWIGLU = range(4)
 
 # Every entry point the C header declares (checked by the tests).
 EXPORTS = (
@@ -51,6 +53,9 @@ EXPORTS = (
     "ep_kv_push_staged_static",
     "ep_kv_pages_bytes", "ep_kv_extend", "ep_kv_fork", "ep_kv_free", "ep_kv_compact",
     "ep_kv_copy_pages", "ep_rope_freqs", "ep_kv_append", "ep_kv_attend_bytes", "ep_kv_attend",
+    "ep_rms_norm", "ep_rms_norm_grad_bytes", "ep_rms_norm_grad",
+    "ep_expert_product", "ep_expert_product_grad_bytes", "ep_expert_product_grad",
+    "ep_combine_grad", "ep_dispatch_grad",
     "ep_probe_copy", "ep_probe_pattern", "ep_status_string",
     "ep_last_error",
 )
@@ -129,6 +134,19 @@ class KvGroups(ctypes.Structure):
                 ("n_groups", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
+class Norm(ctypes.Structure):
+    """ep_norm: RMS norm of rows (see rms_norm)."""
+    _fields_ = [("weight", ctypes.c_void_p), ("rows", ctypes.c_int64), ("hidden", ctypes.c_int32),
+                ("dtype", ctypes.c_int32), ("eps", ctypes.c_float), ("reserved", ctypes.c_int32)]
+
+
+class Product(ctypes.Structure):
+    """ep_product: the experts' matrices (see make_product)."""
+    _fields_ = [("w", ctypes.c_void_p), ("w_scale", ctypes.c_void_p), ("bias", ctypes.c_void_p),
+                ("inn", ctypes.c_int32), ("out", ctypes.c_int32), ("act", ctypes.c_int32),
+                ("dtype", ctypes.c_int32)]
+
+
 def _load() -> ctypes.CDLL:
     # torch first: it loads its own HIP runtime, and the library's dependency
     # on libamdhip64.so.7 must resolve to that same, already-loaded copy
@@ -189,6 +207,14 @@ def _load() -> ctypes.CDLL:
                                         ctypes.POINTER(KvGroups), ctypes.c_int32,
                                         ctypes.POINTER(Rows), ctypes.c_int32,
                                         ctypes.POINTER(Rows), P, ctypes.c_float, P, P, P]),
+        "ep_rms_norm": (ctypes.c_int, [ctypes.POINTER(Norm)] + [P] * 7),
+        "ep_rms_norm_grad_bytes": (ctypes.c_size_t, [ctypes.POINTER(Norm)]),
+        "ep_rms_norm_grad": (ctypes.c_int, [ctypes.POINTER(Norm)] + [P] * 7),
+        "ep_expert_product": (ctypes.c_int, [D, ctypes.POINTER(Product)] + [P] * 6),
+        "ep_expert_product_grad_bytes": (ctypes.c_size_t, [D, ctypes.POINTER(Product)]),
+        "ep_expert_product_grad": (ctypes.c_int, [D, ctypes.POINTER(Product)] + [P] * 9),
+        "ep_combine_grad": (ctypes.c_int, [D] + [P] * 7),
+        "ep_dispatch_grad": (ctypes.c_int, [D] + [P] * 5),
         "ep_probe_copy": (ctypes.c_int, [P, P, ctypes.c_size_t, P]),
         "ep_probe_pattern": (ctypes.c_int, [P, P, P, I64, I64, I64, I64, ctypes.c_int,
                                             ctypes.c_int, ctypes.c_int, ctypes.c_int, I64, P]),
@@ -707,6 +733,166 @@ def probe_pattern(dst, src, table, rows: int, indexed_rows: int, row_bytes: int,
                                  int(indexed_rows), int(row_bytes), int(piece_bytes),
                                  int(fan_in), int(in_flight), int(mode), int(flags), int(waves),
                                  _stream(stream)), "ep_probe_pattern")
+
+
+# ---------------------------------------------------------------------------
+# Around dispatch and combine: norm, experts' products, backward passes
+# ---------------------------------------------------------------------------
+
+_BF16 = _torch.bfloat16
+_RAW = (_torch.uint8, _torch.int16, _torch.uint16)   # row buffers without a number type of their own
+
+
+def _dense(t, need: int, name: str, *dtypes):
+    """Address of a contiguous buffer of at least `need` bytes (-1: not known here) of one of the
+    dtypes; None and raw addresses pass."""
+    if t is None or isinstance(t, int):
+        return t
+    if t.dtype not in dtypes:
+        raise ValueError(f"{name} has dtype {t.dtype}: {', '.join(str(x)[6:] for x in dtypes)} taken")
+    if t.nbytes < need:
+        raise ValueError(f"{name} holds {t.nbytes} bytes, the call needs {need}")
+    return t.data_ptr() if t.is_contiguous() else _addr(t)
+
+
+def _norm(rows: int, hidden: int, weight, dtype, eps: float) -> Norm:
+    if weight.shape != (hidden,) or weight.dtype is not dtype:
+        raise ValueError(f"weight is {weight.dtype} {tuple(weight.shape)}, not {dtype} [{hidden}]")
+    return Norm(_addr(weight), rows, hidden, _dtype(weight, "weight"), eps, 0)
+
+
+def rms_norm(x, weight, eps: float, residual=None, sum=None, y=None, codes=None, scales=None,
+             stream=None) -> None:
+    """RMS norm of the rows of x [..., hidden] (bfloat16 or float16), after the residual's addition
+    (its result goes to sum, which may be residual). y: the normed rows; codes (float8_e4m3fn or
+    uint8) and float32 scales: the same rows as the planes of a block-fp8 dispatch."""
+    hidden, t = x.shape[-1], x.dtype
+    n = x.numel() // hidden if hidden else 0
+    need = 2 * n * hidden
+    p = _norm(n, hidden, weight, t, eps)
+    _check(_lib.ep_rms_norm(
+        ctypes.byref(p), _addr(x), _dense(residual, need, "residual", t),
+        _dense(sum, need, "sum", t), _dense(y, need, "y", t),
+        _dense(codes, n * hidden, "codes", _torch.float8_e4m3fn, _torch.uint8),
+        _dense(scales, n * hidden // 32, "scales", _torch.float32, _torch.uint8),
+        _stream(stream)), "ep_rms_norm")
+
+
+@functools.lru_cache(maxsize=4096)
+def rms_norm_grad_bytes(rows: int, hidden: int) -> int:
+    """Workspace bytes of rms_norm_grad."""
+    n = Norm(None, int(rows), int(hidden), EP_DTYPE_BF16, 0.0, 0)
+    return int(_lib.ep_rms_norm_grad_bytes(ctypes.byref(n)))
+
+
+def rms_norm_grad(dy, h, weight, eps: float, dx, dweight=None, ws=None, dsum=None,
+                  stream=None) -> None:
+    """Backward pass of rms_norm: dx from dy, the normed rows h [..., hidden] and dsum, the gradient
+    that reaches h past the norm (dx may be dsum); float32 dweight."""
+    hidden, t = h.shape[-1], h.dtype
+    n = h.numel() // hidden if hidden else 0
+    need = 2 * n * hidden
+    p = _norm(n, hidden, weight, t, eps)
+    room = rms_norm_grad_bytes(n, hidden) if dweight is not None else 0
+    _check(_lib.ep_rms_norm_grad(
+        ctypes.byref(p), _dense(dy, need, "dy", t), _addr(h), _dense(dsum, need, "dsum", t),
+        _dense(dx, need, "dx", t), _dense(dweight, 4 * hidden, "dweight", _torch.float32),
+        _room(ws, room), _stream(stream)), "ep_rms_norm_grad")
+
+
+def make_product(w, act: int = EP_ACT_NONE, w_scale=None, bias=None) -> Product:
+    """The experts' matrices from w [E, W, in] (bfloat16; or float8_e4m3fn with a float32 w_scale
+    [E, W / 128, in / 128]) and a bfloat16 bias [E, W]. W is the product's out, or twice that for
+    EP_ACT_SWIGLU: the gate's rows, then the up rows."""
+    if w.dim() != 3 or w.dtype not in (_BF16, _torch.float8_e4m3fn):
+        raise ValueError(f"w is {w.dtype} {tuple(w.shape)}: bfloat16 or float8_e4m3fn [E, W, in] taken")
+    e, rows, inn = w.shape
+    if act == EP_ACT_SWIGLU and rows % 2:
+        raise ValueError("EP_ACT_SWIGLU needs an even number of weight rows")
+    if (w_scale is None) != (w.dtype == _BF16):
+        raise ValueError("w_scale belongs to float8_e4m3fn weights")
+    if w_scale is not None and (w_scale.dtype != _torch.float32 or
+                                w_scale.shape != (e, rows // 128, inn // 128)):
+        raise ValueError(f"w_scale must be float32 [{e}, {rows // 128}, {inn // 128}]")
+    if bias is not None and (bias.dtype != _BF16 or bias.shape != (e, rows)):
+        raise ValueError(f"bias must be bfloat16 [{e}, {rows}]")
+    p = Product(_addr(w), _addr(w_scale), _addr(bias), inn, rows // 2 if act == EP_ACT_SWIGLU else rows,
+                int(act), _dtype(w, "w"))
+    p.tensors = (w, w_scale, bias)
+    p.rows = rows
+    return p
+
+
+def _product_rows(d: Desc, p: Product) -> int:
+    """Rows of the grouped buffers; the experts of descriptor and weights must be the same."""
+    if p.tensors[0].shape[0] != d.n_experts:
+        raise ValueError(f"w has {p.tensors[0].shape[0]} experts, the descriptor {d.n_experts}")
+    return d.n_ranks * max(capacity(d), 0)
+
+
+def expert_product(d: Desc, p: Product, x: Sequence, plan_ws, out, residual=None, pre=None,
+                   stream=None) -> None:
+    """out = act(x w^T + bias) + residual for the grouped rows of every expert; pre receives
+    x w^T + bias for the backward pass. x: the grouped planes. plan_ws None: one dense product per
+    rank, over all its capacity rows."""
+    n = _product_rows(d, p)
+    planes = list(x) + [None] * (2 - len(x))
+    if p.dtype == EP_DTYPE_E4M3:
+        px = (_dense(planes[0], n * p.inn, "x", _torch.float8_e4m3fn, *_RAW),
+              _dense(planes[1], n * p.inn // 32, "x scales", _torch.float32, *_RAW))
+    else:
+        px = _dense(planes[0], 2 * n * p.inn, "x", _BF16, *_RAW), _addr(planes[1])
+    wide = 2 * n * p.out
+    _check(_lib.ep_expert_product(
+        ctypes.byref(d), ctypes.byref(p), (ctypes.c_void_p * 2)(*px), _addr(plan_ws),
+        _dense(residual, wide, "residual", _BF16, *_RAW),
+        _dense(pre, 2 * n * p.rows, "pre", _BF16, *_RAW), _dense(out, wide, "out", _BF16, *_RAW),
+        _stream(stream)), "ep_expert_product")
+
+
+def expert_product_grad_bytes(d: Desc, p: Product) -> int:
+    """Workspace bytes of expert_product_grad."""
+    return int(_lib.ep_expert_product_grad_bytes(ctypes.byref(d), ctypes.byref(p)))
+
+
+def expert_product_grad(d: Desc, p: Product, dout, x, pre, plan_ws, ws, dx=None, dw=None,
+                        dbias=None, stream=None) -> None:
+    """Backward pass of a bfloat16 expert_product: gradients of the grouped rows, of the weights and
+    (float32) of the bias, each None if not wanted. pre: as the forward call wrote it; None without
+    an activation."""
+    n = _product_rows(d, p)
+    e = d.n_experts
+    _check(_lib.ep_expert_product_grad(
+        ctypes.byref(d), ctypes.byref(p), _dense(dout, 2 * n * p.out, "dout", _BF16, *_RAW),
+        _dense(x, 2 * n * p.inn, "x", _BF16, *_RAW),
+        _dense(pre, 2 * n * p.rows, "pre", _BF16, *_RAW), _addr(plan_ws),
+        _room(ws, expert_product_grad_bytes(d, p)), _dense(dx, 2 * n * p.inn, "dx", _BF16, *_RAW),
+        _dense(dw, 2 * e * p.rows * p.inn, "dw", _BF16, *_RAW),
+        _dense(dbias, 4 * e * p.rows, "dbias", _torch.float32), _stream(stream)),
+        "ep_expert_product_grad")
+
+
+def combine_grad(d: Desc, dout, y, weights, plan_ws, dy=None, dweights=None, stream=None) -> None:
+    """Backward pass of combine: dy, the gradient of the expert rows y that were combined, and
+    float32 dweights [N, T, R]."""
+    rows, slots = d.n_ranks * max(capacity(d), 0), d.n_ranks * d.tokens * d.topk
+    _check(_lib.ep_combine_grad(
+        ctypes.byref(d), _dense(dout, 2 * d.n_ranks * d.tokens * d.hidden, "dout", _BF16, *_RAW),
+        _dense(y, 2 * rows * d.hidden, "y", _BF16, *_RAW),
+        _dense(weights, 4 * slots, "weights", _torch.float32), _addr(plan_ws),
+        _dense(dy, 2 * rows * d.hidden, "dy", _BF16, *_RAW),
+        _dense(dweights, 4 * slots, "dweights", _torch.float32), _stream(stream)),
+        "ep_combine_grad")
+
+
+def dispatch_grad(d: Desc, dgrouped, plan_ws, dx, add=None, stream=None) -> None:
+    """Backward pass of a dispatch of bfloat16 rows: dx sums the gradients of a token's grouped rows,
+    and add, which reaches the token past the experts (dx may be add)."""
+    rows, need = d.n_ranks * max(capacity(d), 0), 2 * d.n_ranks * d.tokens * d.hidden
+    _check(_lib.ep_dispatch_grad(
+        ctypes.byref(d), _dense(dgrouped, 2 * rows * d.hidden, "dgrouped", _BF16, *_RAW),
+        _dense(add, need, "add", _BF16, *_RAW), _addr(plan_ws),
+        _dense(dx, need, "dx", _BF16, *_RAW), _stream(stream)), "ep_dispatch_grad")
 
 
 # ---------------------------------------------------------------------------

@@ -159,6 +159,40 @@ hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                             int max_new, const ep_rows& q, int n_heads, const ep_rows& out,
                             float* lse, float sm_scale, void* ws, int32_t* status,
                             hipStream_t stream);
+// RMS norm. Threads of the workgroup that holds a row of `hidden` values, and
+// workgroups (each with its own partial dweight row) of the backward pass.
+int norm_threads(int hidden);
+int norm_grad_parts(const ep_norm& n);
+hipError_t launch_rms_norm(const ep_norm& n, const void* x, const void* residual, void* sum,
+                           void* y, uint8_t* codes, float* scales, hipStream_t stream);
+hipError_t launch_rms_norm_grad(const ep_norm& n, const void* dy, const void* h, const void* dsum,
+                                void* dx, float* dweight, float* parts, hipStream_t stream);
+// Rows of the experts' groups: expert e = d L + j owns rows [off[d][j],
+// off[d][j + 1]) of rank d's cap rows (each offset cut at cap), or with off
+// null all of them (L is 1). most: no more rows than this in all.
+struct Groups {
+  const int32_t* off;  // [N][L + 1]
+  int N, L;
+  int64_t cap, most;
+};
+inline int64_t weight_rows(const ep_product& p) {
+  return p.act == EP_ACT_SWIGLU ? 2 * (int64_t)p.out : p.out;
+}
+// Whether every launch of the product's two directions stays inside a grid.
+bool product_fits(const ep_product& p, const Dims& d);
+hipError_t launch_product(const ep_product& p, const Groups& g, const void* const x[2],
+                          const void* residual, void* pre, void* out, hipStream_t stream);
+int64_t product_grad_bytes(const ep_product& p, const Dims& d);
+hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups& g,
+                               const uint16_t* dout, const uint16_t* x, const uint16_t* pre,
+                               void* ws, uint16_t* dx, uint16_t* dw, float* dbias,
+                               hipStream_t stream);
+// Backward passes of combine and dispatch.
+hipError_t launch_combine_grad(const Dims& d, const uint16_t* dout, const uint16_t* y,
+                               const float* w, const PlanPtrs& p, uint16_t* dy, float* dweights,
+                               hipStream_t stream);
+hipError_t launch_dispatch_grad(const Dims& d, const uint16_t* dgrouped, const uint16_t* add,
+                                const PlanPtrs& p, uint16_t* dx, hipStream_t stream);
 hipError_t launch_probe_copy(void* dst, const void* src, size_t bytes,
                              hipStream_t stream);
 

@@ -1,0 +1,307 @@
+// RMS norm with the residual's addition, its output as rows and as the planes
+// of a block-fp8 dispatch, and its backward pass.
+//
+// Forward: h = x + residual rounded to the rows' type, y = h w r with
+// r = 1 / sqrt(mean(h^2) + eps). Backward, with g = dy w:
+// dx = dsum + r (g - h r^2 mean(g h)), dw = sum over rows of dy h r.
+// HBM bounds both: every value is read once and written once, so a row stays
+// in registers between its statistics and its output, and the backward pass
+// forms r anew from the row it holds anyway instead of reading it.
+//
+// One workgroup per row, 8 values (16 bytes) per lane and chunk, V chunks per
+// thread; the 16 lanes of a DPP row hold one 128-value block of the codes.
+#include "ep_device.hpp"
+#include "ep_kernels.hpp"
+#include "ep_quant_device.hpp"
+
+namespace ep {
+namespace {
+
+constexpr int kMaxWaves = 16;  // of a workgroup
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+template <int DT>
+__device__ __forceinline__ void unpack(const u32x4& r, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (DT == EP_DTYPE_BF16) {
+      v[2 * i] = bf16_lo(r[i]);
+      v[2 * i + 1] = bf16_hi(r[i]);
+    } else {
+      const f16x2 h = __builtin_bit_cast(f16x2, (uint32_t)r[i]);
+      v[2 * i] = (float)h[0];
+      v[2 * i + 1] = (float)h[1];
+    }
+  }
+}
+
+// Rounded to nearest even, both types.
+template <int DT>
+__device__ __forceinline__ u32x4 pack(const float (&v)[8]) {
+  u32x4 r;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const f32x2 f = {v[2 * i], v[2 * i + 1]};
+    if constexpr (DT == EP_DTYPE_BF16)
+      r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, bf16x2));
+    else
+      r[i] = __builtin_bit_cast(uint32_t, __builtin_convertvector(f, f16x2));
+  }
+  return r;
+}
+
+__device__ __forceinline__ float wave_sum(float v) {
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) v += __shfl_xor(v, off);
+  return v;
+}
+
+// Sums of N values over the workgroup, in the same order in every run. `room`
+// is free again once every thread has passed the next barrier.
+template <int N>
+__device__ __forceinline__ void block_sum(float (&v)[N], float (*room)[N]) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+  const int waves = blockDim.x / kWave;
+  if (waves == 1) return;
+  if (lane_id() == 0)
+#pragma unroll
+    for (int i = 0; i < N; ++i) room[threadIdx.x / kWave][i] = v[i];
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  for (int w = 0; w < waves; ++w)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += room[w][i];
+}
+
+template <int DT, int V, bool QUANT>
+__global__ __launch_bounds__(1024) void norm_kernel(const u32x4* x, const u32x4* residual,
+                                                    const u32x4* weight, u32x4* sum, u32x4* y,
+                                                    uint2* codes, float* scales, int n16,
+                                                    float per, float eps) {
+  __shared__ float room[kMaxWaves][1];
+  const size_t row = (size_t)blockIdx.x * n16;
+  u32x4 raw[V], res[V], wt[V];
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    raw[i] = res[i] = wt[i] = u32x4{0, 0, 0, 0};
+    if (c < n16) {
+      raw[i] = load_stream(&x[row + c]);
+      if (residual) res[i] = load_stream(&residual[row + c]);
+      wt[i] = weight[c];
+    }
+  }
+  float h[V][8], ss[1] = {0.0f};
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    unpack<DT>(raw[i], h[i]);
+    if (residual) {
+      float b[8];
+      unpack<DT>(res[i], b);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[i][j] += b[j];
+      // The stream keeps the rounded sum, and its norm is what the next layers
+      // and the backward pass see.
+      const u32x4 s = pack<DT>(h[i]);
+      if (c < n16) store_stream(&sum[row + c], s);
+      unpack<DT>(s, h[i]);
+    }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) ss[0] = __builtin_fmaf(h[i][j], h[i][j], ss[0]);
+  }
+  block_sum(ss, room);
+  const float r = rsqrtf(ss[0] * per + eps);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    float w[8];
+    unpack<DT>(wt[i], w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) w[j] *= h[i][j] * r;
+    if (y && c < n16) store_stream(&y[row + c], pack<DT>(w));
+    if constexpr (QUANT) {  // every lane takes part: a block's lanes are all in the row or none
+      uint32_t packed[2];
+      float scale;
+      quantise_values(w, packed, scale);
+      if (c < n16) {
+        codes[row + c] = uint2{packed[0], packed[1]};
+        if (threadIdx.x % 16 == 0) scales[(row + c) / 16] = scale;
+      }
+    }
+  }
+}
+
+// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; with AHEAD the next row's
+// values are on their way while one is worked on (registers for it are there
+// up to 512 threads). Each workgroup keeps its part of dweight in registers
+// and writes it once: sums in a fixed order, without atomics.
+template <int DT, int V, int THREADS, bool AHEAD>
+__global__ __launch_bounds__(THREADS) void norm_grad_kernel(const u32x4* dy, const u32x4* h,
+                                                         const u32x4* weight, const u32x4* dsum,
+                                                         u32x4* dx, float* parts, int64_t rows,
+                                                         int n16, float per, float eps) {
+  __shared__ float room[2][kMaxWaves][2];
+  u32x4 hn[V], dn[V], sn[V];
+  float wt[V][8], dw[V][8];
+  const auto load = [&](int64_t r) {
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      hn[i] = dn[i] = sn[i] = u32x4{0, 0, 0, 0};
+      if (c < n16 && r < rows) {
+        const size_t at = (size_t)r * n16 + c;
+        hn[i] = load_stream(&h[at]);
+        dn[i] = load_stream(&dy[at]);
+        if (dsum) sn[i] = load_stream(&dsum[at]);
+      }
+    }
+  };
+  if (AHEAD) load(blockIdx.x);
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    unpack<DT>(c < n16 ? weight[c] : u32x4{0, 0, 0, 0}, wt[i]);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
+  }
+  int turn = 0;
+  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
+    float hv[V][8], dv[V][8], s[2] = {0.0f, 0.0f};
+    u32x4 add[V];
+    if (!AHEAD) load(r);
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      unpack<DT>(hn[i], hv[i]);
+      unpack<DT>(dn[i], dv[i]);
+      add[i] = sn[i];
+    }
+    if (AHEAD) load(r + gridDim.x);
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        s[0] = __builtin_fmaf(hv[i][j], hv[i][j], s[0]);
+        s[1] = __builtin_fmaf(dv[i][j] * wt[i][j], hv[i][j], s[1]);
+      }
+    block_sum(s, room[turn]);  // two rooms in turn: one barrier per row is enough
+    const float rs = rsqrtf(s[0] * per + eps);
+    const float k = rs * rs * s[1] * per;
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int c = threadIdx.x + i * blockDim.x;
+      float o[8];
+      unpack<DT>(add[i], o);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        o[j] += rs * __builtin_fmaf(-hv[i][j], k, dv[i][j] * wt[i][j]);
+        dw[i][j] = __builtin_fmaf(dv[i][j], hv[i][j] * rs, dw[i][j]);
+      }
+      if (c < n16) store_stream(&dx[(size_t)r * n16 + c], pack<DT>(o));
+    }
+  }
+  if (!parts) return;
+#pragma unroll
+  for (int i = 0; i < V; ++i) {
+    const int c = threadIdx.x + i * blockDim.x;
+    if (c >= n16) continue;
+    float4* p = (float4*)(parts + ((size_t)blockIdx.x * n16 + c) * 8);
+    p[0] = float4{dw[i][0], dw[i][1], dw[i][2], dw[i][3]};
+    p[1] = float4{dw[i][4], dw[i][5], dw[i][6], dw[i][7]};
+  }
+}
+
+// Column sums of the parts: 64 columns per workgroup, 16 waves that each take
+// every 16th part.
+__global__ __launch_bounds__(1024) void norm_weight_kernel(const float* parts, float* dweight,
+                                                           int n, int hidden) {
+  __shared__ float room[16][kWave];
+  const int lane = lane_id(), wave = threadIdx.x / kWave, col = blockIdx.x * kWave + lane;
+  float s = 0.0f;
+  if (col < hidden)
+    for (int p = wave; p < n; p += 16) s += parts[(size_t)p * hidden + col];
+  room[wave][lane] = s;
+  __syncthreads();
+  if (wave != 0 || col >= hidden) return;
+  s = 0.0f;
+#pragma unroll
+  for (int w = 0; w < 16; ++w) s += room[w][lane];
+  dweight[col] = s;
+}
+
+// Chunks per thread: two while 1024 threads hold the row, else four. Two make
+// the 896 chunks of 7168 values fill seven waves.
+int chunks_per_thread(int hidden) { return hidden / 8 <= 2048 ? 2 : 4; }
+
+template <int DT, int V>
+hipError_t run_norm(const ep_norm& n, const void* x, const void* residual, void* sum, void* y,
+                    uint8_t* codes, float* scales, hipStream_t stream) {
+  const dim3 grid((unsigned)n.rows), block(norm_threads(n.hidden));
+  const float per = 1.0f / (float)n.hidden;
+  if (codes)
+    hipLaunchKernelGGL((norm_kernel<DT, V, true>), grid, block, 0, stream, (const u32x4*)x,
+                       (const u32x4*)residual, (const u32x4*)n.weight, (u32x4*)sum, (u32x4*)y,
+                       (uint2*)codes, scales, n.hidden / 8, per, n.eps);
+  else
+    hipLaunchKernelGGL((norm_kernel<DT, V, false>), grid, block, 0, stream, (const u32x4*)x,
+                       (const u32x4*)residual, (const u32x4*)n.weight, (u32x4*)sum, (u32x4*)y,
+                       nullptr, nullptr, n.hidden / 8, per, n.eps);
+  return hipGetLastError();
+}
+
+template <int DT>
+auto grad_kernel(int hidden) {
+  if (chunks_per_thread(hidden) == 4) return norm_grad_kernel<DT, 4, 1024, false>;
+  return norm_threads(hidden) > 512 ? norm_grad_kernel<DT, 2, 1024, false>
+                                    : norm_grad_kernel<DT, 2, 512, true>;
+}
+
+}  // namespace
+
+int norm_threads(int hidden) {
+  const int per_wave = kWave * chunks_per_thread(hidden);
+  return kWave * ((hidden / 8 + per_wave - 1) / per_wave);
+}
+
+// Workgroups that together fill the chip with 1024 threads per CU, a multiple
+// of its 256 CUs; no more than rows.
+int norm_grad_parts(const ep_norm& n) {
+  const int64_t most = 256 * (1024 / norm_threads(n.hidden));
+  return (int)(n.rows < most ? n.rows : most);
+}
+
+hipError_t launch_rms_norm(const ep_norm& n, const void* x, const void* residual, void* sum,
+                           void* y, uint8_t* codes, float* scales, hipStream_t stream) {
+  const auto run = n.dtype == EP_DTYPE_BF16
+                       ? (chunks_per_thread(n.hidden) == 2 ? run_norm<EP_DTYPE_BF16, 2>
+                                                           : run_norm<EP_DTYPE_BF16, 4>)
+                       : (chunks_per_thread(n.hidden) == 2 ? run_norm<EP_DTYPE_F16, 2>
+                                                           : run_norm<EP_DTYPE_F16, 4>);
+  return run(n, x, residual, sum, y, codes, scales, stream);
+}
+
+hipError_t launch_rms_norm_grad(const ep_norm& n, const void* dy, const void* h, const void* dsum,
+                                void* dx, float* dweight, float* parts, hipStream_t stream) {
+  const int blocks = norm_grad_parts(n);
+  if (blocks > 0) {
+    const auto kernel =
+        n.dtype == EP_DTYPE_BF16 ? grad_kernel<EP_DTYPE_BF16>(n.hidden) : grad_kernel<EP_DTYPE_F16>(n.hidden);
+    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(norm_threads(n.hidden)), 0, stream,
+                       (const u32x4*)dy, (const u32x4*)h, (const u32x4*)n.weight,
+                       (const u32x4*)dsum, (u32x4*)dx, dweight ? parts : nullptr, n.rows,
+                       n.hidden / 8, 1.0f / (float)n.hidden, n.eps);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || !dweight) return e;
+  }
+  if (dweight)
+    hipLaunchKernelGGL(norm_weight_kernel, dim3((n.hidden + kWave - 1) / kWave), dim3(1024), 0,
+                       stream, parts, dweight, blocks, n.hidden);
+  return hipGetLastError();
+}
+
+}  // namespace ep

@@ -683,6 +683,118 @@ EP_API int ep_combine_presum(const ep_desc *d, const uint16_t *expert_out,
                              uint16_t *partial, uint16_t *out,
                              hipStream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Around dispatch and combine in an MoE layer: the norm in front of the
+ * router and the dispatch (ep_rms_norm), the experts' products on the grouped
+ * rows (ep_expert_product) and the backward passes of all of them. Sums, norms
+ * and statistics are held in 32 bits; each output is rounded once (nearest
+ * even). Inputs and outputs may not overlap.
+ * ---------------------------------------------------------------------- */
+
+/* RMS norm of rows of `hidden` values. */
+typedef struct ep_norm {
+  const void *weight;  /* [hidden], in the rows' dtype */
+  int64_t rows;        /* at least 0, fewer than 2^31 */
+  int32_t hidden;      /* a multiple of 8, at most EP_NORM_MAX_HIDDEN */
+  int32_t dtype;       /* EP_DTYPE_BF16 or EP_DTYPE_F16, of rows and weight */
+  float eps;           /* not negative */
+  int32_t reserved;    /* 0 */
+} ep_norm;
+#define EP_NORM_MAX_HIDDEN 32768
+
+/* h = x + residual, rounded to the rows' dtype (x itself when residual is
+ * NULL), y = h weight / sqrt(mean(h^2) + eps). x, residual, sum, y:
+ * [rows][hidden]. sum (required with residual, NULL without) receives h and may
+ * be residual itself; y (or NULL) the normed rows. codes and scales (both or
+ * neither; hidden % 128 == 0) receive the same rows as the planes of a block-fp8 dispatch:
+ * codes [rows][hidden] e4m3fn, scales fp32 [rows][hidden / 128], quantised from
+ * the 32-bit values (not from the rounded y) by the rules of
+ * ep_dispatch_pack_quant. Either y or codes must be given. */
+EP_API int ep_rms_norm(const ep_norm *n, const void *x, const void *residual,
+                       void *sum, void *y, uint8_t *codes, float *scales,
+                       hipStream_t stream);
+
+/* Backward pass. h: the normed rows (sum of the forward call, or its x);
+ * dy: the gradient of y; dsum (or NULL): the gradient that reaches h
+ * past the norm. With r = 1 / sqrt(mean(h^2) + eps) and g = dy weight:
+ *   dx = dsum + r (g - h r^2 mean(g h)), the gradient of x and of residual;
+ *   dweight[j] = sum over rows of dy h r, fp32, or NULL.
+ * dx may be dsum. Deterministic. ws: ep_rms_norm_grad_bytes(n), 16-byte
+ * aligned; it holds nothing between calls (may be NULL without dweight). */
+EP_API size_t ep_rms_norm_grad_bytes(const ep_norm *n);
+EP_API int ep_rms_norm_grad(const ep_norm *n, const void *dy, const void *h,
+                            const void *dsum, void *dx, float *dweight,
+                            void *ws, hipStream_t stream);
+
+#define EP_ACT_NONE 0   /* y = z */
+#define EP_ACT_SILU 1   /* y = z / (1 + exp(-z)) */
+#define EP_ACT_GELU 2   /* y = z (1 + erf(z / sqrt(2))) / 2 */
+#define EP_ACT_SWIGLU 3 /* y[j] = silu(z[j]) z[out + j]: gate rows of w, then up rows */
+
+/* The experts' matrices. W = out, or 2 out for EP_ACT_SWIGLU. `in` and `out`
+ * are multiples of 8 (e4m3: of 128), in * W < 2^30, both below 2^20. */
+typedef struct ep_product {
+  const void *w;        /* [E][W][in] */
+  const float *w_scale; /* e4m3: fp32 [E][W / 128][in / 128]; else NULL */
+  const void *bias;     /* bf16 [E][W], or NULL */
+  int32_t in;
+  int32_t out;
+  int32_t act;          /* EP_ACT_* */
+  int32_t dtype;        /* of w and x: EP_DTYPE_BF16 or EP_DTYPE_E4M3 */
+} ep_product;
+
+/* Grouped product ("Dispatch and combine": the grouped GEMM between dispatch
+ * and combine): for every delivered row i of expert e,
+ *   z = x[i] w[e]^T + bias[e], out[i] = act(z) + residual[i].
+ * Of the descriptor only N, E and cap matter: rows have the product's own
+ * widths. x: bf16 [N][cap][in] in x[0]; or e4m3 codes in x[0] and their scales
+ * [N][cap][in / 128] in x[1], as a block-fp8 dispatch delivers them (a value is
+ * code * scale, and w's the same by blocks of 128 x 128; products of 128 codes
+ * are summed first, then scaled). out, residual: bf16
+ * [N][cap][out], residual or NULL. pre (or NULL): receives z, bf16
+ * [N][cap][W], for the backward pass. Rows that no expert owns are neither
+ * read for a result nor written. plan_ws NULL: E must be N, and all cap rows
+ * of a rank belong to its one expert (a dense product). */
+EP_API int ep_expert_product(const ep_desc *d, const ep_product *p,
+                             const void *const x[2], const void *plan_ws,
+                             const void *residual, void *pre, void *out,
+                             hipStream_t stream);
+
+/* Backward pass of a bf16 product (the residual's gradient is dout itself).
+ * dz = dout act'(pre), rounded to bf16 where it enters a product;
+ *   dx[i] = dz[i] w[e], bf16 [N][cap][in];
+ *   dw[e] = sum over e's rows of dz[i]^T x[i], bf16 [E][W][in];
+ *   dbias[e] = sum over e's rows of the 32-bit dz, fp32 [E][W].
+ * Each may be NULL, not all; x may be NULL without dw. pre: as the forward
+ * call wrote it (NULL for EP_ACT_NONE). An expert without rows gets zeros in
+ * dw and dbias. Deterministic. ws: ep_expert_product_grad_bytes(d, p), 16-byte
+ * aligned; it holds nothing between calls. plan_ws: as above. */
+EP_API size_t ep_expert_product_grad_bytes(const ep_desc *d,
+                                           const ep_product *p);
+EP_API int ep_expert_product_grad(const ep_desc *d, const ep_product *p,
+                                  const uint16_t *dout, const uint16_t *x,
+                                  const uint16_t *pre, const void *plan_ws,
+                                  void *ws, uint16_t *dx, uint16_t *dw,
+                                  float *dbias, hipStream_t stream);
+
+/* Backward pass of ep_combine. dout: bf16 [N][T][H], y and weights as the
+ * forward call's. dy: bf16 [N][cap][H], the delivered rows
+ * dy[e / L][grp_pos] = bf16(w dout[s][t]) (others are not written); dweights:
+ * fp32 [N][T][R], sum_h dout y, 0 for dropped slots. dy or dweights may be
+ * NULL, not both; y may be NULL without dweights. Deterministic. */
+EP_API int ep_combine_grad(const ep_desc *d, const uint16_t *dout,
+                           const uint16_t *y, const float *weights,
+                           const void *plan_ws, uint16_t *dy, float *dweights,
+                           hipStream_t stream);
+
+/* Backward pass of a dispatch of bf16 rows: dx[s][t] = bf16( add[s][t] +
+ * sum_k dgrouped[e_k / L][grp_pos[s][t][k]] ), in k order; bf16, dgrouped
+ * [N][cap][H]. Dropped slots contribute nothing. add (or NULL): a gradient that
+ * reaches x past the experts; dx may be add. */
+EP_API int ep_dispatch_grad(const ep_desc *d, const uint16_t *dgrouped,
+                            const uint16_t *add, const void *plan_ws,
+                            uint16_t *dx, hipStream_t stream);
+
 /* Copy `bytes` (a multiple of 16) from src to dst with the library's row
  * copy loop (non-temporal loads and stores, 7 KB per wave): a bandwidth
  * reference for measurements, not part of the method. Its non-temporal

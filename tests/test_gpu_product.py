@@ -1,0 +1,184 @@
+"""The experts' product on the GPU against the definition in 64 bits.
+
+Tolerances, from the arithmetic. z is a 32-bit sum of K exact products of
+16-bit values (or of two 8-bit ones, times a scale product that is rounded
+twice), in some order: off by e = (K + 8) 2^-23 A with A = sum |x||w| + |bias|
+(a matrix instruction may cut instead of rounding: a whole step each). An
+activation's slope is under 1.13, and its own evaluation is off by under 2^-16
+relative. SwiGLU: the error of either factor times the other. Outputs are
+rounded once: half a step of bf16."""
+import pytest
+import torch
+
+import combine_ep_plan_amd as ep
+from gpu_util import note
+from layer_ref import BF, F8, HALF, NAMES, TINY, Dense, Routed, activate, check, ids
+
+pytestmark = pytest.mark.gpu
+ACTS = [ep.EP_ACT_NONE, ep.EP_ACT_SILU, ep.EP_ACT_GELU, ep.EP_ACT_SWIGLU]
+
+
+class Case:
+    """Rows and matrices on the CPU; rows that no expert owns hold NaN."""
+
+    def __init__(self, where, experts, k, n, act, fp8=False, bias=False, residual=False, seed=0):
+        g = torch.Generator().manual_seed(seed)
+        self.where, self.k, self.n, self.act, self.fp8 = where, k, n, act, fp8
+        self.wrows = 2 * n if act == ep.EP_ACT_SWIGLU else n
+        x = torch.randn((where.rows, k), generator=g)
+        w = torch.randn((experts, self.wrows, k), generator=g)
+        if fp8:
+            self.x, self.w = (x * 100).clamp(-448, 448).to(F8), (w * 100).clamp(-448, 448).to(F8)
+            self.xs = (torch.rand((where.rows, k // 128), generator=g) + 0.5) / 100
+            self.ws = (torch.rand((experts, self.wrows // 128, k // 128), generator=g) + 0.5) / (100 * k**0.5)
+            self.x64 = self.x.double() * self.xs.double().repeat_interleave(128, 1)
+            self.w64 = self.w.double() * self.ws.double().repeat_interleave(128, 1).repeat_interleave(128, 2)
+            self.x.view(torch.uint8)[~where.owned] = 0x7F
+            self.xs[~where.owned] = float("nan")
+        else:
+            self.x, self.w = x.to(BF), (w * k**-0.5).to(BF)
+            self.x64, self.w64 = self.x.double(), self.w.double()
+            self.x[~where.owned] = float("nan")
+            self.xs = self.ws = None
+        self.bias = torch.randn((experts, self.wrows), generator=g).to(BF) if bias else None
+        self.residual = torch.randn((where.rows, n), generator=g).to(BF) if residual else None
+
+    def run(self, pre=False, stream=None):
+        """Outputs, after a row of 7 in front of and behind them that must stay."""
+        c, dev = self.where, "cuda"
+        p = ep.make_product(self.w.to(dev), self.act, w_scale=None if self.ws is None else self.ws.to(dev),
+                            bias=None if self.bias is None else self.bias.to(dev))
+        x = [self.x.to(dev)] + ([] if self.xs is None else [self.xs.to(dev)])
+        out = torch.full((c.rows + 2, self.n), 7.0, dtype=BF, device=dev)
+        z = torch.full((c.rows + 2, self.wrows), 7.0, dtype=BF, device=dev) if pre else None
+        ep.expert_product(c.desc, p, x, c.plan, out[1:-1], residual=None if self.residual is None else
+                          self.residual.to(dev), pre=None if z is None else z[1:-1], stream=stream)
+        torch.cuda.synchronize()
+        for t in (out, z):
+            if t is not None:
+                assert (t[0] == 7).all() and (t[-1] == 7).all() and (t[1:-1][~c.owned.to(dev)] == 7).all()
+        return out[1:-1].cpu(), None if z is None else z[1:-1].cpu()
+
+    def expect(self):
+        """z, out and their tolerances, rows of experts only."""
+        c = self.where
+        z = torch.zeros((c.rows, self.wrows), dtype=torch.float64)
+        tz = torch.zeros_like(z)
+        for e, (a, m) in enumerate(c.groups):
+            b = 0 if self.bias is None else self.bias[e].double()
+            z[a:a + m] = self.x64[a:a + m] @ self.w64[e].T + b
+            tz[a:a + m] = (self.x64[a:a + m].abs() @ self.w64[e].abs().T + (b if self.bias is None else b.abs())) * \
+                (self.k + 8) * 2.0**-23
+        y = activate(z, self.act)
+        if self.act == ep.EP_ACT_SWIGLU:
+            gate, up = z.chunk(2, -1)
+            tg, tu = tz.chunk(2, -1)
+            s = activate(gate, ep.EP_ACT_SILU)
+            ty = 1.13 * tg * (up.abs() + tu) + s.abs() * tu + y.abs() * 2.0**-16
+        else:
+            ty = 1.13 * tz + y.abs() * 2.0**-16
+        if self.residual is not None:
+            y = y + self.residual.double()
+            ty = ty + (y.abs() + self.residual.double().abs()) * 2.0**-24
+        return z, tz + HALF[BF] * (z.abs() + tz) + TINY[BF], y, ty + HALF[BF] * (y.abs() + ty) + TINY[BF]
+
+    def check(self, pre=False):
+        out, z = self.run(pre)
+        wz, tz, wy, ty = self.expect()
+        o = self.where.owned
+        check(out[o], wy[o], ty[o], "out")
+        if pre:
+            check(z[o], wz[o], tz[o], "pre")
+
+
+def routed(n, t, e, r, seed=0, cap=0, only=None):
+    return Routed(n, t, e, r, ids(n, t, e, r, seed, only), cap=cap)
+
+
+@pytest.mark.parametrize("act", ACTS, ids=NAMES.get)
+@pytest.mark.parametrize("n,t,e,r,k,m", [
+    (1, 1, 4, 1, 8, 8),           # one row, one chunk of k
+    (1, 1, 8, 3, 72, 40),         # single rows of several experts
+    (4, 16, 16, 2, 256, 512),     # the tiny workload
+    (2, 37, 6, 2, 520, 264),      # odd sizes, k and columns that end inside a tile
+    (1, 150, 4, 1, 136, 72),      # about 37 rows an expert
+    (1, 515, 3, 2, 200, 104),     # several row blocks an expert
+])
+def test_product(n, t, e, r, k, m, act):
+    note(f"product {n} {t} {e} {r} {k} {m} {NAMES[act]}")
+    Case(routed(n, t, e, r), e, k, m, act, bias=True, residual=True).check(pre=True)
+
+
+@pytest.mark.parametrize("act", ACTS, ids=NAMES.get)
+@pytest.mark.parametrize("n,t,e,r,k,m", [(1, 1, 4, 2, 128, 128), (2, 40, 4, 2, 384, 256), (1, 60, 2, 1, 256, 384),
+                                         (1, 300, 3, 2, 640, 128), (1, 700, 2, 1, 128, 512)])
+def test_product_of_codes(n, t, e, r, k, m, act):
+    note(f"product fp8 {n} {t} {e} {r} {k} {m} {NAMES[act]}")
+    Case(routed(n, t, e, r), e, k, m, act, fp8=True, bias=True, residual=True).check(pre=True)
+
+
+@pytest.mark.parametrize("bias,residual,pre", [(False, False, False), (True, False, False), (False, True, False),
+                                               (False, False, True)])
+@pytest.mark.parametrize("fp8", [False, True])
+def test_product_options(bias, residual, pre, fp8):
+    note(f"product options {bias} {residual} {pre} {fp8}")
+    Case(routed(1, 90, 4, 2), 4, 256, 128, ep.EP_ACT_SWIGLU, fp8, bias, residual).check(pre)
+
+
+@pytest.mark.parametrize("fp8", [False, True])
+def test_product_empty_experts_and_capacity(fp8):
+    """Experts without rows, at the front, between and at the end; rows past the capacity are not there."""
+    note(f"product empty experts {fp8}")
+    Case(routed(1, 50, 12, 2, only=[3, 4, 9]), 12, 128, 128, ep.EP_ACT_SILU, fp8).check()
+    Case(routed(2, 64, 4, 2, cap=50), 4, 128, 128, ep.EP_ACT_NONE, fp8).check()
+    Case(routed(1, 1, 2048, 5), 2048, 128, 128, ep.EP_ACT_NONE, fp8).check()
+
+
+def test_product_bad_ids_and_no_tokens():
+    idx = ids(2, 20, 4, 2, 3)
+    idx[0, 3, 1], idx[1, 7, 0] = -5, 9
+    Case(Routed(2, 20, 4, 2, idx), 4, 64, 64, ep.EP_ACT_NONE).check()
+    idx[:] = 4
+    Case(Routed(2, 20, 4, 2, idx), 4, 64, 64, ep.EP_ACT_NONE).check()      # every slot is dropped
+    Case(Routed(2, 0, 4, 2, idx[:, :0], cap=3), 4, 64, 64, ep.EP_ACT_NONE).check()
+
+
+@pytest.mark.parametrize("n,rows,k,m,act", [(1, 1, 520, 264, ep.EP_ACT_GELU), (1, 33, 72, 520, ep.EP_ACT_SWIGLU),
+                                            (3, 70, 264, 40, ep.EP_ACT_SILU), (2, 300, 128, 136, ep.EP_ACT_NONE)])
+def test_dense_product(n, rows, k, m, act):
+    note(f"dense {n} {rows} {k} {m}")
+    Case(Dense(n, rows), n, k, m, act, bias=True, residual=True).check(pre=True)
+
+
+def test_product_special_values_stay_in_their_row():
+    """Infinities and NaN of a row or of a weight row reach only what the definition gives them to; a NaN behind the
+    last k, in the next row, reaches nothing."""
+    note("product special values")
+    for k in (72, 64):
+        c = Case(routed(1, 40, 3, 1), 3, k, 72, ep.EP_ACT_NONE)
+        plain, _ = c.run()
+        rows = c.where.owned.nonzero().flatten().tolist()
+        c.x[rows[5], 3], c.x[rows[7], 0] = float("nan"), float("inf")
+        c.w[1, 9, k - 1] = float("nan")
+        out, _ = c.run()
+        keep = c.where.owned.clone()
+        keep[rows[5]] = keep[rows[7]] = False
+        cols = torch.ones(72, dtype=torch.bool)
+        cols[9] = False
+        assert torch.equal(out[keep][:, cols], plain[keep][:, cols])
+        assert out[rows[5]].isnan().all()
+        a, m = c.where.groups[1]
+        assert out[a:a + m, 9].isnan().all()
+
+
+def test_product_large_gates():
+    """Activations far out: no overflow of the exponential where the definition has a value."""
+    c = Case(routed(1, 40, 2, 1), 2, 64, 64, ep.EP_ACT_SWIGLU)
+    c.w = (c.w.float() * 300).to(BF)
+    c.w64 = c.w.double()
+    c.check(pre=True)
+    for act in (ep.EP_ACT_SILU, ep.EP_ACT_GELU):
+        c = Case(routed(1, 40, 2, 1), 2, 64, 64, act)
+        c.w = (c.w.float() * 6).to(BF)
+        c.w64 = c.w.double()
+        c.check()
