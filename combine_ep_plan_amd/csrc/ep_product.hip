@@ -34,7 +34,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
   *(uint2*)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Fragments of a SwiGLU tile alternate: 32 gate rows of w, the 32 up rows of
+// Fragments of a SwiGLU tile alternate: 16 gate rows of w, the 16 up rows of
 // the same columns; a lane then holds both of a column.
 template <typename S, int ACT>
 __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
@@ -48,7 +48,7 @@ __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
   const uint8_t* w = a.w + (int64_t)t.expert * wrows * line;
   // Weight row of row r of the tile, beside the tile's first.
   const auto w_row = [&](int r) {
-    return glu ? r / 64 * 32 + r % 32 + (r & 32 ? a.n : 0) : r;
+    return glu ? r / 32 * 16 + r % 16 + (r & 16 ? a.n : 0) : r;
   };
   Pair p;
   p.r = a.x + (int64_t)t.first * line;
@@ -56,6 +56,8 @@ __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
   p.r_size = t.rows * line;
   p.c_size = (int64_t)(wrows - c0) * line;
   p.r_step = p.c_step = kStep;
+  p.r_line = p.c_line = (uint32_t)line;
+  p.turn = t.col % 8;
   p.k_bytes = line;
   p.rs = p.cs = nullptr;
   p.rs_size = p.cs_size = 0;
@@ -71,41 +73,37 @@ __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
       p, lds_base(lds), [&](int r) { return (uint32_t)(r * line); },
       [&](int r) { return (uint32_t)(w_row(r) * line); },
       [&](int r) { return (uint32_t)(r * kb * 4); },
-      [&](int f) { return (uint32_t)((c0 + w_row(f * 32)) / 128 * kb * 4); });
-  const int lane = lane_id(), half = lane / 32;
+      [&](int wc, int f) { return (uint32_t)((c0 + w_row((wc * S::FC + f) * kFrag)) / 128 * kb * 4); });
+  const int lane = lane_id();
   const uint16_t* bias = a.bias ? a.bias + (int64_t)t.expert * wrows : nullptr;
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
-    const int r = (tile.wr * S::FR + i) * 32 + lane % 32;
+    const int r = (tile.wr * S::FR + i) * kFrag + lane % 16;
     if (r >= t.rows) continue;
     const int64_t row = t.first + r;
 #pragma unroll
     for (int j = 0; j < S::FC; j += glu ? 2 : 1) {
-      const int f = tile.wc * S::FC + j;
+      const int f = tile.wc * S::FC + j, c = c0 + (glu ? f / 2 : f) * kFrag + lane / 16 * 4;
+      if (c >= a.n) continue;
+      float z[4], y[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = c0 + (glu ? f / 2 : f) * 32 + 8 * q + 4 * half;
-        if (c >= a.n) continue;
-        float z[4], y[4];
+      for (int v = 0; v < 4; ++v) z[v] = tile.acc[i][j][v];
+      if (bias) add4(z, bias + c);
+      if (a.pre) store4(a.pre + row * wrows + c, z);
+      if constexpr (glu) {
+        float up[4];
 #pragma unroll
-        for (int v = 0; v < 4; ++v) z[v] = tile.acc[i][j][4 * q + v];
-        if (bias) add4(z, bias + c);
-        if (a.pre) store4(a.pre + row * wrows + c, z);
-        if constexpr (glu) {
-          float up[4];
+        for (int v = 0; v < 4; ++v) up[v] = tile.acc[i][j + 1][v];
+        if (bias) add4(up, bias + a.n + c);
+        if (a.pre) store4(a.pre + row * wrows + a.n + c, up);
 #pragma unroll
-          for (int v = 0; v < 4; ++v) up[v] = tile.acc[i][j + 1][4 * q + v];
-          if (bias) add4(up, bias + a.n + c);
-          if (a.pre) store4(a.pre + row * wrows + a.n + c, up);
+        for (int v = 0; v < 4; ++v) y[v] = activate<EP_ACT_SILU>(z[v]) * up[v];
+      } else {
 #pragma unroll
-          for (int v = 0; v < 4; ++v) y[v] = activate<EP_ACT_SILU>(z[v]) * up[v];
-        } else {
-#pragma unroll
-          for (int v = 0; v < 4; ++v) y[v] = activate<ACT>(z[v]);
-        }
-        if (a.residual) add4(y, a.residual + row * a.n + c);
-        store4(a.out + row * a.n + c, y);
+        for (int v = 0; v < 4; ++v) y[v] = activate<ACT>(z[v]);
       }
+      if (a.residual) add4(y, a.residual + row * a.n + c);
+      store4(a.out + row * a.n + c, y);
     }
   }
 }
@@ -126,9 +124,9 @@ hipError_t run(FwdArgs a, int act, hipStream_t stream) {
 template <bool FP8>
 hipError_t by_rows(const FwdArgs& a, int act, hipStream_t stream) {
   const int64_t mean = a.g.most / (a.g.N * a.g.L);
-  if (mean <= 24) return run<Shape<1, 1, 2, 2, false, false, FP8, 4>>(a, act, stream);
-  if (mean <= 48) return run<Shape<1, 2, 4, 2, false, false, FP8, 3>>(a, act, stream);
-  return run<Shape<2, 4, 4, 2, false, false, FP8, 2>>(a, act, stream);
+  if (mean <= 24) return run<Shape<1, 2, 2, 4, false, false, FP8, 4>>(a, act, stream);
+  if (mean <= 48) return run<Shape<1, 4, 4, 4, false, false, FP8, 3>>(a, act, stream);
+  return run<Shape<2, 8, 4, 4, false, false, FP8, 2>>(a, act, stream);
 }
 
 }  // namespace

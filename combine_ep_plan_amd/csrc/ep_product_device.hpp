@@ -3,17 +3,19 @@
 //
 // A workgroup computes C[r][c] = sum_k R[r][k] Cc[c][k] for BR rows (r) and BC
 // columns (c). Both operands go to LDS with copies that pass through no
-// registers, 128 bytes of k a step (64 bf16 or 128 e4m3), STAGES steps in
-// turn. An operand lies in memory either with k dense (rows of 128 bytes in
-// LDS) or with k as its slow axis (64 rows of B values in LDS, read with the
-// transposing LDS reads). The 32x32 matrix products are laid out so that a
-// lane holds one row r (lane % 32) and four neighbouring columns c at a time:
-// register i is column 8 (i / 4) + 4 (lane / 32) + i % 4 of its 32.
+// registers, 128 bytes of k a step, `stages` steps on their way. An operand
+// lies in memory either with k dense (rows of 128 bytes in LDS) or with k as
+// its slow axis (64 rows of B values in LDS, read with the transposing LDS
+// reads). The 16x16 matrix products are laid out so that a lane holds one row
+// r (lane % 16) and four neighbouring columns c: register i of a fragment is
+// column 4 (lane / 16) + i of its 16.
 //
 // Reads past an operand's end give zeros (the buffer's bounds), so k may end
 // inside a step. Rows and columns past the end of the tile's group or matrix
 // compute what nothing stores.
 #pragma once
+
+#include <utility>
 
 #include "ep_device.hpp"
 #include "ep_kernels.hpp"
@@ -26,10 +28,11 @@ typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 typedef float f32x2 __attribute__((ext_vector_type(2)));
-typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kStep = 128;     // bytes of k in a step
+constexpr int kFrag = 16;      // rows or columns of a fragment
 constexpr uint32_t kNowhere = 0x80000000u;  // an offset past every buffer's end
 
 __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // nearest even
@@ -68,6 +71,25 @@ __device__ __forceinline__ void settle() {
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
+// f(0), ..., f(N - 1) with compile-time numbers: loops of several hundred
+// products and reads whose registers must have fixed names.
+template <int... I, typename F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F&& f) {
+  (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, typename F>
+__device__ __forceinline__ void each(F&& f) {
+  each_of(std::make_integer_sequence<int, N>{}, f);
+}
+
+// f(q) for those of n things that stand at slot m when they are spread over
+// `slots` slots: q slots / n rounded down is m.
+template <int N, int SLOTS, int M, typename F>
+__device__ __forceinline__ void spread(F&& f) {
+  constexpr int from = (M * N + SLOTS - 1) / SLOTS, to = ((M + 1) * N + SLOTS - 1) / SLOTS;
+  each<to - from>([&](auto i) { f(std::integral_constant<int, from + decltype(i)::value>{}); });
+}
+
 template <typename V>
 __device__ __forceinline__ V read_lds(uint32_t at) {
   typedef V __attribute__((address_space(3))) lds_v;
@@ -80,76 +102,75 @@ struct Operand {
   static constexpr int copies = B * kStep / 1024 / WAVES;  // per wave and step
   static_assert(copies * WAVES * 1024 == B * kStep, "whole copies");
   static constexpr int row = T ? B * 2 : kStep;            // bytes in LDS
-  uint32_t at[copies];
+  static constexpr int rows = 1024 / row;                  // of a copy
+  static_assert(!T || (B % 128 == 0 && rows >= 1 && (copies & (copies - 1)) == 0),
+                "the places of a slow-k tile's chunks are by bits of the row");
 
-  // 16-byte chunks are stored at places that make the reads of a wave meet
-  // all banks: eight rows of a dense-k tile, four of a slow-k one.
-  static __device__ __forceinline__ int place(int r, int chunk) {
-    if constexpr (!T) return chunk ^ (r & 7);
-    else if constexpr (B % 128 == 0) return chunk ^ ((r & 3) << 2);
-    else return chunk ^ ((r >> 1 & 1) << 2);
+  // 16-byte chunks of row r are stored at their number ^ turn(r): places that
+  // make the reads of a wave meet all banks (they take eight rows of a dense-k
+  // tile at a time, rows 0-3 and 8-11 of 16 of a slow-k one).
+  static __device__ __forceinline__ constexpr int turn(int r) {
+    return T ? ((r & 3) | (r >> 1 & 4)) << 1 : r & 7;
   }
 
-  // Offsets of this lane's chunks; row_at(r): byte offset of row r of the tile
-  // (dense k) or of row r of k (slow k).
+  uint32_t lane_row, lane_chunk;  // of the lane's chunk in a copy, in bytes
+  uint32_t copy_at[copies];       // of the copies' first rows, the same for all lanes
+
+  // row_at(r): byte offset of row r of the tile (dense k) or of row r of k
+  // (slow k); `line`: from one row to the next inside a copy.
   template <typename F>
-  __device__ __forceinline__ void init(F&& row_at) {
-    const int wave = threadIdx.x / kWave, lane = lane_id();
+  __device__ __forceinline__ void init(F&& row_at, uint32_t line) {
+    const int first = wave_uniform(threadIdx.x / kWave) * copies * rows;
+    const int lane = lane_id(), r = lane * 16 / row, chunk = lane * 16 % row / 16;
+    lane_row = r * line;
+    lane_chunk = (chunk ^ turn(first + r)) * 16;
 #pragma unroll
-    for (int i = 0; i < copies; ++i) {
-      const int byte = (wave * copies + i) * 1024 + lane * 16;
-      const int r = byte / row, chunk = place(r, byte % row / 16);
-      at[i] = row_at(r) + chunk * 16;
-    }
+    for (int i = 0; i < copies; ++i) copy_at[i] = wave_uniform(row_at(first + i * rows));
   }
 
-  // tail: bytes of k that are left, in a dense-k tile's last step.
-  __device__ __forceinline__ void load(const u32x4& from, uint32_t to, int tail) const {
-    const int wave = wave_uniform(threadIdx.x / kWave), lane = lane_id();
-#pragma unroll
-    for (int i = 0; i < copies; ++i) {
-      uint32_t a = at[i];
-      if (!T && tail < kStep) {
-        const int byte = (wave * copies + i) * 1024 + lane * 16;
-        if (place(byte / row, byte % row / 16) * 16 >= tail) a = kNowhere;
-      }
-      copy16(from, a, to + (wave * copies + i) * 1024);
-    }
+  // Whether the lane's chunk lies before the end of k, `tail` bytes from the
+  // step's start (always, for a slow-k tile: rows behind k are behind the
+  // buffer).
+  __device__ __forceinline__ bool before(int tail) const {
+    return T || (int)lane_chunk < tail;
+  }
+
+  // Copy i of the wave's.
+  __device__ __forceinline__ void load(int i, const u32x4& from, uint32_t to, bool there) const {
+    const int wave = wave_uniform(threadIdx.x / kWave);
+    const uint32_t at = lane_row + (lane_chunk ^ (turn(i * rows) * 16)) + copy_at[i];
+    copy16(from, there ? at : kNowhere, to + (wave * copies + i) * 1024);
   }
 };
 
-// Where a lane reads fragments of 32 rows: `first` is the wave's first row.
+// Where a lane reads fragments of 16 rows: `first` is the wave's first row.
 template <int B, bool T, int F>
 struct Reads {
-  uint32_t at[T ? F : 4];
+  static_assert(!T || (F & (F - 1)) == 0, "a slow-k tile's fragments are by bits");
+  uint32_t at;
 
   __device__ __forceinline__ Reads(int first) {
-    const int lane = lane_id(), half = lane / 32;
+    const int lane = lane_id(), group = lane / 16, i16 = lane % 16;
     using Op = Operand<B, T, 1>;
     if constexpr (!T) {
-#pragma unroll
-      for (int kk = 0; kk < 4; ++kk)
-        at[kk] = (first + lane % 32) * kStep + Op::place(lane, 2 * kk + half) * 16;
+      at = (first + i16) * kStep + (group ^ Op::turn(i16)) * 16;
     } else {
       // A group of 16 lanes reads 4 rows of k by 16 columns; lane i gets
       // column i of them.
-      const int i16 = lane % 16, r = 8 * half + i16 / 4;
-#pragma unroll
-      for (int f = 0; f < F; ++f)
-        at[f] = r * Op::row +
-                Op::place(r, (first / 32 + f) * 4 + lane / 16 % 2 * 2 + i16 % 4 / 2) * 16 +
-                i16 % 2 * 8;
+      const int r = 8 * group + i16 / 4;
+      at = r * Op::row + ((first / 16 * 2 + i16 % 4 / 2) ^ Op::turn(r)) * 16 + i16 % 2 * 8;
     }
   }
 
-  // Fragment f of 16 values of k (the kk-th of a step): k = 8 half + j.
+  // Fragment f of 32 values of k (the kk-th of a step): k = 8 group + j. The
+  // places of other chunks are an exclusive or away from the first one's.
   __device__ __forceinline__ s16x8 get(uint32_t base, int f, int kk) const {
     if constexpr (!T) {
-      return read_lds<s16x8>(base + at[kk] + f * 32 * kStep);
+      return read_lds<s16x8>(((base + at) ^ (kk * 64)) + f * kFrag * kStep);
     } else {
       typedef s16x4 __attribute__((address_space(3))) lds_s16x4;
       constexpr int row = Operand<B, T, 1>::row;
-      const uint32_t a = base + at[f] + kk * 16 * row;
+      const uint32_t a = ((base + at) ^ (f * 32)) + kk * 32 * row;
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)a);
       const s16x4 hi =
           __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(uintptr_t)(a + 4 * row));
@@ -157,33 +178,36 @@ struct Reads {
     }
   }
 
-  // Fragment f of 64 e4m3 values of k: 32 per lane; both operands take the
-  // same ones.
-  __device__ __forceinline__ i32x8 get8(uint32_t base, int f, int kk) const {
+  // Fragment f of a step's 128 e4m3 values of k: chunks `group` and 4 + group,
+  // which meet all banks as above. What counts is that both operands take the
+  // same values of k.
+  __device__ __forceinline__ i32x8 get8(uint32_t base, int f) const {
     static_assert(!T, "e4m3 operands have k dense");
-    const u32x4 a = read_lds<u32x4>(base + at[2 * kk] + f * 32 * kStep);
-    const u32x4 b = read_lds<u32x4>(base + at[2 * kk + 1] + f * 32 * kStep);
-    return i32x8{(int)a[0], (int)a[1], (int)a[2], (int)a[3],
-                 (int)b[0], (int)b[1], (int)b[2], (int)b[3]};
+    const uint32_t a = base + at;
+    const u32x4 x = read_lds<u32x4>(a + f * kFrag * kStep);
+    const u32x4 y = read_lds<u32x4>((a ^ 64) + f * kFrag * kStep);
+    return i32x8{(int)x[0], (int)x[1], (int)x[2], (int)x[3],
+                 (int)y[0], (int)y[1], (int)y[2], (int)y[3]};
   }
 };
 
-// WR x WC waves of FR x FC fragments of 32 x 32.
+// WR x WC waves of FR x FC fragments of 16 x 16.
 template <int WR_, int FR_, int WC_, int FC_, bool RT_, bool CT_, bool FP8_, int STAGES_>
 struct Shape {
   static constexpr int WR = WR_, FR = FR_, WC = WC_, FC = FC_, stages = STAGES_;
   static constexpr bool RT = RT_, CT = CT_, FP8 = FP8_;
-  static constexpr int BR = WR * FR * 32, BC = WC * FC * 32, waves = WR * WC;
+  static constexpr int BR = WR * FR * kFrag, BC = WC * FC * kFrag, waves = WR * WC;
   static constexpr int threads = waves * kWave;
-  // A stage: the two tiles; for e4m3 the scales of BR rows and of BC / 32
-  // fragments, and a place for what the waves without scales copy.
+  // A stage: the two tiles; for e4m3 the scales of BR rows and of the waves'
+  // two blocks of columns, and a place for what the waves without scales copy.
   static constexpr int scales_at = (BR + BC) * kStep;
   static constexpr int scale_slots = BR / kWave + (BR % kWave != 0);
   static constexpr int stage_bytes = scales_at + (FP8 ? (scale_slots + 2) * 256 : 0);
   static constexpr int lds_bytes = stage_bytes * stages;
   static constexpr int copies = Operand<BR, RT, waves>::copies + Operand<BC, CT, waves>::copies +
-                                (FP8 ? 1 : 0);
-  static_assert(!FP8 || waves >= scale_slots + 1, "one copy of scales per wave");
+                                (FP8 ? 2 : 0);  // two of scales
+  static_assert(!FP8 || waves >= scale_slots, "a wave copies the scales of 64 rows");
+  static_assert(!FP8 || FC * kFrag <= 128, "a wave's columns lie in one or two blocks of scales");
 };
 
 // What a workgroup multiplies. Sizes in bytes from the tile's first byte.
@@ -191,19 +215,32 @@ struct Pair {
   const uint8_t *r, *c;
   int64_t r_size, c_size;
   int64_t r_step, c_step;  // bytes from one step to the next
+  uint32_t r_line, c_line; // bytes from one row (of k, where it is slow) to the next
+  int turn;                // the step of k that comes first
   int64_t k_bytes;         // of k in all, as a dense-k operand counts it (2 per value when bf16)
-  // e4m3: scales of the rows, [row][k / 128], and of the fragments' blocks.
+  // e4m3: scales of the rows, [row][k / 128], and of the columns' blocks.
   const float *rs, *cs;
   int64_t rs_size, cs_size;
 };
 
 template <typename S>
 struct Tile {
-  f32x16 acc[S::FR][S::FC];
+  f32x4 acc[S::FR][S::FC];
   int wr, wc;  // the wave's place
 
-  // r_at, c_at: byte offsets of rows (see Operand); rs_at(row), cs_at(fragment):
-  // byte offsets of scales.
+  using ROperand = Operand<S::BR, S::RT, S::waves>;
+  using COperand = Operand<S::BC, S::CT, S::waves>;
+  using RReads = Reads<S::BR, S::RT, S::FR>;
+  using CReads = Reads<S::BC, S::CT, S::FC>;
+
+  // Where the copies of a step come from.
+  struct Source {
+    u32x4 r, c, rs, cs;
+    bool r_there, c_there;
+  };
+
+  // r_at, c_at: byte offsets of rows (see Operand); rs_at(row), cs_at(wave
+  // column, parity of the fragment): byte offsets of scales.
   template <typename FR_AT, typename FC_AT, typename RS_AT, typename CS_AT>
   __device__ __forceinline__ void run(const Pair& p, uint32_t lds, FR_AT&& r_at, FC_AT&& c_at,
                                       RS_AT&& rs_at, CS_AT&& cs_at) {
@@ -213,101 +250,188 @@ struct Tile {
 #pragma unroll
     for (int i = 0; i < S::FR; ++i)
 #pragma unroll
-      for (int j = 0; j < S::FC; ++j) acc[i][j] = f32x16{};
-    Operand<S::BR, S::RT, S::waves> ro;
-    Operand<S::BC, S::CT, S::waves> co;
-    ro.init(r_at);
-    co.init(c_at);
-    uint32_t scale_at = kNowhere;
-    const uint8_t* scale_base = nullptr;
-    int64_t scale_size = 0;
+      for (int j = 0; j < S::FC; ++j) acc[i][j] = f32x4{};
+    ROperand ro;
+    COperand co;
+    ro.init(r_at, p.r_line);
+    co.init(c_at, p.c_line);
+    // Waves copy the scales of 64 rows each, the first also those of the
+    // columns; the others fill a place that nothing reads.
+    uint32_t rs_lane = kNowhere, cs_lane = kNowhere;
+    const int rs_slot = wave < S::scale_slots ? wave : S::scale_slots + 1;
+    const int cs_slot = S::scale_slots + (wave == 0 ? 0 : 1);
     if constexpr (S::FP8) {
-      scale_base = wave < S::scale_slots ? (const uint8_t*)p.rs : (const uint8_t*)p.cs;
-      scale_size = wave < S::scale_slots ? p.rs_size : p.cs_size;
-      if (wave < S::scale_slots) {
-        if (wave * kWave + lane < S::BR) scale_at = rs_at(wave * kWave + lane);
-      } else if (wave == S::scale_slots && lane < S::BC / 32) {
-        scale_at = cs_at(lane);
-      }
+      if (wave * kWave + lane < S::BR) rs_lane = rs_at(wave * kWave + lane);
+      if (wave == 0 && lane < 2 * S::WC) cs_lane = cs_at(lane / 2, lane % 2);
     }
-    const Reads<S::BR, S::RT, S::FR> rr(wr * S::FR * 32);
-    const Reads<S::BC, S::CT, S::FC> cr(wc * S::FC * 32);
+    const RReads rr(wr * S::FR * kFrag);
+    const CReads cr(wc * S::FC * kFrag);
     const int steps = (int)((p.k_bytes + kStep - 1) / kStep);
+    const int first = steps > 0 ? p.turn % steps : 0;
     // Steps past the last are copied too, as zeros from an empty buffer: every
     // stage counts the same number of copies.
-    const auto start = [&](int s, uint32_t to) {
-      const bool there = s < steps;
+    Source from;
+    const auto aim = [&](int at) {
+      const bool there = at < steps;
+      const int s = at + first < steps ? at + first : at + first - steps;
       const int64_t left = p.k_bytes - (int64_t)s * kStep;
       const int tail = left < kStep ? (int)left : kStep;
-      ro.load(buffer_of(p.r + s * p.r_step, there ? p.r_size - s * p.r_step : 0), to, tail);
-      co.load(buffer_of(p.c + s * p.c_step, there ? p.c_size - s * p.c_step : 0),
-              to + S::BR * kStep, tail);
+      from.r = buffer_of(p.r + s * p.r_step, there ? p.r_size - s * p.r_step : 0);
+      from.c = buffer_of(p.c + s * p.c_step, there ? p.c_size - s * p.c_step : 0);
+      from.r_there = ro.before(tail);
+      from.c_there = co.before(tail);
       if constexpr (S::FP8) {
-        const int slot = wave <= S::scale_slots ? wave : S::scale_slots + 1;
-        copy4(buffer_of(scale_base + 4 * s, there ? scale_size - 4 * s : 0), scale_at,
-              to + S::scales_at + slot * 256);
+        from.rs = buffer_of((const uint8_t*)p.rs + 4 * s, there ? p.rs_size - 4 * s : 0);
+        from.cs = buffer_of((const uint8_t*)p.cs + 4 * s, there ? p.cs_size - 4 * s : 0);
+      }
+    };
+    const auto copy = [&](int i, uint32_t to) {
+      if (i < ROperand::copies) {
+        ro.load(i, from.r, to, from.r_there);
+      } else if (i < ROperand::copies + COperand::copies) {
+        co.load(i - ROperand::copies, from.c, to + S::BR * kStep, from.c_there);
+      } else if (i == ROperand::copies + COperand::copies) {
+        copy4(from.rs, rs_lane, to + S::scales_at + rs_slot * 256);
+      } else {
+        copy4(from.cs, cs_lane, to + S::scales_at + cs_slot * 256);
       }
     };
 #pragma unroll
-    for (int s = 0; s < S::stages - 1; ++s) start(s, lds + s * S::stage_bytes);
-    uint32_t here = lds, next = lds + (S::stages - 1) * S::stage_bytes;
-    const uint32_t end = lds + S::lds_bytes;
+    for (int s = 0; s < S::stages; ++s) {
+      aim(s);
+#pragma unroll
+      for (int i = 0; i < S::copies; ++i)
+        if (s < S::stages - 1 || i < early) copy(i, lds + s * S::stage_bytes);
+    }
+    uint32_t here = lds, last = lds + (S::stages - 1) * S::stage_bytes;
+    settle<(S::stages - 2) * S::copies + early>();
+    Fragments f;
+    fetch_first(f, here, rr, cr);
     for (int s = 0; s < steps; ++s) {
-      settle<(S::stages - 2) * S::copies>();
-      start(s + S::stages - 1, next);
-      step(here, rr, cr);
-      here = here + S::stage_bytes == end ? lds : here + S::stage_bytes;
-      next = next + S::stage_bytes == end ? lds : next + S::stage_bytes;
+      const uint32_t next =
+          here == lds + (S::stages - 1) * S::stage_bytes ? lds : here + S::stage_bytes;
+      step(f, here, next, last, rr, cr, copy, [&] { aim(s + S::stages); });
+      last = here;
+      here = next;
     }
     settle<0>();
   }
 
-  __device__ __forceinline__ void step(uint32_t base, const Reads<S::BR, S::RT, S::FR>& rr,
-                                       const Reads<S::BC, S::CT, S::FC>& cr) {
-    const uint32_t cbase = base + S::BR * kStep;
+  // Fragments on their way from LDS while the products before them run: in
+  // turn two sets of 32 values of k; for e4m3 a step's fragments of columns and
+  // in turn two of rows, with their scales.
+  struct Fragments {
+    s16x8 a[2][S::FP8 ? 1 : S::FC], b[2][S::FP8 ? 1 : S::FR];
+    i32x8 a8[S::FP8 ? S::FC : 1], b8[2];
+    float sc[2], sr[2];
+  };
+
+  // Part i of what the products of the kk-th 32 values of k need, in the order
+  // in which they need it.
+  static constexpr int parts = S::FC + S::FR;
+  __device__ __forceinline__ void fetch(Fragments& f, int i, uint32_t base, int kk,
+                                        const RReads& rr, const CReads& cr) {
+    if (i < S::FC) f.a[kk][i] = cr.get(base + S::BR * kStep, i, kk);
+    else f.b[kk][i - S::FC] = rr.get(base, i - S::FC, kk);
+  }
+  __device__ __forceinline__ void fetch_row(Fragments& f, int i, uint32_t base, const RReads& rr) {
+    f.b8[i % 2] = rr.get8(base, i);
+    f.sr[i % 2] = read_lds<float>(base + S::scales_at + ((wr * S::FR + i) * kFrag + lane_id() % 16) * 4);
+  }
+  __device__ __forceinline__ void fetch_column_scales(Fragments& f, uint32_t base) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      f.sc[j] = read_lds<float>(base + S::scales_at + S::scale_slots * 256 + (wc * 2 + j) * 4);
+  }
+
+  __device__ __forceinline__ void fetch_first(Fragments& f, uint32_t base, const RReads& rr,
+                                              const CReads& cr) {
     if constexpr (!S::FP8) {
 #pragma unroll
-      for (int kk = 0; kk < 4; ++kk) {
-        s16x8 a[S::FC], b[S::FR];
-#pragma unroll
-        for (int j = 0; j < S::FC; ++j) a[j] = cr.get(cbase, j, kk);
-#pragma unroll
-        for (int i = 0; i < S::FR; ++i) b[i] = rr.get(base, i, kk);
-#pragma unroll
-        for (int i = 0; i < S::FR; ++i)
-#pragma unroll
-          for (int j = 0; j < S::FC; ++j)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
-                __builtin_bit_cast(bf16x8, a[j]), __builtin_bit_cast(bf16x8, b[i]), acc[i][j], 0, 0,
-                0);
-      }
+      for (int i = 0; i < parts; ++i) fetch(f, i, base, 0, rr, cr);
     } else {
-      const uint32_t sbase = base + S::scales_at;
-      i32x8 a[S::FC][2];
-      float sc[S::FC];
+      fetch_row(f, 0, base, rr);
+      fetch_column_scales(f, base);
 #pragma unroll
-      for (int j = 0; j < S::FC; ++j) {
-        a[j][0] = cr.get8(cbase, j, 0);
-        a[j][1] = cr.get8(cbase, j, 1);
-        sc[j] = read_lds<float>(sbase + S::scale_slots * 256 + (wc * S::FC + j) * 4);
-      }
+      for (int j = 0; j < S::FC; ++j) f.a8[j] = cr.get8(base + S::BR * kStep, j);
+    }
+  }
+
+  // Copies of a step that start in the step before the one that they are
+  // counted in.
+  static constexpr int early = S::FP8 ? S::copies / 4 : S::copies;
+
+  // One step's products. Before its last part every wave has read the step's
+  // tiles (the last fragments are in registers) and the next step's have
+  // arrived; then copy(i, here), aimed by aim(), starts the early copies of a later
+  // step in their place. The other copies of the step before, to `last`, stand
+  // at the beginning. They are spread over the products, since a copy holds a
+  // wave up while the memory pipeline takes it.
+  template <typename F, typename A>
+  __device__ __forceinline__ void step(Fragments& f, uint32_t here, uint32_t next, uint32_t last,
+                                       const RReads& rr, const CReads& cr, F&& copy, A&& aim) {
+    constexpr int products = S::FR * S::FC;
+    if constexpr (!S::FP8) {
+      each<2>([&](auto half) {
+        constexpr int kk = half;
+        if constexpr (kk == 1) settle<(S::stages - 2) * S::copies>();
+        each<products>([&](auto product) {
+          constexpr int m = product, i = m / S::FC, j = m % S::FC;
+          // The reads before the barrier are through by then.
+          constexpr int slots = kk ? products : (3 * products + 3) / 4;
+          if constexpr (m < slots)
+            spread<parts, slots, m>([&](auto q) { fetch(f, q, kk ? next : here, 1 - kk, rr, cr); });
+          if constexpr (kk == 0 && m == slots - 1) aim();
+          if constexpr (kk == 1)
+            spread<S::copies, products, m>([&](auto q) { copy(q, here); });
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, f.a[kk][j]), __builtin_bit_cast(bf16x8, f.b[kk][i]),
+              acc[i][j], 0, 0, 0);
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+    } else {
+      // Scales of 2^0 for both operands of the matrix instruction; the blocks'
+      // own multiply its sum over 128 values of k, in 32 bits, two products
+      // later, when it is there.
+      constexpr int behind = 2, late = S::copies - early;
+      f32x4 sum[behind + 1];
+      float by[S::FR][2];
+      const auto scale = [&](auto product) {
+        constexpr int m = product, i = m / S::FC, j = m % S::FC;
 #pragma unroll
-      for (int i = 0; i < S::FR; ++i) {
-        const i32x8 b0 = rr.get8(base, i, 0), b1 = rr.get8(base, i, 1);
-        const float sr = read_lds<float>(sbase + ((wr * S::FR + i) * 32 + lane_id() % 32) * 4);
-#pragma unroll
-        for (int j = 0; j < S::FC; ++j) {
-          // Scales of 2^0 for both operands; the blocks' own multiply the sum
-          // over their 128 values of k, in 32 bits.
-          f32x16 s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[j][0], b0, f32x16{}, 0, 0, 0,
-                                                                     0x7f7f7f7f, 0, 0x7f7f7f7f);
-          s = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(a[j][1], b1, s, 0, 0, 0, 0x7f7f7f7f,
-                                                              0, 0x7f7f7f7f);
-          const float f = sr * sc[j];
-#pragma unroll
-          for (int v = 0; v < 16; ++v) acc[i][j][v] = __builtin_fmaf(s[v], f, acc[i][j][v]);
+        for (int v = 0; v < 4; ++v)
+          acc[i][j][v] = __builtin_fmaf(sum[m % (behind + 1)][v], by[i][j % 2], acc[i][j][v]);
+      };
+      each<S::FR>([&](auto fragment) {
+        constexpr int i = fragment;
+        constexpr bool turned = i == S::FR - 1;
+        by[i][0] = f.sr[i % 2] * f.sc[0];
+        by[i][1] = f.sr[i % 2] * f.sc[1];
+        if constexpr (turned) {
+          settle<(S::stages - 2) * S::copies>();
+          fetch_column_scales(f, next);
+        } else {
+          fetch_row(f, i + 1, here, rr);
         }
-      }
+        each<S::FC>([&](auto column) {
+          constexpr int j = column, m = i * S::FC + j;
+          sum[m % (behind + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              f.a8[j], f.b8[i % 2], f32x4{}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+          if constexpr (turned) {
+            f.a8[j] = cr.get8(next + S::BR * kStep, j);
+            spread<early, S::FC, j>([&](auto q) { copy(q, here); });
+          } else {
+            spread<late, products - S::FC, m>([&](auto q) { copy(q + early, last); });
+            if constexpr (m == products - S::FC - 1) aim();
+          }
+          __builtin_amdgcn_sched_barrier(0);
+          if constexpr (m >= behind) scale(std::integral_constant<int, m - behind>{});
+          __builtin_amdgcn_sched_barrier(0);
+        });
+      });
+      fetch_row(f, 0, next, rr);
+      each<behind>([&](auto b) { scale(std::integral_constant<int, products - behind + b>{}); });
     }
   }
 };

@@ -130,7 +130,9 @@ struct GradArgs {
   int rows, cols;
 };
 
-__device__ __forceinline__ uint32_t no_scale(int) { return kNowhere; }
+struct NoScale {
+  __device__ __forceinline__ uint32_t operator()(int, int = 0) const { return kNowhere; }
+};
 
 // dx[r][c] = sum over n of dz[r][n] w[n][c].
 template <typename S>
@@ -147,27 +149,28 @@ __global__ __launch_bounds__(S::threads) void rows_grad_kernel(GradArgs a) {
   p.c = (const uint8_t*)a.w + (int64_t)t.expert * a.W * w_line + c0 * 2;
   p.c_size = a.W * w_line - c0 * 2;
   p.c_step = kStep / 2 * w_line;
+  p.r_line = (uint32_t)line;
+  p.c_line = (uint32_t)w_line;
+  p.turn = t.col % 8;
   p.k_bytes = line;
   p.rs = p.cs = nullptr;
   p.rs_size = p.cs_size = 0;
   Tile<S> tile;
   tile.run(p, lds_base(lds), [&](int r) { return (uint32_t)(r * line); },
-           [&](int r) { return (uint32_t)(r * w_line); }, no_scale, no_scale);
-  const int lane = lane_id(), half = lane / 32;
+           [&](int r) { return (uint32_t)(r * w_line); }, NoScale{}, NoScale{});
+  const int lane = lane_id();
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
-    const int r = (tile.wr * S::FR + i) * 32 + lane % 32;
+    const int r = (tile.wr * S::FR + i) * kFrag + lane % 16;
     if (r >= t.rows) continue;
     uint16_t* o = a.dx + (int64_t)(t.first + r) * a.in;
 #pragma unroll
-    for (int j = 0; j < S::FC; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = c0 + (tile.wc * S::FC + j) * 32 + 8 * q + 4 * half;
-        const float v[4] = {tile.acc[i][j][4 * q], tile.acc[i][j][4 * q + 1],
-                            tile.acc[i][j][4 * q + 2], tile.acc[i][j][4 * q + 3]};
-        if (c < a.in) store4(o + c, v);
-      }
+    for (int j = 0; j < S::FC; ++j) {
+      const int c = c0 + (tile.wc * S::FC + j) * kFrag + lane / 16 * 4;
+      const float v[4] = {tile.acc[i][j][0], tile.acc[i][j][1], tile.acc[i][j][2],
+                          tile.acc[i][j][3]};
+      if (c < a.in) store4(o + c, v);
+    }
   }
 }
 
@@ -187,32 +190,33 @@ __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   p.c = (const uint8_t*)a.x + first * x_line + c0 * 2;
   p.c_size = rows * x_line - c0 * 2;
   p.c_step = kStep / 2 * x_line;
+  p.r_line = (uint32_t)line;
+  p.c_line = (uint32_t)x_line;
+  p.turn = 0;
   p.k_bytes = (int64_t)rows * 2;
   p.rs = p.cs = nullptr;
   p.rs_size = p.cs_size = 0;
   Tile<S> tile;
   tile.run(p, lds_base(lds), [&](int r) { return (uint32_t)(r * line); },
-           [&](int r) { return (uint32_t)(r * x_line); }, no_scale, no_scale);
-  const int lane = lane_id(), half = lane / 32;
+           [&](int r) { return (uint32_t)(r * x_line); }, NoScale{}, NoScale{});
+  const int lane = lane_id();
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
-    const int r = r0 + (tile.wr * S::FR + i) * 32 + lane % 32;
+    const int r = r0 + (tile.wr * S::FR + i) * kFrag + lane % 16;
     if (r >= a.W) continue;
     uint16_t* o = a.dw + ((int64_t)e * a.W + r) * a.in;
 #pragma unroll
-    for (int j = 0; j < S::FC; ++j)
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int c = c0 + (tile.wc * S::FC + j) * 32 + 8 * q + 4 * half;
-        const float v[4] = {tile.acc[i][j][4 * q], tile.acc[i][j][4 * q + 1],
-                            tile.acc[i][j][4 * q + 2], tile.acc[i][j][4 * q + 3]};
-        if (c < a.in) store4(o + c, v);
-      }
+    for (int j = 0; j < S::FC; ++j) {
+      const int c = c0 + (tile.wc * S::FC + j) * kFrag + lane / 16 * 4;
+      const float v[4] = {tile.acc[i][j][0], tile.acc[i][j][1], tile.acc[i][j][2],
+                          tile.acc[i][j][3]};
+      if (c < a.in) store4(o + c, v);
+    }
   }
 }
 
-using RowsShape = Shape<2, 4, 4, 2, false, true, false, 2>;
-using WeightsShape = Shape<2, 4, 4, 2, true, true, false, 2>;
+using RowsShape = Shape<2, 8, 4, 4, false, true, false, 2>;
+using WeightsShape = Shape<2, 8, 4, 4, true, true, false, 2>;
 
 int64_t blocks_of(const Groups& g) { return tile_grid(g, kChunkRows, 1); }
 
