@@ -34,22 +34,17 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
   *(uint2*)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Fragments of a SwiGLU tile alternate: 16 gate rows of w, the 16 up rows of
-// the same columns; a lane then holds both of a column.
+// One tile. Fragments of a SwiGLU tile alternate: 16 gate rows of w, the 16 up
+// rows of the same columns; a lane then holds both of a column.
 template <typename S, int ACT>
-__global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
+__device__ __forceinline__ void product_tile(const FwdArgs& a, const Where& t, uint32_t lds) {
   constexpr bool glu = ACT == EP_ACT_SWIGLU;
   constexpr int es = S::FP8 ? 1 : 2, per_tile = glu ? S::BC / 2 : S::BC;
-  Where t;
-  if (!find_tile<S::BR, S::threads>(a.g, a.cols, &t)) return;
   const int c0 = t.col * per_tile, wrows = glu ? 2 * a.n : a.n;
   const int64_t line = (int64_t)a.in * es;
   const uint8_t* w = a.w + (int64_t)t.expert * wrows * line;
   // Weight row of row r of the tile, beside the tile's first.
-  const auto w_row = [&](int r) {
-    return glu ? r / 32 * 16 + r % 16 + (r & 16 ? a.n : 0) : r;
-  };
+  const auto w_row = [&](int r) { return glu ? r / 32 * 16 + r % 16 + (r & 16 ? a.n : 0) : r; };
   Pair p;
   p.r = a.x + (int64_t)t.first * line;
   p.c = w + c0 * line;
@@ -70,10 +65,12 @@ __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
   }
   Tile<S> tile;
   tile.run(
-      p, lds_base(lds), [&](int r) { return (uint32_t)(r * line); },
+      p, lds, [&](int r) { return (uint32_t)(r * line); },
       [&](int r) { return (uint32_t)(w_row(r) * line); },
       [&](int r) { return (uint32_t)(r * kb * 4); },
-      [&](int wc, int f) { return (uint32_t)((c0 + w_row((wc * S::FC + f) * kFrag)) / 128 * kb * 4); });
+      [&](int wc, int f) {
+        return (uint32_t)((c0 + w_row((wc * S::FC + f) * kFrag)) / 128 * kb * 4);
+      });
   const int lane = lane_id();
   const uint16_t* bias = a.bias ? a.bias + (int64_t)t.expert * wrows : nullptr;
 #pragma unroll
@@ -108,25 +105,56 @@ __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
   }
 }
 
-template <typename S>
+// S: the kernel's largest tile; T...: smaller ones, in ascending order, of
+// which the first that holds the rows is taken.
+template <int ACT, typename S>
+__device__ __forceinline__ void pick_tile(const FwdArgs& a, const Where& t, uint32_t lds) {
+  product_tile<S, ACT>(a, t, lds);
+}
+template <int ACT, typename S, typename T, typename... U>
+__device__ __forceinline__ void pick_tile(const FwdArgs& a, const Where& t, uint32_t lds) {
+  if (t.rows <= T::BR) product_tile<T, ACT>(a, t, lds);
+  else pick_tile<ACT, S, U...>(a, t, lds);
+}
+
+template <typename... S>
+constexpr int most_lds() {
+  int most = 0;
+  ((most = S::lds_bytes > most ? S::lds_bytes : most), ...);
+  return most;
+}
+
+template <int ACT, typename S, typename... T>
+__global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[most_lds<S, T...>()];
+  static_assert(((T::threads == S::threads && T::BC == S::BC) && ...),
+                "the smaller tiles are the largest one's with fewer rows");
+  Where t;
+  if (!find_tile<S::BR, S::threads>(a.g, a.cols, &t)) return;
+  pick_tile<ACT, S, T...>(a, t, lds_base(lds));
+}
+
+template <typename S, typename... T>
 hipError_t run(FwdArgs a, int act, hipStream_t stream) {
   const int per_tile = act == EP_ACT_SWIGLU ? S::BC / 2 : S::BC;
   a.cols = (a.n + per_tile - 1) / per_tile;
-  const auto kernel = act == EP_ACT_SWIGLU ? product_kernel<S, EP_ACT_SWIGLU>
-                      : act == EP_ACT_SILU ? product_kernel<S, EP_ACT_SILU>
-                      : act == EP_ACT_GELU ? product_kernel<S, EP_ACT_GELU>
-                                           : product_kernel<S, EP_ACT_NONE>;
+  const auto kernel = act == EP_ACT_SWIGLU ? product_kernel<EP_ACT_SWIGLU, S, T...>
+                      : act == EP_ACT_SILU ? product_kernel<EP_ACT_SILU, S, T...>
+                      : act == EP_ACT_GELU ? product_kernel<EP_ACT_GELU, S, T...>
+                                           : product_kernel<EP_ACT_NONE, S, T...>;
   hipLaunchKernelGGL(kernel, dim3((unsigned)tile_grid(a.g, S::BR, a.cols)), dim3(S::threads), 0,
                      stream, a);
   return hipGetLastError();
 }
 
+template <int FR, bool FP8, int STAGES, bool ONCE = true>
+using Rows = Shape<2, FR, 4, 4, false, false, FP8, STAGES, ONCE>;
+
 template <bool FP8>
 hipError_t by_rows(const FwdArgs& a, int act, hipStream_t stream) {
   const int64_t mean = a.g.most / (a.g.N * a.g.L);
-  if (mean <= 24) return run<Shape<1, 2, 2, 4, false, false, FP8, 4>>(a, act, stream);
-  if (mean <= 48) return run<Shape<1, 4, 4, 4, false, false, FP8, 3>>(a, act, stream);
-  return run<Shape<2, 8, 4, 4, false, false, FP8, 2>>(a, act, stream);
+  if (mean <= 24) return run<Shape<1, 2, 2, 4, false, false, FP8, 4, true>>(a, act, stream);
+  return run<Rows<8, FP8, 2, false>, Rows<2, FP8, 3>, Rows<4, FP8, 3>, Rows<6, FP8, 2>>(a, act, stream);
 }
 
 }  // namespace

@@ -51,11 +51,19 @@ __device__ __forceinline__ u32x4 buffer_of(const uint8_t* base, int64_t size) {
 
 // Starts the copy of 16 (or 4) bytes per lane from offset `at` of the buffer
 // to LDS, lane l's to `to` + 16 l (4 l). Nothing waits for it but settle().
+// ONCE: nothing else reads the bytes soon (they do not stay in the caches).
+template <bool ONCE>
 __device__ __forceinline__ void copy16(const u32x4& from, uint32_t at, uint32_t to) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :
-               : "s"(to), "v"(at), "s"(from)
-               : "memory", "m0");
+  if constexpr (ONCE)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen nt lds"
+                 :
+                 : "s"(to), "v"(at), "s"(from)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(to), "v"(at), "s"(from)
+                 : "memory", "m0");
 }
 __device__ __forceinline__ void copy4(const u32x4& from, uint32_t at, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
@@ -136,10 +144,11 @@ struct Operand {
   }
 
   // Copy i of the wave's.
+  template <bool ONCE>
   __device__ __forceinline__ void load(int i, const u32x4& from, uint32_t to, bool there) const {
     const int wave = wave_uniform(threadIdx.x / kWave);
     const uint32_t at = lane_row + (lane_chunk ^ (turn(i * rows) * 16)) + copy_at[i];
-    copy16(from, there ? at : kNowhere, to + (wave * copies + i) * 1024);
+    copy16<ONCE>(from, there ? at : kNowhere, to + (wave * copies + i) * 1024);
   }
 };
 
@@ -191,11 +200,13 @@ struct Reads {
   }
 };
 
-// WR x WC waves of FR x FC fragments of 16 x 16.
-template <int WR_, int FR_, int WC_, int FC_, bool RT_, bool CT_, bool FP8_, int STAGES_>
+// WR x WC waves of FR x FC fragments of 16 x 16. ONCE: no other workgroup reads
+// the columns' operand.
+template <int WR_, int FR_, int WC_, int FC_, bool RT_, bool CT_, bool FP8_, int STAGES_,
+          bool ONCE_ = false>
 struct Shape {
   static constexpr int WR = WR_, FR = FR_, WC = WC_, FC = FC_, stages = STAGES_;
-  static constexpr bool RT = RT_, CT = CT_, FP8 = FP8_;
+  static constexpr bool RT = RT_, CT = CT_, FP8 = FP8_, ONCE = ONCE_;
   static constexpr int BR = WR * FR * kFrag, BC = WC * FC * kFrag, waves = WR * WC;
   static constexpr int threads = waves * kWave;
   // A stage: the two tiles; for e4m3 the scales of BR rows and of the waves'
@@ -204,8 +215,10 @@ struct Shape {
   static constexpr int scale_slots = BR / kWave + (BR % kWave != 0);
   static constexpr int stage_bytes = scales_at + (FP8 ? (scale_slots + 2) * 256 : 0);
   static constexpr int lds_bytes = stage_bytes * stages;
-  static constexpr int copies = Operand<BR, RT, waves>::copies + Operand<BC, CT, waves>::copies +
-                                (FP8 ? 2 : 0);  // two of scales
+  // A wave's copies in a step, those of scales with them.
+  static constexpr int r_copies = Operand<BR, RT, waves>::copies + (FP8 ? 1 : 0);
+  static constexpr int c_copies = Operand<BC, CT, waves>::copies + (FP8 ? 1 : 0);
+  static constexpr int copies = r_copies + c_copies;
   static_assert(!FP8 || waves >= scale_slots, "a wave copies the scales of 64 rows");
   static_assert(!FP8 || FC * kFrag <= 128, "a wave's columns lie in one or two blocks of scales");
 };
@@ -285,32 +298,34 @@ struct Tile {
         from.cs = buffer_of((const uint8_t*)p.cs + 4 * s, there ? p.cs_size - 4 * s : 0);
       }
     };
-    const auto copy = [&](int i, uint32_t to) {
-      if (i < ROperand::copies) {
-        ro.load(i, from.r, to, from.r_there);
-      } else if (i < ROperand::copies + COperand::copies) {
-        co.load(i - ROperand::copies, from.c, to + S::BR * kStep, from.c_there);
-      } else if (i == ROperand::copies + COperand::copies) {
-        copy4(from.rs, rs_lane, to + S::scales_at + rs_slot * 256);
-      } else {
-        copy4(from.cs, cs_lane, to + S::scales_at + cs_slot * 256);
-      }
+    const auto copy_r = [&](int i, uint32_t to) {
+      if (i < ROperand::copies) ro.template load<false>(i, from.r, to, from.r_there);
+      else copy4(from.rs, rs_lane, to + S::scales_at + rs_slot * 256);
     };
+    const auto copy_c = [&](int i, uint32_t to) {
+      if (i < COperand::copies)
+        co.template load<S::ONCE>(i, from.c, to + S::BR * kStep, from.c_there);
+      else
+        copy4(from.cs, cs_lane, to + S::scales_at + cs_slot * 256);
+    };
+    // As many as there are when a first step begins.
 #pragma unroll
     for (int s = 0; s < S::stages; ++s) {
       aim(s);
 #pragma unroll
-      for (int i = 0; i < S::copies; ++i)
-        if (s < S::stages - 1 || i < early) copy(i, lds + s * S::stage_bytes);
+      for (int i = 0; i < S::c_copies; ++i) copy_c(i, lds + s * S::stage_bytes);
+#pragma unroll
+      for (int i = 0; i < S::r_copies; ++i)
+        if (s < S::stages - 1 || i < early) copy_r(i, lds + s * S::stage_bytes);
     }
     uint32_t here = lds, last = lds + (S::stages - 1) * S::stage_bytes;
-    settle<(S::stages - 2) * S::copies + early>();
+    settle<(S::stages - 2) * S::copies + S::c_copies + early>();
     Fragments f;
     fetch_first(f, here, rr, cr);
     for (int s = 0; s < steps; ++s) {
       const uint32_t next =
           here == lds + (S::stages - 1) * S::stage_bytes ? lds : here + S::stage_bytes;
-      step(f, here, next, last, rr, cr, copy, [&] { aim(s + S::stages); });
+      step(f, here, next, last, rr, cr, copy_r, copy_c, [&] { aim(s + S::stages); });
       last = here;
       here = next;
     }
@@ -357,19 +372,22 @@ struct Tile {
     }
   }
 
-  // Copies of a step that start in the step before the one that they are
-  // counted in.
-  static constexpr int early = S::FP8 ? S::copies / 4 : S::copies;
+  // Copies of rows that start in the step before the one whose beginning has
+  // the others.
+  static constexpr int early = S::FP8 ? S::r_copies / 2 : S::r_copies;
+  // e4m3: the columns' tile is free as soon as the step has begun, since its
+  // fragments stay in registers.
+  static constexpr bool columns_first = S::FP8 && S::FR >= 4;
 
   // One step's products. Before its last part every wave has read the step's
   // tiles (the last fragments are in registers) and the next step's have
-  // arrived; then copy(i, here), aimed by aim(), starts the early copies of a later
-  // step in their place. The other copies of the step before, to `last`, stand
-  // at the beginning. They are spread over the products, since a copy holds a
-  // wave up while the memory pipeline takes it.
-  template <typename F, typename A>
+  // arrived; then the copies of the step that is `stages` further, which aim()
+  // finds, start in their place. They are spread over the products, since a
+  // copy holds a wave up while the memory pipeline takes it.
+  template <typename FR_, typename FC_, typename A>
   __device__ __forceinline__ void step(Fragments& f, uint32_t here, uint32_t next, uint32_t last,
-                                       const RReads& rr, const CReads& cr, F&& copy, A&& aim) {
+                                       const RReads& rr, const CReads& cr, FR_&& copy_r,
+                                       FC_&& copy_c, A&& aim) {
     constexpr int products = S::FR * S::FC;
     if constexpr (!S::FP8) {
       each<2>([&](auto half) {
@@ -383,7 +401,10 @@ struct Tile {
             spread<parts, slots, m>([&](auto q) { fetch(f, q, kk ? next : here, 1 - kk, rr, cr); });
           if constexpr (kk == 0 && m == slots - 1) aim();
           if constexpr (kk == 1)
-            spread<S::copies, products, m>([&](auto q) { copy(q, here); });
+            spread<S::copies, products, m>([&](auto q) {
+              if constexpr (q < S::c_copies) copy_c(q, here);
+              else copy_r(q - S::c_copies, here);
+            });
           acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
               __builtin_bit_cast(bf16x8, f.a[kk][j]), __builtin_bit_cast(bf16x8, f.b[kk][i]),
               acc[i][j], 0, 0, 0);
@@ -394,7 +415,7 @@ struct Tile {
       // Scales of 2^0 for both operands of the matrix instruction; the blocks'
       // own multiply its sum over 128 values of k, in 32 bits, two products
       // later, when it is there.
-      constexpr int behind = 2, late = S::copies - early;
+      constexpr int behind = 2;
       f32x4 sum[behind + 1];
       float by[S::FR][2];
       const auto scale = [&](auto product) {
@@ -408,8 +429,10 @@ struct Tile {
         constexpr bool turned = i == S::FR - 1;
         by[i][0] = f.sr[i % 2] * f.sc[0];
         by[i][1] = f.sr[i % 2] * f.sc[1];
+        if constexpr (i == 1 && columns_first)
+          asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
         if constexpr (turned) {
-          settle<(S::stages - 2) * S::copies>();
+          settle<(S::stages - 2) * S::copies + (columns_first ? S::c_copies : 0)>();
           fetch_column_scales(f, next);
         } else {
           fetch_row(f, i + 1, here, rr);
@@ -418,12 +441,17 @@ struct Tile {
           constexpr int j = column, m = i * S::FC + j;
           sum[m % (behind + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
               f.a8[j], f.b8[i % 2], f32x4{}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+          if constexpr (turned) f.a8[j] = cr.get8(next + S::BR * kStep, j);
+          if constexpr (i == 0) {
+            spread<S::r_copies - early, S::FC, j>([&](auto q) { copy_r(early + q, last); });
+            if constexpr (j == S::FC - 1) aim();
+          }
+          if constexpr (columns_first && i >= 1 && i < 3)
+            spread<S::c_copies, 2 * S::FC, m - S::FC>([&](auto q) { copy_c(q, here); });
           if constexpr (turned) {
-            f.a8[j] = cr.get8(next + S::BR * kStep, j);
-            spread<early, S::FC, j>([&](auto q) { copy(q, here); });
-          } else {
-            spread<late, products - S::FC, m>([&](auto q) { copy(q + early, last); });
-            if constexpr (m == products - S::FC - 1) aim();
+            if constexpr (!columns_first)
+              spread<S::c_copies, S::FC, j>([&](auto q) { copy_c(q, here); });
+            spread<early, S::FC, j>([&](auto q) { copy_r(q, here); });
           }
           __builtin_amdgcn_sched_barrier(0);
           if constexpr (m >= behind) scale(std::integral_constant<int, m - behind>{});

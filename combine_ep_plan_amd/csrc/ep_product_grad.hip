@@ -7,8 +7,9 @@ namespace {
 
 // --- dz and dbias -----------------------------------------------------------
 
-constexpr int kChunkRows = 64;   // rows of one group per workgroup
-constexpr int kActThreads = 128; // columns / 4
+constexpr int kChunkRows = 32;     // rows of one group per workgroup
+constexpr int kActThreads = 256;   // four rows at a time, 64 lanes of 4 columns
+constexpr int kActCols = kWave * 4;
 
 struct ActArgs {
   const uint16_t *dout, *pre;
@@ -21,8 +22,7 @@ struct ActArgs {
 
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
 
-__device__ __forceinline__ void load4(const uint16_t* p, float (&v)[4]) {
-  const uint2 u = *(const uint2*)p;
+__device__ __forceinline__ void unpack4(const uint2& u, float (&v)[4]) {
   v[0] = bf16_lo(u.x);
   v[1] = bf16_hi(u.x);
   v[2] = bf16_lo(u.y);
@@ -32,72 +32,87 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
   *(uint2*)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// Row blocks before expert e's, for blocks of BR rows: the place of its parts.
+// dz of a block of rows and columns, and the columns' sums over the rows: wave
+// w takes rows w, w + 4, ..., all of them on their way at once.
 template <int ACT>
 __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   constexpr bool glu = ACT == EP_ACT_SWIGLU;
-  __shared__ int block_at;
+  constexpr int waves = kActThreads / kWave, steps = kChunkRows / waves;
+  __shared__ int before[waves];
+  __shared__ float room[waves][glu ? 2 : 1][kActCols];
   Where t;
   if (!find_tile<kChunkRows, kActThreads>(a.g, a.cols, &t)) return;
-  // The row block's number on the line of all groups' row blocks.
-  if (a.parts) {
-    __shared__ int sums[kActThreads / kWave];
-    int before = 0;
-    for (int e = threadIdx.x; e < t.expert; e += kActThreads)
-      before += (group_of(a.g, e).rows + kChunkRows - 1) / kChunkRows;
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int c = t.col * kActCols + lane * 4, W = glu ? 2 * a.n : a.n;
+  float s[glu ? 2 : 1][4] = {};
+  if (c < a.n) {
+    uint2 d2[steps], z2[steps], u2[steps];
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) before += __shfl_xor(before, off);
-    if (lane_id() == 0) sums[threadIdx.x / kWave] = before;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      int s = t.at / kChunkRows;
-      for (int w = 0; w < kActThreads / kWave; ++w) s += sums[w];
-      block_at = s;
+    for (int i = 0; i < steps; ++i) {
+      const int r = wave + i * waves;
+      const int64_t row = t.first + r;
+      d2[i] = z2[i] = u2[i] = uint2{0, 0};
+      if (r >= t.rows) continue;
+      d2[i] = *(const uint2*)(a.dout + row * a.n + c);
+      if constexpr (ACT != EP_ACT_NONE) z2[i] = *(const uint2*)(a.pre + row * W + c);
+      if constexpr (glu) u2[i] = *(const uint2*)(a.pre + row * W + a.n + c);
     }
-    __syncthreads();
-  }
-  const int c = (t.col * kActThreads + threadIdx.x) * 4;
-  if (c >= a.n) return;
-  const int W = glu ? 2 * a.n : a.n;
-  float s0[4] = {0, 0, 0, 0}, s1[4] = {0, 0, 0, 0};
-  for (int r = 0; r < t.rows; ++r) {
-    const int64_t row = t.first + r;
-    float d[4], z[4], u[4], o[4];
-    load4(a.dout + row * a.n + c, d);
-    if constexpr (ACT == EP_ACT_NONE) {
 #pragma unroll
-      for (int v = 0; v < 4; ++v) s0[v] += d[v];
-      continue;
-    }
-    load4(a.pre + row * W + c, z);
-    if constexpr (glu) load4(a.pre + row * W + a.n + c, u);
+    for (int i = 0; i < steps; ++i) {
+      const int r = wave + i * waves;
+      if (r >= t.rows) continue;
+      const int64_t row = t.first + r;
+      float d[4], z[4], u[4], o[4];
+      unpack4(d2[i], d);
+      unpack4(z2[i], z);
+      unpack4(u2[i], u);
 #pragma unroll
-    for (int v = 0; v < 4; ++v) {
-      if constexpr (ACT == EP_ACT_GELU) {
-        const float cdf = 0.5f * erfcf(z[v] * -0.70710678118654752f);
-        o[v] = d[v] * (cdf + z[v] * 0.39894228040143268f * __expf(-0.5f * z[v] * z[v]));
-      } else {
-        const float s = sigmoid(z[v]);
-        const float slope = s * (1.0f + z[v] * (1.0f - s));
-        if constexpr (glu) {
-          o[v] = d[v] * u[v] * slope;
-          u[v] = d[v] * z[v] * s;
-          s1[v] += u[v];
+      for (int v = 0; v < 4; ++v) {
+        if constexpr (ACT == EP_ACT_NONE) {
+          o[v] = d[v];
+        } else if constexpr (ACT == EP_ACT_GELU) {
+          const float cdf = 0.5f * erfcf(z[v] * -0.70710678118654752f);
+          o[v] = d[v] * (cdf + z[v] * 0.39894228040143268f * __expf(-0.5f * z[v] * z[v]));
         } else {
-          o[v] = d[v] * slope;
+          const float sg = sigmoid(z[v]);
+          const float slope = sg * (1.0f + z[v] * (1.0f - sg));
+          if constexpr (glu) {
+            o[v] = d[v] * u[v] * slope;
+            u[v] = d[v] * z[v] * sg;
+            s[1][v] += u[v];
+          } else {
+            o[v] = d[v] * slope;
+          }
         }
+        s[0][v] += o[v];
       }
-      s0[v] += o[v];
-    }
-    if (a.dz) {
-      store4(a.dz + row * W + c, o);
-      if constexpr (glu) store4(a.dz + row * W + a.n + c, u);
+      if (ACT != EP_ACT_NONE && a.dz) {
+        store4(a.dz + row * W + c, o);
+        if constexpr (glu) store4(a.dz + row * W + a.n + c, u);
+      }
     }
   }
   if (!a.parts) return;
-  float* p = a.parts + (int64_t)block_at * W + c;
-  *(float4*)p = float4{s0[0], s0[1], s0[2], s0[3]};
-  if constexpr (glu) *(float4*)(p + a.n) = float4{s1[0], s1[1], s1[2], s1[3]};
+  // The row block's number among all groups' row blocks: those of the experts
+  // before, then those of its own.
+  int mine = 0;
+  for (int e = threadIdx.x; e < t.expert; e += kActThreads)
+    mine += (group_of(a.g, e).rows + kChunkRows - 1) / kChunkRows;
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) mine += __shfl_xor(mine, off);
+  if (lane == 0) before[wave] = mine;
+#pragma unroll
+  for (int h = 0; h < (glu ? 2 : 1); ++h)
+    *(float4*)&room[wave][h][lane * 4] = float4{s[h][0], s[h][1], s[h][2], s[h][3]};
+  __syncthreads();
+  const int block = t.at / kChunkRows + before[0] + before[1] + before[2] + before[3];
+  const int col = t.col * kActCols + threadIdx.x;
+  if (col >= a.n) return;
+#pragma unroll
+  for (int h = 0; h < (glu ? 2 : 1); ++h)
+    a.parts[(int64_t)block * W + h * a.n + col] =
+        room[0][h][threadIdx.x] + room[1][h][threadIdx.x] + room[2][h][threadIdx.x] +
+        room[3][h][threadIdx.x];
 }
 
 // dbias[e][c]: the parts of e's row blocks, in order.
@@ -136,10 +151,7 @@ struct NoScale {
 
 // dx[r][c] = sum over n of dz[r][n] w[n][c].
 template <typename S>
-__global__ __launch_bounds__(S::threads) void rows_grad_kernel(GradArgs a) {
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
-  Where t;
-  if (!find_tile<S::BR, S::threads>(a.g, a.cols, &t)) return;
+__device__ __forceinline__ void rows_tile(const GradArgs& a, const Where& t, uint32_t lds) {
   const int c0 = t.col * S::BC;
   const int64_t line = (int64_t)a.W * 2, w_line = (int64_t)a.in * 2;
   Pair p;
@@ -156,7 +168,7 @@ __global__ __launch_bounds__(S::threads) void rows_grad_kernel(GradArgs a) {
   p.rs = p.cs = nullptr;
   p.rs_size = p.cs_size = 0;
   Tile<S> tile;
-  tile.run(p, lds_base(lds), [&](int r) { return (uint32_t)(r * line); },
+  tile.run(p, lds, [&](int r) { return (uint32_t)(r * line); },
            [&](int r) { return (uint32_t)(r * w_line); }, NoScale{}, NoScale{});
   const int lane = lane_id();
 #pragma unroll
@@ -174,12 +186,33 @@ __global__ __launch_bounds__(S::threads) void rows_grad_kernel(GradArgs a) {
   }
 }
 
+template <int FR, bool ONCE>
+using RowsShape = Shape<2, FR, 4, 4, false, true, false, 2, ONCE>;
+
+__global__ __launch_bounds__(512) void rows_grad_kernel(GradArgs a) {
+  using S = RowsShape<8, false>;
+  static_assert(S::threads == 512, "");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
+  Where t;
+  if (!find_tile<S::BR, S::threads>(a.g, a.cols, &t)) return;
+  if (t.rows <= 64) rows_tile<RowsShape<2, true>>(a, t, lds_base(lds));
+  else if (t.rows <= 128) rows_tile<RowsShape<4, true>>(a, t, lds_base(lds));
+  else if (t.rows <= 192) rows_tile<RowsShape<6, true>>(a, t, lds_base(lds));
+  else rows_tile<S>(a, t, lds_base(lds));
+}
+
 // dw[n][c] = sum over the expert's rows r of dz[r][n] x[r][c].
 template <typename S>
 __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
-  const int tiles = a.rows * a.cols, e = blockIdx.x / tiles, at = blockIdx.x - e * tiles;
-  const int r0 = at / a.cols * S::BR, c0 = at % a.cols * S::BC;
+  // The experts' tiles lie on a line that the XCDs share, as in find_tile.
+  const int tiles = a.rows * a.cols, all = tiles * a.g.N * a.g.L, stretch = (all + 7) / 8;
+  const int slot = blockIdx.x / 8, want = blockIdx.x % 8 * stretch + slot;
+  if (slot >= stretch || want >= all) return;
+  const int e = want / tiles, at = want - e * tiles, stripe = at / (a.rows * 8);
+  const int wide = a.cols - stripe * 8 < 8 ? a.cols - stripe * 8 : 8;
+  const int in = at - stripe * a.rows * 8;
+  const int r0 = in / wide * S::BR, c0 = (stripe * 8 + in % wide) * S::BC;
   const Group g = group_of(a.g, e);
   const int first = wave_uniform(g.first), rows = wave_uniform(g.rows);
   const int64_t line = (int64_t)a.W * 2, x_line = (int64_t)a.in * 2;
@@ -215,7 +248,6 @@ __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   }
 }
 
-using RowsShape = Shape<2, 8, 4, 4, false, true, false, 2>;
 using WeightsShape = Shape<2, 8, 4, 4, true, true, false, 2>;
 
 int64_t blocks_of(const Groups& g) { return tile_grid(g, kChunkRows, 1); }
@@ -238,7 +270,7 @@ int64_t most_blocks(const Dims& d) {
 }  // namespace
 
 bool product_fits(const ep_product& p, const Dims& d) {
-  // The smallest tiles are 32 x 64 (columns of a SwiGLU tile), 64 x 512 in the
+  // The smallest tiles are 32 x 64 (columns of a SwiGLU tile), 32 x 256 in the
   // elementwise part; no workgroup has more than 512 threads.
   const int64_t rows = d.NTR > d.N * d.cap ? d.NTR : d.N * d.cap;
   const int64_t most = (int64_t)1 << 23, W = weight_rows(p);
@@ -268,7 +300,7 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
       dbias ? (float*)((char*)ws + (none ? 0 : align256((int64_t)d.N * d.cap * W * 2))) : nullptr;
   act.g = g;
   act.n = p.out;
-  act.cols = (p.out / 4 + kActThreads - 1) / kActThreads;
+  act.cols = (p.out + kActCols - 1) / kActCols;
   hipError_t e = hipSuccess;
   if (g.most > 0 && (act.dz || act.parts)) {
     const auto kernel = p.act == EP_ACT_SWIGLU ? act_grad_kernel<EP_ACT_SWIGLU>
@@ -297,17 +329,18 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
   a.W = W;
   a.rows = (W + WeightsShape::BR - 1) / WeightsShape::BR;
   if (dx && g.most > 0) {
-    a.cols = (p.in + RowsShape::BC - 1) / RowsShape::BC;
-    hipLaunchKernelGGL(rows_grad_kernel<RowsShape>,
-                       dim3((unsigned)tile_grid(g, RowsShape::BR, a.cols)),
-                       dim3(RowsShape::threads), 0, stream, a);
+    using S = RowsShape<8, false>;
+    a.cols = (p.in + S::BC - 1) / S::BC;
+    hipLaunchKernelGGL(rows_grad_kernel, dim3((unsigned)tile_grid(g, S::BR, a.cols)),
+                       dim3(S::threads), 0, stream, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (dw) {
     a.cols = (p.in + WeightsShape::BC - 1) / WeightsShape::BC;
     hipLaunchKernelGGL(weights_grad_kernel<WeightsShape>,
-                       dim3((unsigned)(experts * a.rows * a.cols)), dim3(WeightsShape::threads), 0,
+                       dim3((unsigned)((experts * a.rows * a.cols + 7) / 8 * 8)),
+                       dim3(WeightsShape::threads), 0,
                        stream, a);
     e = hipGetLastError();
   }
