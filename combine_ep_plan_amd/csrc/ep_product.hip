@@ -34,44 +34,13 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
   *(uint2*)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
 }
 
-// One tile. Fragments of a SwiGLU tile alternate: 16 gate rows of w, the 16 up
-// rows of the same columns; a lane then holds both of a column.
+// A tile's output. Fragments of a SwiGLU tile alternate: 16 gate rows of w, the
+// 16 up rows of the same columns; a lane then holds both of a column.
 template <typename S, int ACT>
-__device__ __forceinline__ void product_tile(const FwdArgs& a, const Where& t, uint32_t lds) {
+__device__ __forceinline__ void write_tile(const FwdArgs& a, const Tile<S>& tile, const Where& t) {
   constexpr bool glu = ACT == EP_ACT_SWIGLU;
-  constexpr int es = S::FP8 ? 1 : 2, per_tile = glu ? S::BC / 2 : S::BC;
-  const int c0 = t.col * per_tile, wrows = glu ? 2 * a.n : a.n;
-  const int64_t line = (int64_t)a.in * es;
-  const uint8_t* w = a.w + (int64_t)t.expert * wrows * line;
-  // Weight row of row r of the tile, beside the tile's first.
-  const auto w_row = [&](int r) { return glu ? r / 32 * 16 + r % 16 + (r & 16 ? a.n : 0) : r; };
-  Pair p;
-  p.r = a.x + (int64_t)t.first * line;
-  p.c = w + c0 * line;
-  p.r_size = t.rows * line;
-  p.c_size = (int64_t)(wrows - c0) * line;
-  p.r_step = p.c_step = kStep;
-  p.r_line = p.c_line = (uint32_t)line;
-  p.turn = t.col % 8;
-  p.k_bytes = line;
-  p.rs = p.cs = nullptr;
-  p.rs_size = p.cs_size = 0;
-  const int kb = a.in / 128;
-  if constexpr (S::FP8) {
-    p.rs = a.xs + (int64_t)t.first * kb;
-    p.rs_size = (int64_t)t.rows * kb * 4;
-    p.cs = a.ws + (int64_t)t.expert * (wrows / 128) * kb;
-    p.cs_size = (int64_t)(wrows / 128) * kb * 4;
-  }
-  Tile<S> tile;
-  tile.run(
-      p, lds, [&](int r) { return (uint32_t)(r * line); },
-      [&](int r) { return (uint32_t)(w_row(r) * line); },
-      [&](int r) { return (uint32_t)(r * kb * 4); },
-      [&](int wc, int f) {
-        return (uint32_t)((c0 + w_row((wc * S::FC + f) * kFrag)) / 128 * kb * 4);
-      });
-  const int lane = lane_id();
+  const int lane = lane_id(), c0 = t.col * (glu ? S::BC / 2 : S::BC);
+  const int wrows = glu ? 2 * a.n : a.n;
   const uint16_t* bias = a.bias ? a.bias + (int64_t)t.expert * wrows : nullptr;
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
@@ -105,16 +74,66 @@ __device__ __forceinline__ void product_tile(const FwdArgs& a, const Where& t, u
   }
 }
 
-// S: the kernel's largest tile; T...: smaller ones, in ascending order, of
-// which the first that holds the rows is taken.
-template <int ACT, typename S>
-__device__ __forceinline__ void pick_tile(const FwdArgs& a, const Where& t, uint32_t lds) {
-  product_tile<S, ACT>(a, t, lds);
+// Tiles of more than MIN and at most S::BR rows, from t on, while the line has
+// such ones. Returns whether t is then a tile of another height.
+template <typename S, int ACT, int MIN, typename L>
+__device__ __forceinline__ bool run_tiles(const FwdArgs& a, L& line_, Where& t, uint32_t lds) {
+  constexpr bool glu = ACT == EP_ACT_SWIGLU;
+  constexpr int es = S::FP8 ? 1 : 2, per_tile = glu ? S::BC / 2 : S::BC;
+  const int wrows = glu ? 2 * a.n : a.n, kb = a.in / 128;
+  const int line = a.in * es;
+  // Weight row of row r of the tile, beside the tile's first.
+  const auto w_row = [&](int r) { return glu ? r / 32 * 16 + r % 16 + (r & 16 ? a.n : 0) : r; };
+  const auto feed_of = [&](const Where& w) {
+    const int c0 = w.col * per_tile;
+    Feed p;
+    p.r = a.x + (int64_t)w.first * line;
+    p.c = a.w + ((int64_t)w.expert * wrows + c0) * line;
+    p.r_size = w.rows * line;
+    p.c_size = (wrows - c0) * line;
+    p.r_off = p.c_off = 0;
+    p.left = line;
+    p.rs = p.cs = nullptr;
+    p.rs_size = p.cs_size = 0;
+    if constexpr (S::FP8) {
+      const int64_t block = (int64_t)w.expert * (wrows / 128) + c0 / 128;
+      p.rs = a.xs + (int64_t)w.first * kb;
+      p.rs_size = w.rows * kb * 4;
+      p.cs = a.ws + block * kb;
+      p.cs_size = (wrows / 128 - c0 / 128) * kb * 4;
+    }
+    return p;
+  };
+  Tile<S> tile(
+      lds, line, line, [&](int r) { return (uint32_t)(r * line); },
+      [&](int r) { return (uint32_t)(w_row(r) * line); },
+      [&](int r) { return (uint32_t)(r * kb * 4); },
+      [&](int wc, int f) { return (uint32_t)(w_row((wc * S::FC + f) * kFrag) / 128 * kb * 4); });
+  Feed p = feed_of(t);
+  const bool long_enough = p.steps() >= S::stages;
+  for (bool primed = false;;) {
+    Where n = t;
+    const bool more = line_.next(&n);
+    const bool same = more && n.rows > MIN && n.rows <= S::BR, chained = same && long_enough;
+    const Feed after = feed_of(n);
+    tile.run(p, primed, after, chained);
+    write_tile<S, ACT>(a, tile, t);
+    t = n;
+    if (!same) return more;
+    p = after;
+    primed = chained;
+  }
 }
-template <int ACT, typename S, typename T, typename... U>
-__device__ __forceinline__ void pick_tile(const FwdArgs& a, const Where& t, uint32_t lds) {
-  if (t.rows <= T::BR) product_tile<T, ACT>(a, t, lds);
-  else pick_tile<ACT, S, U...>(a, t, lds);
+
+// S: the kernel's largest tile; T...: smaller ones, in ascending order.
+template <int ACT, int MIN, typename S, typename L>
+__device__ __forceinline__ bool pick_tiles(const FwdArgs& a, L& line, Where& t, uint32_t lds) {
+  return run_tiles<S, ACT, MIN>(a, line, t, lds);
+}
+template <int ACT, int MIN, typename S, typename T, typename... U, typename L>
+__device__ __forceinline__ bool pick_tiles(const FwdArgs& a, L& line, Where& t, uint32_t lds) {
+  if (t.rows <= T::BR) return run_tiles<T, ACT, MIN>(a, line, t, lds);
+  return pick_tiles<ACT, T::BR, S, U...>(a, line, t, lds);
 }
 
 template <typename... S>
@@ -127,11 +146,13 @@ constexpr int most_lds() {
 template <int ACT, typename S, typename... T>
 __global__ __launch_bounds__(S::threads) void product_kernel(FwdArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[most_lds<S, T...>()];
+  extern __shared__ int ends[];
   static_assert(((T::threads == S::threads && T::BC == S::BC) && ...),
                 "the smaller tiles are the largest one's with fewer rows");
+  Line<S::BR, S::threads> line(a.g, a.cols, ends);
   Where t;
-  if (!find_tile<S::BR, S::threads>(a.g, a.cols, &t)) return;
-  pick_tile<ACT, S, T...>(a, t, lds_base(lds));
+  bool more = line.next(&t);
+  while (more) more = pick_tiles<ACT, 0, S, T...>(a, line, t, lds_base(lds));
 }
 
 template <typename S, typename... T>
@@ -142,8 +163,8 @@ hipError_t run(FwdArgs a, int act, hipStream_t stream) {
                       : act == EP_ACT_SILU ? product_kernel<EP_ACT_SILU, S, T...>
                       : act == EP_ACT_GELU ? product_kernel<EP_ACT_GELU, S, T...>
                                            : product_kernel<EP_ACT_NONE, S, T...>;
-  hipLaunchKernelGGL(kernel, dim3((unsigned)tile_grid(a.g, S::BR, a.cols)), dim3(S::threads), 0,
-                     stream, a);
+  hipLaunchKernelGGL(kernel, dim3(line_grid(tile_grid(a.g, S::BR, a.cols))), dim3(S::threads),
+                     (size_t)a.g.N * a.g.L * 4, stream, a);
   return hipGetLastError();
 }
 

@@ -40,13 +40,12 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // nearest ev
 }
 
 // Bytes [base, base + size) as the buffer instructions take them (raw: 32-bit
-// offsets, reads past the end give zeros).
-__device__ __forceinline__ u32x4 buffer_of(const uint8_t* base, int64_t size) {
+// offsets, reads past the end give zeros; no bytes when size is negative).
+__device__ __forceinline__ u32x4 buffer_of(const uint8_t* base, int size) {
   const uint64_t p = (uint64_t)(uintptr_t)base;
-  const int64_t n = size < 0 ? 0 : size < 0x7fffffff ? size : 0x7fffffff;
-  return u32x4{(uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)p),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)((uint32_t)(p >> 32) & 0xffffu)),
-               (uint32_t)__builtin_amdgcn_readfirstlane((int)n), 0x00020000u};
+  return u32x4{(uint32_t)wave_uniform((int)(uint32_t)p),
+               (uint32_t)wave_uniform((int)(uint32_t)(p >> 32)),
+               (uint32_t)wave_uniform(size > 0 ? size : 0), 0x00020000u};
 }
 
 // Starts the copy of 16 (or 4) bytes per lane from offset `at` of the buffer
@@ -136,11 +135,16 @@ struct Operand {
     for (int i = 0; i < copies; ++i) copy_at[i] = wave_uniform(row_at(first + i * rows));
   }
 
-  // Whether the lane's chunk lies before the end of k, `tail` bytes from the
+  // Whether the lane's chunk lies before the end of k, `left` bytes from the
   // step's start (always, for a slow-k tile: rows behind k are behind the
   // buffer).
-  __device__ __forceinline__ bool before(int tail) const {
-    return T || (int)lane_chunk < tail;
+  __device__ __forceinline__ bool before(int left) const { return T || (int)lane_chunk < left; }
+
+  // Bytes that a step may read, given those from its first row on (dense k) or
+  // the bytes of k that are left and of the first row before the tile (slow k).
+  static __device__ __forceinline__ int bytes(int size, int left, int line, int off) {
+    if constexpr (!T) return size;
+    else return (left < kStep ? left : kStep) / 2 * line - off;
   }
 
   // Copy i of the wave's.
@@ -223,19 +227,22 @@ struct Shape {
   static_assert(!FP8 || FC * kFrag <= 128, "a wave's columns lie in one or two blocks of scales");
 };
 
-// What a workgroup multiplies. Sizes in bytes from the tile's first byte.
-struct Pair {
+// What a tile multiplies, from some step of k on: the next copies' sources.
+struct Feed {
   const uint8_t *r, *c;
-  int64_t r_size, c_size;
-  int64_t r_step, c_step;  // bytes from one step to the next
-  uint32_t r_line, c_line; // bytes from one row (of k, where it is slow) to the next
-  int turn;                // the step of k that comes first
-  int64_t k_bytes;         // of k in all, as a dense-k operand counts it (2 per value when bf16)
-  // e4m3: scales of the rows, [row][k / 128], and of the columns' blocks.
-  const float *rs, *cs;
-  int64_t rs_size, cs_size;
+  int r_size, c_size;      // dense k: bytes from there to the operand's end
+  int r_off, c_off;        // slow k: bytes of a row before the tile
+  int left;                // bytes of k, as a dense-k operand counts them (2 per value when bf16)
+  const float *rs, *cs;    // e4m3: scales of the rows, [row][k / 128], and of the columns' blocks
+  int rs_size, cs_size;
+
+  __device__ __forceinline__ int steps() const { return (left + kStep - 1) / kStep; }
 };
 
+// A workgroup's tiles, one after the other. The copies of the next tile's
+// first steps start during the last ones of a tile, so that neither the way
+// from memory nor the tile's output leaves the matrix units without work for
+// long: apart, a tile of 16 steps took 38 us of which 25 were its steps.
 template <typename S>
 struct Tile {
   f32x4 acc[S::FR][S::FC];
@@ -246,127 +253,157 @@ struct Tile {
   using RReads = Reads<S::BR, S::RT, S::FR>;
   using CReads = Reads<S::BC, S::CT, S::FC>;
 
+  ROperand ro;
+  COperand co;
+  RReads rr;
+  CReads cr;
+  int r_line, c_line;           // bytes from one row (of k, where it is slow) to the next
+  uint32_t lds, here, last;     // the ring of steps; the places of this one and the one before
+  uint32_t rs_lane, cs_lane;    // of the lane's scales
+  Feed feed;                    // of the copies that start next
   // Where the copies of a step come from.
-  struct Source {
+  struct {
     u32x4 r, c, rs, cs;
     bool r_there, c_there;
-  };
+  } from;
 
-  // r_at, c_at: byte offsets of rows (see Operand); rs_at(row), cs_at(wave
-  // column, parity of the fragment): byte offsets of scales.
+  // r_at, c_at: byte offsets of rows (see Operand); rs_at(row), cs_at(wave column, parity of the fragment): byte
+  // offsets of scales. The same for all of the workgroup's tiles.
   template <typename FR_AT, typename FC_AT, typename RS_AT, typename CS_AT>
-  __device__ __forceinline__ void run(const Pair& p, uint32_t lds, FR_AT&& r_at, FC_AT&& c_at,
-                                      RS_AT&& rs_at, CS_AT&& cs_at) {
-    const int wave = wave_uniform(threadIdx.x / kWave), lane = lane_id();
-    wr = wave / S::WC;
-    wc = wave % S::WC;
+  __device__ __forceinline__ Tile(uint32_t lds, int r_line, int c_line, FR_AT&& r_at,
+                                  FC_AT&& c_at, RS_AT&& rs_at, CS_AT&& cs_at)
+      : wr(wave_uniform(threadIdx.x / kWave) / S::WC),
+        wc(wave_uniform(threadIdx.x / kWave) % S::WC),
+        rr(wr * S::FR * kFrag),
+        cr(wc * S::FC * kFrag),
+        r_line(r_line),
+        c_line(c_line),
+        lds(lds) {
+    ro.init(r_at, (uint32_t)r_line);
+    co.init(c_at, (uint32_t)c_line);
+    if constexpr (S::FP8) {
+      // Waves copy the scales of 64 rows each, the first also those of the
+      // columns; the others fill a place that nothing reads.
+      const int wave = wave_uniform(threadIdx.x / kWave), lane = lane_id();
+      rs_lane = wave * kWave + lane < S::BR ? rs_at(wave * kWave + lane) : kNowhere;
+      cs_lane = wave == 0 && lane < 2 * S::WC ? cs_at(lane / 2, lane % 2) : kNowhere;
+    }
+  }
+
+  // Sets the sources of one step's copies. Behind a tile's last step come those
+  // of the tile after it, if there is one (once), else zeros from an empty
+  // buffer, so that every stage counts the same number of copies.
+  __device__ __forceinline__ void aim(const Feed& after, bool& chained) {
+    if (feed.left <= 0) {
+      if (chained) feed = after;
+      else feed.r_size = feed.c_size = feed.rs_size = feed.cs_size = 0;
+      chained = false;
+    }
+    from.r = buffer_of(feed.r, ROperand::bytes(feed.r_size, feed.left, r_line, feed.r_off));
+    from.c = buffer_of(feed.c, COperand::bytes(feed.c_size, feed.left, c_line, feed.c_off));
+    from.r_there = ro.before(feed.left);
+    from.c_there = co.before(feed.left);
+    feed.r += S::RT ? kStep / 2 * (int64_t)r_line : kStep;
+    feed.c += S::CT ? kStep / 2 * (int64_t)c_line : kStep;
+    feed.r_size -= kStep;
+    feed.c_size -= kStep;
+    feed.left -= kStep;
+    if constexpr (S::FP8) {
+      from.rs = buffer_of((const uint8_t*)feed.rs, feed.rs_size);
+      from.cs = buffer_of((const uint8_t*)feed.cs, feed.cs_size);
+      ++feed.rs;
+      ++feed.cs;
+      feed.rs_size -= 4;
+      feed.cs_size -= 4;
+    }
+  }
+  __device__ __forceinline__ void copy_r(int i, uint32_t to) {
+    const int wave = wave_uniform(threadIdx.x / kWave);
+    if (i < ROperand::copies)
+      ro.template load<false>(i, from.r, to, from.r_there);
+    else
+      copy4(from.rs, rs_lane,
+            to + S::scales_at + (wave < S::scale_slots ? wave : S::scale_slots + 1) * 256);
+  }
+  __device__ __forceinline__ void copy_c(int i, uint32_t to) {
+    const int wave = wave_uniform(threadIdx.x / kWave);
+    if (i < COperand::copies)
+      co.template load<S::ONCE>(i, from.c, to + S::BR * kStep, from.c_there);
+    else
+      copy4(from.cs, cs_lane, to + S::scales_at + (S::scale_slots + (wave == 0 ? 0 : 1)) * 256);
+  }
+
+  // The products of tile p into acc. primed: its first copies have been started
+  // by the run before it. chained: `after` is the tile of the next run, which
+  // has at least as many steps as there are stages.
+  __device__ __forceinline__ void run(const Feed& p, bool primed, const Feed& after, bool chained) {
+    bool to_come = chained;
 #pragma unroll
     for (int i = 0; i < S::FR; ++i)
 #pragma unroll
       for (int j = 0; j < S::FC; ++j) acc[i][j] = f32x4{};
-    ROperand ro;
-    COperand co;
-    ro.init(r_at, p.r_line);
-    co.init(c_at, p.c_line);
-    // Waves copy the scales of 64 rows each, the first also those of the
-    // columns; the others fill a place that nothing reads.
-    uint32_t rs_lane = kNowhere, cs_lane = kNowhere;
-    const int rs_slot = wave < S::scale_slots ? wave : S::scale_slots + 1;
-    const int cs_slot = S::scale_slots + (wave == 0 ? 0 : 1);
-    if constexpr (S::FP8) {
-      if (wave * kWave + lane < S::BR) rs_lane = rs_at(wave * kWave + lane);
-      if (wave == 0 && lane < 2 * S::WC) cs_lane = cs_at(lane / 2, lane % 2);
-    }
-    const RReads rr(wr * S::FR * kFrag);
-    const CReads cr(wc * S::FC * kFrag);
-    const int steps = (int)((p.k_bytes + kStep - 1) / kStep);
-    const int first = steps > 0 ? p.turn % steps : 0;
-    // Steps past the last are copied too, as zeros from an empty buffer: every
-    // stage counts the same number of copies.
-    Source from;
-    const auto aim = [&](int at) {
-      const bool there = at < steps;
-      const int s = at + first < steps ? at + first : at + first - steps;
-      const int64_t left = p.k_bytes - (int64_t)s * kStep;
-      const int tail = left < kStep ? (int)left : kStep;
-      from.r = buffer_of(p.r + s * p.r_step, there ? p.r_size - s * p.r_step : 0);
-      from.c = buffer_of(p.c + s * p.c_step, there ? p.c_size - s * p.c_step : 0);
-      from.r_there = ro.before(tail);
-      from.c_there = co.before(tail);
-      if constexpr (S::FP8) {
-        from.rs = buffer_of((const uint8_t*)p.rs + 4 * s, there ? p.rs_size - 4 * s : 0);
-        from.cs = buffer_of((const uint8_t*)p.cs + 4 * s, there ? p.cs_size - 4 * s : 0);
+    if (!primed) {
+      // As many copies as there are when a first step begins.
+      feed = p;
+#pragma unroll
+      for (int s = 0; s < S::stages; ++s) {
+        aim(after, to_come);
+#pragma unroll
+        for (int i = 0; i < S::c_copies; ++i) copy_c(i, lds + s * S::stage_bytes);
+#pragma unroll
+        for (int i = 0; i < S::r_copies; ++i)
+          if (s < S::stages - 1 || i < early) copy_r(i, lds + s * S::stage_bytes);
       }
-    };
-    const auto copy_r = [&](int i, uint32_t to) {
-      if (i < ROperand::copies) ro.template load<false>(i, from.r, to, from.r_there);
-      else copy4(from.rs, rs_lane, to + S::scales_at + rs_slot * 256);
-    };
-    const auto copy_c = [&](int i, uint32_t to) {
-      if (i < COperand::copies)
-        co.template load<S::ONCE>(i, from.c, to + S::BR * kStep, from.c_there);
-      else
-        copy4(from.cs, cs_lane, to + S::scales_at + cs_slot * 256);
-    };
-    // As many as there are when a first step begins.
-#pragma unroll
-    for (int s = 0; s < S::stages; ++s) {
-      aim(s);
-#pragma unroll
-      for (int i = 0; i < S::c_copies; ++i) copy_c(i, lds + s * S::stage_bytes);
-#pragma unroll
-      for (int i = 0; i < S::r_copies; ++i)
-        if (s < S::stages - 1 || i < early) copy_r(i, lds + s * S::stage_bytes);
+      here = lds;
+      last = lds + (S::stages - 1) * S::stage_bytes;
+      settle<(S::stages - 2) * S::copies + S::c_copies + early>();
+      fetch_first(here);
     }
-    uint32_t here = lds, last = lds + (S::stages - 1) * S::stage_bytes;
-    settle<(S::stages - 2) * S::copies + S::c_copies + early>();
-    Fragments f;
-    fetch_first(f, here, rr, cr);
+    const int steps = p.steps();
     for (int s = 0; s < steps; ++s) {
       const uint32_t next =
           here == lds + (S::stages - 1) * S::stage_bytes ? lds : here + S::stage_bytes;
-      step(f, here, next, last, rr, cr, copy_r, copy_c, [&] { aim(s + S::stages); });
+      step(next, [&] { aim(after, to_come); });
       last = here;
       here = next;
     }
-    settle<0>();
+    if (!chained) settle<0>();
   }
 
   // Fragments on their way from LDS while the products before them run: in
   // turn two sets of 32 values of k; for e4m3 a step's fragments of columns and
   // in turn two of rows, with their scales.
-  struct Fragments {
+  struct {
     s16x8 a[2][S::FP8 ? 1 : S::FC], b[2][S::FP8 ? 1 : S::FR];
     i32x8 a8[S::FP8 ? S::FC : 1], b8[2];
     float sc[2], sr[2];
-  };
+  } f;
 
   // Part i of what the products of the kk-th 32 values of k need, in the order
   // in which they need it.
   static constexpr int parts = S::FC + S::FR;
-  __device__ __forceinline__ void fetch(Fragments& f, int i, uint32_t base, int kk,
-                                        const RReads& rr, const CReads& cr) {
+  __device__ __forceinline__ void fetch(int i, uint32_t base, int kk) {
     if (i < S::FC) f.a[kk][i] = cr.get(base + S::BR * kStep, i, kk);
     else f.b[kk][i - S::FC] = rr.get(base, i - S::FC, kk);
   }
-  __device__ __forceinline__ void fetch_row(Fragments& f, int i, uint32_t base, const RReads& rr) {
+  __device__ __forceinline__ void fetch_row(int i, uint32_t base) {
     f.b8[i % 2] = rr.get8(base, i);
-    f.sr[i % 2] = read_lds<float>(base + S::scales_at + ((wr * S::FR + i) * kFrag + lane_id() % 16) * 4);
+    f.sr[i % 2] = read_lds<float>(base + S::scales_at +
+                                  ((wr * S::FR + i) * kFrag + lane_id() % 16) * 4);
   }
-  __device__ __forceinline__ void fetch_column_scales(Fragments& f, uint32_t base) {
+  __device__ __forceinline__ void fetch_column_scales(uint32_t base) {
 #pragma unroll
     for (int j = 0; j < 2; ++j)
       f.sc[j] = read_lds<float>(base + S::scales_at + S::scale_slots * 256 + (wc * 2 + j) * 4);
   }
 
-  __device__ __forceinline__ void fetch_first(Fragments& f, uint32_t base, const RReads& rr,
-                                              const CReads& cr) {
+  __device__ __forceinline__ void fetch_first(uint32_t base) {
     if constexpr (!S::FP8) {
 #pragma unroll
-      for (int i = 0; i < parts; ++i) fetch(f, i, base, 0, rr, cr);
+      for (int i = 0; i < parts; ++i) fetch(i, base, 0);
     } else {
-      fetch_row(f, 0, base, rr);
-      fetch_column_scales(f, base);
+      fetch_row(0, base);
+      fetch_column_scales(base);
 #pragma unroll
       for (int j = 0; j < S::FC; ++j) f.a8[j] = cr.get8(base + S::BR * kStep, j);
     }
@@ -384,10 +421,8 @@ struct Tile {
   // arrived; then the copies of the step that is `stages` further, which aim()
   // finds, start in their place. They are spread over the products, since a
   // copy holds a wave up while the memory pipeline takes it.
-  template <typename FR_, typename FC_, typename A>
-  __device__ __forceinline__ void step(Fragments& f, uint32_t here, uint32_t next, uint32_t last,
-                                       const RReads& rr, const CReads& cr, FR_&& copy_r,
-                                       FC_&& copy_c, A&& aim) {
+  template <typename A>
+  __device__ __forceinline__ void step(uint32_t next, A&& aim) {
     constexpr int products = S::FR * S::FC;
     if constexpr (!S::FP8) {
       each<2>([&](auto half) {
@@ -398,7 +433,7 @@ struct Tile {
           // The reads before the barrier are through by then.
           constexpr int slots = kk ? products : (3 * products + 3) / 4;
           if constexpr (m < slots)
-            spread<parts, slots, m>([&](auto q) { fetch(f, q, kk ? next : here, 1 - kk, rr, cr); });
+            spread<parts, slots, m>([&](auto q) { fetch(q, kk ? next : here, 1 - kk); });
           if constexpr (kk == 0 && m == slots - 1) aim();
           if constexpr (kk == 1)
             spread<S::copies, products, m>([&](auto q) {
@@ -433,9 +468,9 @@ struct Tile {
           asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" : : : "memory");
         if constexpr (turned) {
           settle<(S::stages - 2) * S::copies + (columns_first ? S::c_copies : 0)>();
-          fetch_column_scales(f, next);
+          fetch_column_scales(next);
         } else {
-          fetch_row(f, i + 1, here, rr);
+          fetch_row(i + 1, here);
         }
         each<S::FC>([&](auto column) {
           constexpr int j = column, m = i * S::FC + j;
@@ -458,7 +493,7 @@ struct Tile {
           __builtin_amdgcn_sched_barrier(0);
         });
       });
-      fetch_row(f, 0, next, rr);
+      fetch_row(0, next);
       each<behind>([&](auto b) { scale(std::integral_constant<int, products - behind + b>{}); });
     }
   }
@@ -549,6 +584,69 @@ inline int64_t tile_grid(const Groups& g, int br, int64_t cols) {
     blocks = g.most / br + (experts < g.most ? experts : g.most);
   return (blocks * cols + 7) / 8 * 8;
 }
+
+// The tiles of a workgroup that takes one after the other, on the line that
+// find_tile describes; `ends` (experts + 1 numbers in LDS): row blocks before
+// the end of each expert's.
+template <int BR, int THREADS>
+struct Line {
+  const Groups& g;
+  int* ends;
+  int experts, cols, place;  // place: of the workgroup's next tile in its XCD's stretch
+  int64_t tiles, stretch;
+
+  __device__ __forceinline__ Line(const Groups& g, int cols, int* ends)
+      : g(g), ends(ends), experts(g.N * g.L), cols(cols), place(blockIdx.x / 8) {
+    __shared__ int wave_sum[THREADS / kWave];
+    const int tid = threadIdx.x, lane = lane_id();
+    int total = 0;
+    for (int e0 = 0; e0 < experts; e0 += THREADS) {
+      const int e = e0 + tid;
+      int sum = e < experts ? (group_of(g, e).rows + BR - 1) / BR : 0;
+#pragma unroll
+      for (int off = 1; off < kWave; off <<= 1) {
+        const int up = __shfl_up(sum, off);
+        if (lane >= off) sum += up;
+      }
+      if (lane == kWave - 1) wave_sum[tid / kWave] = sum;
+      __syncthreads();
+      int all = 0;
+      for (int w = 0; w < THREADS / kWave; ++w) {
+        if (w < tid / kWave) sum += wave_sum[w];
+        all += wave_sum[w];
+      }
+      if (e < experts) ends[e] = total + sum;
+      total += all;
+      __syncthreads();
+    }
+    tiles = (int64_t)wave_uniform(total) * cols;
+    stretch = (tiles + 7) / 8;
+  }
+
+  // The workgroup's next tile; false: none is left.
+  __device__ __forceinline__ bool next(Where* out) {
+    const int64_t want = (int64_t)(blockIdx.x % 8) * stretch + place;
+    if (place >= stretch || want >= tiles) return false;
+    place += gridDim.x / 8;
+    const int block = (int)(want / cols);  // row blocks of whole groups lie before it
+    int e = 0;
+    for (int e0 = 0; e0 < experts; e0 += kWave)
+      e += __popcll(ballot(e0 + lane_id() < experts && ends[e0 + lane_id()] <= block));
+    e = wave_uniform(e);
+    const Group gr = group_of(g, e);
+    const int blocks = wave_uniform((gr.rows + BR - 1) / BR), first = wave_uniform(gr.first);
+    const int start = wave_uniform(e > 0 ? ends[e - 1] : 0), rows = wave_uniform(gr.rows);
+    const int at = (int)(want - (int64_t)start * cols), stripe = at / (blocks * 8);
+    const int wide = cols - stripe * 8 < 8 ? cols - stripe * 8 : 8;
+    const int in = at - stripe * blocks * 8, rb = in / wide;
+    *out = Where{e, first + rb * BR, rows - rb * BR < BR ? rows - rb * BR : BR, rb * BR,
+                 stripe * 8 + in % wide};
+    return true;
+  }
+};
+
+// Workgroups for a line: one per CU, or as many as there are tiles.
+inline unsigned line_grid(int64_t tiles) { return (unsigned)(tiles < 256 ? tiles : 256); }
 
 __device__ __forceinline__ uint32_t lds_base(const void* p) {
   return (uint32_t)(uintptr_t)(const lds_u8*)p;

@@ -149,102 +149,136 @@ struct NoScale {
   __device__ __forceinline__ uint32_t operator()(int, int = 0) const { return kNowhere; }
 };
 
-// dx[r][c] = sum over n of dz[r][n] w[n][c].
+// A tile's output: rows [0, rows) of `out`, columns [c0, cols) of a line of them.
 template <typename S>
-__device__ __forceinline__ void rows_tile(const GradArgs& a, const Where& t, uint32_t lds) {
-  const int c0 = t.col * S::BC;
-  const int64_t line = (int64_t)a.W * 2, w_line = (int64_t)a.in * 2;
-  Pair p;
-  p.r = (const uint8_t*)a.dz + t.first * line;
-  p.r_size = t.rows * line;
-  p.r_step = kStep;
-  p.c = (const uint8_t*)a.w + (int64_t)t.expert * a.W * w_line + c0 * 2;
-  p.c_size = a.W * w_line - c0 * 2;
-  p.c_step = kStep / 2 * w_line;
-  p.r_line = (uint32_t)line;
-  p.c_line = (uint32_t)w_line;
-  p.turn = t.col % 8;
-  p.k_bytes = line;
-  p.rs = p.cs = nullptr;
-  p.rs_size = p.cs_size = 0;
-  Tile<S> tile;
-  tile.run(p, lds, [&](int r) { return (uint32_t)(r * line); },
-           [&](int r) { return (uint32_t)(r * w_line); }, NoScale{}, NoScale{});
+__device__ __forceinline__ void write_tile(const Tile<S>& tile, uint16_t* out, int rows, int c0,
+                                           int cols) {
   const int lane = lane_id();
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
     const int r = (tile.wr * S::FR + i) * kFrag + lane % 16;
-    if (r >= t.rows) continue;
-    uint16_t* o = a.dx + (int64_t)(t.first + r) * a.in;
+    if (r >= rows) continue;
+    uint16_t* o = out + (int64_t)r * cols;
 #pragma unroll
     for (int j = 0; j < S::FC; ++j) {
       const int c = c0 + (tile.wc * S::FC + j) * kFrag + lane / 16 * 4;
       const float v[4] = {tile.acc[i][j][0], tile.acc[i][j][1], tile.acc[i][j][2],
                           tile.acc[i][j][3]};
-      if (c < a.in) store4(o + c, v);
+      if (c < cols) store4(o + c, v);
     }
   }
 }
 
 template <int FR, bool ONCE>
 using RowsShape = Shape<2, FR, 4, 4, false, true, false, 2, ONCE>;
+using RowsLine = Line<RowsShape<8, false>::BR, RowsShape<8, false>::threads>;
+
+// dx[r][c] = sum over n of dz[r][n] w[n][c], for tiles of more than MIN and at
+// most S::BR rows, from t on, while the line has such ones. Returns whether t is
+// then a tile of another height.
+template <typename S, int MIN>
+__device__ __forceinline__ bool rows_tiles(const GradArgs& a, RowsLine& line_, Where& t,
+                                           uint32_t lds) {
+  const int line = a.W * 2, w_line = a.in * 2;
+  const auto feed_of = [&](const Where& w) {
+    Feed p;
+    p.r = (const uint8_t*)a.dz + (int64_t)w.first * line;
+    p.r_size = w.rows * line;
+    p.r_off = 0;
+    p.c_off = w.col * S::BC * 2;
+    p.c = (const uint8_t*)a.w + (int64_t)w.expert * a.W * w_line + p.c_off;
+    p.c_size = 0;
+    p.left = line;
+    p.rs = p.cs = nullptr;
+    p.rs_size = p.cs_size = 0;
+    return p;
+  };
+  Tile<S> tile(
+      lds, line, w_line, [&](int r) { return (uint32_t)(r * line); },
+      [&](int r) { return (uint32_t)(r * w_line); }, NoScale{}, NoScale{});
+  Feed p = feed_of(t);
+  const bool long_enough = p.steps() >= S::stages;
+  for (bool primed = false;;) {
+    Where n = t;
+    const bool more = line_.next(&n);
+    const bool same = more && n.rows > MIN && n.rows <= S::BR, chained = same && long_enough;
+    const Feed after = feed_of(n);
+    tile.run(p, primed, after, chained);
+    write_tile(tile, a.dx + (int64_t)t.first * a.in, t.rows, t.col * S::BC, a.in);
+    t = n;
+    if (!same) return more;
+    p = after;
+    primed = chained;
+  }
+}
 
 __global__ __launch_bounds__(512) void rows_grad_kernel(GradArgs a) {
   using S = RowsShape<8, false>;
-  static_assert(S::threads == 512, "");
+  static_assert(S::threads == 512, "one size for all heights");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
+  extern __shared__ int ends[];
+  RowsLine line(a.g, a.cols, ends);
   Where t;
-  if (!find_tile<S::BR, S::threads>(a.g, a.cols, &t)) return;
-  if (t.rows <= 64) rows_tile<RowsShape<2, true>>(a, t, lds_base(lds));
-  else if (t.rows <= 128) rows_tile<RowsShape<4, true>>(a, t, lds_base(lds));
-  else if (t.rows <= 192) rows_tile<RowsShape<6, true>>(a, t, lds_base(lds));
-  else rows_tile<S>(a, t, lds_base(lds));
+  bool more = line.next(&t);
+  while (more) {
+    if (t.rows <= 64) more = rows_tiles<RowsShape<2, true>, 0>(a, line, t, lds_base(lds));
+    else if (t.rows <= 128) more = rows_tiles<RowsShape<4, true>, 64>(a, line, t, lds_base(lds));
+    else if (t.rows <= 192) more = rows_tiles<RowsShape<6, true>, 128>(a, line, t, lds_base(lds));
+    else more = rows_tiles<S, 192>(a, line, t, lds_base(lds));
+  }
 }
 
-// dw[n][c] = sum over the expert's rows r of dz[r][n] x[r][c].
+// dw[n][c] = sum over the expert's rows r of dz[r][n] x[r][c]. The experts'
+// tiles lie on a line that the XCDs share, as in find_tile.
 template <typename S>
 __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
-  // The experts' tiles lie on a line that the XCDs share, as in find_tile.
   const int tiles = a.rows * a.cols, all = tiles * a.g.N * a.g.L, stretch = (all + 7) / 8;
-  const int slot = blockIdx.x / 8, want = blockIdx.x % 8 * stretch + slot;
-  if (slot >= stretch || want >= all) return;
-  const int e = want / tiles, at = want - e * tiles, stripe = at / (a.rows * 8);
-  const int wide = a.cols - stripe * 8 < 8 ? a.cols - stripe * 8 : 8;
-  const int in = at - stripe * a.rows * 8;
-  const int r0 = in / wide * S::BR, c0 = (stripe * 8 + in % wide) * S::BC;
-  const Group g = group_of(a.g, e);
-  const int first = wave_uniform(g.first), rows = wave_uniform(g.rows);
-  const int64_t line = (int64_t)a.W * 2, x_line = (int64_t)a.in * 2;
-  Pair p;
-  p.r = (const uint8_t*)a.dz + first * line + r0 * 2;
-  p.r_size = rows * line - r0 * 2;
-  p.r_step = kStep / 2 * line;
-  p.c = (const uint8_t*)a.x + first * x_line + c0 * 2;
-  p.c_size = rows * x_line - c0 * 2;
-  p.c_step = kStep / 2 * x_line;
-  p.r_line = (uint32_t)line;
-  p.c_line = (uint32_t)x_line;
-  p.turn = 0;
-  p.k_bytes = (int64_t)rows * 2;
-  p.rs = p.cs = nullptr;
-  p.rs_size = p.cs_size = 0;
-  Tile<S> tile;
-  tile.run(p, lds_base(lds), [&](int r) { return (uint32_t)(r * line); },
-           [&](int r) { return (uint32_t)(r * x_line); }, NoScale{}, NoScale{});
-  const int lane = lane_id();
-#pragma unroll
-  for (int i = 0; i < S::FR; ++i) {
-    const int r = r0 + (tile.wr * S::FR + i) * kFrag + lane % 16;
-    if (r >= a.W) continue;
-    uint16_t* o = a.dw + ((int64_t)e * a.W + r) * a.in;
-#pragma unroll
-    for (int j = 0; j < S::FC; ++j) {
-      const int c = c0 + (tile.wc * S::FC + j) * kFrag + lane / 16 * 4;
-      const float v[4] = {tile.acc[i][j][0], tile.acc[i][j][1], tile.acc[i][j][2],
-                          tile.acc[i][j][3]};
-      if (c < a.in) store4(o + c, v);
-    }
+  const int line = a.W * 2, x_line = a.in * 2;
+  struct At {
+    int e, r0, c0;
+  };
+  const auto place_of = [&](int want) {
+    const int e = want / tiles, at = want - e * tiles, stripe = at / (a.rows * 8);
+    const int wide = a.cols - stripe * 8 < 8 ? a.cols - stripe * 8 : 8;
+    const int in = at - stripe * a.rows * 8;
+    return At{e, in / wide * S::BR, (stripe * 8 + in % wide) * S::BC};
+  };
+  const auto feed_of = [&](const At& w) {
+    const Group g = group_of(a.g, w.e);
+    const int first = wave_uniform(g.first), rows = wave_uniform(g.rows);
+    Feed p;
+    p.r_off = w.r0 * 2;
+    p.c_off = w.c0 * 2;
+    p.r = (const uint8_t*)a.dz + (int64_t)first * line + p.r_off;
+    p.c = (const uint8_t*)a.x + (int64_t)first * x_line + p.c_off;
+    p.r_size = p.c_size = 0;
+    p.left = rows * 2;
+    p.rs = p.cs = nullptr;
+    p.rs_size = p.cs_size = 0;
+    return p;
+  };
+  const int end = min(all, ((int)blockIdx.x % 8 + 1) * stretch);
+  int want = blockIdx.x % 8 * stretch + blockIdx.x / 8;
+  if (want >= end) return;
+  Tile<S> tile(
+      lds_base(lds), line, x_line,
+      [&](int r) { return (uint32_t)(r * line); }, [&](int r) { return (uint32_t)(r * x_line); },
+      NoScale{}, NoScale{});
+  At t = place_of(want);
+  Feed p = feed_of(t);
+  for (bool primed = false;;) {
+    want += gridDim.x / 8;
+    const bool more = want < end;
+    const At n = more ? place_of(want) : t;
+    const Feed after = feed_of(n);
+    const bool chained = more && after.steps() >= S::stages;
+    tile.run(p, primed, after, chained);
+    write_tile(tile, a.dw + ((int64_t)t.e * a.W + t.r0) * a.in, a.W - t.r0, t.c0, a.in);
+    if (!more) return;
+    t = n;
+    p = after;
+    primed = chained;
   }
 }
 
@@ -331,15 +365,15 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
   if (dx && g.most > 0) {
     using S = RowsShape<8, false>;
     a.cols = (p.in + S::BC - 1) / S::BC;
-    hipLaunchKernelGGL(rows_grad_kernel, dim3((unsigned)tile_grid(g, S::BR, a.cols)),
-                       dim3(S::threads), 0, stream, a);
+    hipLaunchKernelGGL(rows_grad_kernel, dim3(line_grid(tile_grid(g, S::BR, a.cols))),
+                       dim3(S::threads), (size_t)experts * 4, stream, a);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
   if (dw) {
     a.cols = (p.in + WeightsShape::BC - 1) / WeightsShape::BC;
     hipLaunchKernelGGL(weights_grad_kernel<WeightsShape>,
-                       dim3((unsigned)((experts * a.rows * a.cols + 7) / 8 * 8)),
+                       dim3(line_grid(((int64_t)experts * a.rows * a.cols + 7) / 8 * 8)),
                        dim3(WeightsShape::threads), 0,
                        stream, a);
     e = hipGetLastError();
