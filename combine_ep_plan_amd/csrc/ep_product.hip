@@ -22,18 +22,6 @@ __device__ __forceinline__ float activate(float z) {
   return z;
 }
 
-__device__ __forceinline__ void add4(float (&v)[4], const uint16_t* p) {
-  const uint2 u = *(const uint2*)p;
-  v[0] += bf16_lo(u.x);
-  v[1] += bf16_hi(u.x);
-  v[2] += bf16_lo(u.y);
-  v[3] += bf16_hi(u.y);
-}
-
-__device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
-  *(uint2*)p = uint2{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3])};
-}
-
 // A tile's output. Fragments of a SwiGLU tile alternate: 16 gate rows of w, the
 // 16 up rows of the same columns; a lane then holds both of a column.
 template <typename S, int ACT>
@@ -45,31 +33,29 @@ __device__ __forceinline__ void write_tile(const FwdArgs& a, const Tile<S>& tile
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
     const int r = (tile.wr * S::FR + i) * kFrag + lane % 16;
-    if (r >= t.rows) continue;
+    const bool there = r < t.rows;
     const int64_t row = t.first + r;
 #pragma unroll
-    for (int j = 0; j < S::FC; j += glu ? 2 : 1) {
-      const int f = tile.wc * S::FC + j, c = c0 + (glu ? f / 2 : f) * kFrag + lane / 16 * 4;
-      if (c >= a.n) continue;
-      float z[4], y[4];
-#pragma unroll
-      for (int v = 0; v < 4; ++v) z[v] = tile.acc[i][j][v];
-      if (bias) add4(z, bias + c);
-      if (a.pre) store4(a.pre + row * wrows + c, z);
+    for (int j = 0; j < S::FC; j += glu ? 4 : 2) {
+      const int f = tile.wc * S::FC + j, c = c0 + (glu ? f / 2 : f) * kFrag + column_of_lane();
+      float y[8];
+      eight_columns(tile.acc[i][j], tile.acc[i][j + (glu ? 2 : 1)], y);
+      float up[8];
+      if constexpr (glu) eight_columns(tile.acc[i][j + 1], tile.acc[i][j + 3], up);
+      if (!there || c >= a.n) continue;
+      if (bias) add8(y, bias + c);
+      if (a.pre) store8(a.pre + row * wrows + c, y);
       if constexpr (glu) {
-        float up[4];
+        if (bias) add8(up, bias + a.n + c);
+        if (a.pre) store8(a.pre + row * wrows + a.n + c, up);
 #pragma unroll
-        for (int v = 0; v < 4; ++v) up[v] = tile.acc[i][j + 1][v];
-        if (bias) add4(up, bias + a.n + c);
-        if (a.pre) store4(a.pre + row * wrows + a.n + c, up);
-#pragma unroll
-        for (int v = 0; v < 4; ++v) y[v] = activate<EP_ACT_SILU>(z[v]) * up[v];
+        for (int v = 0; v < 8; ++v) y[v] = activate<EP_ACT_SILU>(y[v]) * up[v];
       } else {
 #pragma unroll
-        for (int v = 0; v < 4; ++v) y[v] = activate<ACT>(z[v]);
+        for (int v = 0; v < 8; ++v) y[v] = activate<ACT>(y[v]);
       }
-      if (a.residual) add4(y, a.residual + row * a.n + c);
-      store4(a.out + row * a.n + c, y);
+      if (a.residual) add8(y, a.residual + row * a.n + c);
+      store8(a.out + row * a.n + c, y);
     }
   }
 }

@@ -499,6 +499,37 @@ struct Tile {
   }
 };
 
+// Two neighbouring fragments' registers, turned so that a lane holds eight
+// neighbouring columns of its row: lanes of odd groups of 16 swap the first
+// fragment's values for the second's of the group before. The columns are
+// 8 (group / 2) ... of fragment group % 2. Outputs then go out 16 bytes at a
+// time and 64 in a row.
+__device__ __forceinline__ void eight_columns(const f32x4& a, const f32x4& b, float (&v)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const auto x = __builtin_amdgcn_permlane16_swap(__float_as_uint(a[i]), __float_as_uint(b[i]),
+                                                    false, false);
+    v[i] = __uint_as_float(x[0]);
+    v[4 + i] = __uint_as_float(x[1]);
+  }
+}
+__device__ __forceinline__ int column_of_lane() {
+  return lane_id() / 16 % 2 * kFrag + lane_id() / 32 * 8;
+}
+
+__device__ __forceinline__ void add8(float (&v)[8], const uint16_t* p) {
+  const u32x4 u = *(const u32x4*)p;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] += bf16_lo(u[i]);
+    v[2 * i + 1] += bf16_hi(u[i]);
+  }
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  *(u32x4*)p = u32x4{pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]), pack_bf16(v[4], v[5]),
+                     pack_bf16(v[6], v[7])};
+}
+
 // Rows [first, first + rows) of the grouped buffers.
 struct Group {
   int first, rows;

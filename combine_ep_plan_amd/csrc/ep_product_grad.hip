@@ -157,14 +157,13 @@ __device__ __forceinline__ void write_tile(const Tile<S>& tile, uint16_t* out, i
 #pragma unroll
   for (int i = 0; i < S::FR; ++i) {
     const int r = (tile.wr * S::FR + i) * kFrag + lane % 16;
-    if (r >= rows) continue;
     uint16_t* o = out + (int64_t)r * cols;
 #pragma unroll
-    for (int j = 0; j < S::FC; ++j) {
-      const int c = c0 + (tile.wc * S::FC + j) * kFrag + lane / 16 * 4;
-      const float v[4] = {tile.acc[i][j][0], tile.acc[i][j][1], tile.acc[i][j][2],
-                          tile.acc[i][j][3]};
-      if (c < cols) store4(o + c, v);
+    for (int j = 0; j < S::FC; j += 2) {
+      const int c = c0 + (tile.wc * S::FC + j) * kFrag + column_of_lane();
+      float v[8];
+      eight_columns(tile.acc[i][j], tile.acc[i][j + 1], v);
+      if (r < rows && c < cols) store8(o + c, v);
     }
   }
 }
