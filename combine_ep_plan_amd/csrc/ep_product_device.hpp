@@ -616,18 +616,45 @@ inline int64_t tile_grid(const Groups& g, int br, int64_t cols) {
   return (blocks * cols + 7) / 8 * 8;
 }
 
-// The tiles of a workgroup that takes one after the other, on the line that
-// find_tile describes; `ends` (experts + 1 numbers in LDS): row blocks before
-// the end of each expert's.
+// A workgroup's i-th tile on a line of `all`, or -1: the XCDs take turns with
+// as many neighbouring tiles as they have workgroups, so that what several of
+// them read is still in the memory-side cache, and share what is left at the
+// end evenly.
+__device__ __forceinline__ int64_t tile_of(int i, int64_t all) {
+  const int slots = gridDim.x / 8, xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
+  const int64_t before = (int64_t)i * 8 * slots, left = all - before;
+  if (left >= 8 * slots) return before + xcd * slots + slot;
+  const int each = (int)((left + 7) / 8);
+  return left > 0 && slot < each && xcd * each + slot < left ? before + xcd * each + slot : -1;
+}
+
+// Row block and column block of the at-th tile of blocks x cols: the tiles go by
+// stripes of 16 columns, in those by four rows, in those by 8 columns, so that
+// 32 neighbours, an XCD's at one time, are 4 x 8 and need 12 blocks of operands.
+struct RowCol {
+  int row, col;
+};
+__device__ __forceinline__ RowCol place_of(int at, int blocks, int cols) {
+  const int stripe = at / (blocks * 16), in = at - stripe * blocks * 16;
+  const int wide = cols - stripe * 16 < 16 ? cols - stripe * 16 : 16;
+  const int four = in / (4 * wide), rows = blocks - 4 * four < 4 ? blocks - 4 * four : 4;
+  const int left = wide < 8 ? wide : 8, i = in - four * 4 * wide, j = i - rows * left;
+  return j < 0 ? RowCol{4 * four + i / left, stripe * 16 + i % left}
+               : RowCol{4 * four + j / (wide - left), stripe * 16 + left + j % (wide - left)};
+}
+
+// The tiles of a workgroup that takes one after the other. The groups' tiles
+// lie on the line as find_tile describes; `ends` (a number per expert, in LDS):
+// row blocks before the end of each expert's.
 template <int BR, int THREADS>
 struct Line {
   const Groups& g;
   int* ends;
-  int experts, cols, place;  // place: of the workgroup's next tile in its XCD's stretch
-  int64_t tiles, stretch;
+  int experts, cols, taken;  // taken: tiles that the workgroup has had
+  int64_t tiles;
 
   __device__ __forceinline__ Line(const Groups& g, int cols, int* ends)
-      : g(g), ends(ends), experts(g.N * g.L), cols(cols), place(blockIdx.x / 8) {
+      : g(g), ends(ends), experts(g.N * g.L), cols(cols), taken(0) {
     __shared__ int wave_sum[THREADS / kWave];
     const int tid = threadIdx.x, lane = lane_id();
     int total = 0;
@@ -651,14 +678,13 @@ struct Line {
       __syncthreads();
     }
     tiles = (int64_t)wave_uniform(total) * cols;
-    stretch = (tiles + 7) / 8;
   }
 
   // The workgroup's next tile; false: none is left.
   __device__ __forceinline__ bool next(Where* out) {
-    const int64_t want = (int64_t)(blockIdx.x % 8) * stretch + place;
-    if (place >= stretch || want >= tiles) return false;
-    place += gridDim.x / 8;
+    const int64_t want = tile_of(taken, tiles);
+    if (want < 0) return false;
+    ++taken;
     const int block = (int)(want / cols);  // row blocks of whole groups lie before it
     int e = 0;
     for (int e0 = 0; e0 < experts; e0 += kWave)
@@ -667,11 +693,9 @@ struct Line {
     const Group gr = group_of(g, e);
     const int blocks = wave_uniform((gr.rows + BR - 1) / BR), first = wave_uniform(gr.first);
     const int start = wave_uniform(e > 0 ? ends[e - 1] : 0), rows = wave_uniform(gr.rows);
-    const int at = (int)(want - (int64_t)start * cols), stripe = at / (blocks * 8);
-    const int wide = cols - stripe * 8 < 8 ? cols - stripe * 8 : 8;
-    const int in = at - stripe * blocks * 8, rb = in / wide;
-    *out = Where{e, first + rb * BR, rows - rb * BR < BR ? rows - rb * BR : BR, rb * BR,
-                 stripe * 8 + in % wide};
+    const RowCol rc = place_of((int)(want - (int64_t)start * cols), blocks, cols);
+    const int at = rc.row * BR;
+    *out = Where{e, first + at, rows - at < BR ? rows - at : BR, at, rc.col};
     return true;
   }
 };

@@ -228,20 +228,19 @@ __global__ __launch_bounds__(512) void rows_grad_kernel(GradArgs a) {
 }
 
 // dw[n][c] = sum over the expert's rows r of dz[r][n] x[r][c]. The experts'
-// tiles lie on a line that the XCDs share, as in find_tile.
+// tiles lie on a line, as those of the rows do.
 template <typename S>
 __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
-  const int tiles = a.rows * a.cols, all = tiles * a.g.N * a.g.L, stretch = (all + 7) / 8;
+  const int tiles = a.rows * a.cols, all = tiles * a.g.N * a.g.L;
   const int line = a.W * 2, x_line = a.in * 2;
   struct At {
     int e, r0, c0;
   };
-  const auto place_of = [&](int want) {
-    const int e = want / tiles, at = want - e * tiles, stripe = at / (a.rows * 8);
-    const int wide = a.cols - stripe * 8 < 8 ? a.cols - stripe * 8 : 8;
-    const int in = at - stripe * a.rows * 8;
-    return At{e, in / wide * S::BR, (stripe * 8 + in % wide) * S::BC};
+  const auto at_of = [&](int want) {
+    const int e = want / tiles;
+    const RowCol rc = place_of(want - e * tiles, a.rows, a.cols);
+    return At{e, rc.row * S::BR, rc.col * S::BC};
   };
   const auto feed_of = [&](const At& w) {
     const Group g = group_of(a.g, w.e);
@@ -257,19 +256,19 @@ __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
     p.rs_size = p.cs_size = 0;
     return p;
   };
-  const int end = min(all, ((int)blockIdx.x % 8 + 1) * stretch);
-  int want = blockIdx.x % 8 * stretch + blockIdx.x / 8;
-  if (want >= end) return;
+  int64_t want = tile_of(0, all);
+  if (want < 0) return;
   Tile<S> tile(
       lds_base(lds), line, x_line,
       [&](int r) { return (uint32_t)(r * line); }, [&](int r) { return (uint32_t)(r * x_line); },
       NoScale{}, NoScale{});
-  At t = place_of(want);
+  At t = at_of((int)want);
   Feed p = feed_of(t);
-  for (bool primed = false;;) {
-    want += gridDim.x / 8;
-    const bool more = want < end;
-    const At n = more ? place_of(want) : t;
+  int taken = 1;
+  for (bool primed = false;; ++taken) {
+    want = tile_of(taken, all);
+    const bool more = want >= 0;
+    const At n = more ? at_of((int)want) : t;
     const Feed after = feed_of(n);
     const bool chained = more && after.steps() >= S::stages;
     tile.run(p, primed, after, chained);
