@@ -159,9 +159,8 @@ hipError_t launch_kv_attend(const ep_kv_cache& c, const ep_kv_batch& b, const ep
                             int max_new, const ep_rows& q, int n_heads, const ep_rows& out,
                             float* lse, float sm_scale, void* ws, int32_t* status,
                             hipStream_t stream);
-// RMS norm. Threads of the workgroup that holds a row of `hidden` values, and
-// workgroups (each with its own partial dweight row) of the backward pass.
-int norm_threads(int hidden);
+// RMS norm. norm_grad_parts: workgroups of the backward pass, each with a
+// partial row of dweight.
 int norm_grad_parts(const ep_norm& n);
 hipError_t launch_rms_norm(const ep_norm& n, const void* x, const void* residual, void* sum,
                            void* y, uint8_t* codes, float* scales, hipStream_t stream);

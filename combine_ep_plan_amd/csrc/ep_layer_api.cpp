@@ -74,9 +74,6 @@ int check_norm(const ep_norm* n) {
     return fail(EP_ERR_UNSUPPORTED, "norm: hidden must be at most EP_NORM_MAX_HIDDEN");
   if (n->rows >= ((int64_t)1 << 31))
     return fail(EP_ERR_UNSUPPORTED, "norm: rows must be < 2^31");
-  // A workgroup of up to 1024 threads per row; a launch holds 2^32 threads.
-  if (n->rows * ep::norm_threads(n->hidden) >= ((int64_t)1 << 32))
-    return fail(EP_ERR_UNSUPPORTED, "norm: too many rows for one launch");
   return EP_OK;
 }
 

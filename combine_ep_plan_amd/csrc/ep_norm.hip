@@ -238,20 +238,36 @@ __global__ __launch_bounds__(1024) void norm_weight_kernel(const float* parts, f
 // the 896 chunks of 7168 values fill seven waves.
 int chunks_per_thread(int hidden) { return hidden / 8 <= 2048 ? 2 : 4; }
 
+// Threads of the workgroup that holds a row.
+int norm_threads(int hidden) {
+  const int per_wave = kWave * chunks_per_thread(hidden);
+  return kWave * ((hidden / 8 + per_wave - 1) / per_wave);
+}
+
+// A launch holds fewer than 2^32 threads, of at most 1024 per row; more rows
+// go in several launches.
+constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
+
 template <int DT, int V>
 hipError_t run_norm(const ep_norm& n, const void* x, const void* residual, void* sum, void* y,
                     uint8_t* codes, float* scales, hipStream_t stream) {
-  const dim3 grid((unsigned)n.rows), block(norm_threads(n.hidden));
-  const float per = 1.0f / (float)n.hidden;
-  if (codes)
-    hipLaunchKernelGGL((norm_kernel<DT, V, true>), grid, block, 0, stream, (const u32x4*)x,
-                       (const u32x4*)residual, (const u32x4*)n.weight, (u32x4*)sum, (u32x4*)y,
-                       (uint2*)codes, scales, n.hidden / 8, per, n.eps);
-  else
-    hipLaunchKernelGGL((norm_kernel<DT, V, false>), grid, block, 0, stream, (const u32x4*)x,
-                       (const u32x4*)residual, (const u32x4*)n.weight, (u32x4*)sum, (u32x4*)y,
-                       nullptr, nullptr, n.hidden / 8, per, n.eps);
-  return hipGetLastError();
+  const dim3 block(norm_threads(n.hidden));
+  const int n16 = n.hidden / 8;
+  const auto kernel = codes ? norm_kernel<DT, V, true> : norm_kernel<DT, V, false>;
+  const auto from = [&](const void* p, int64_t row) {
+    return p ? (u32x4*)const_cast<void*>(p) + row * n16 : nullptr;
+  };
+  for (int64_t row = 0; row < n.rows; row += kRowsPerLaunch) {
+    const int64_t rows = n.rows - row < kRowsPerLaunch ? n.rows - row : kRowsPerLaunch;
+    hipLaunchKernelGGL(kernel, dim3((unsigned)rows), block, 0, stream, from(x, row),
+                       from(residual, row), (const u32x4*)n.weight, from(sum, row), from(y, row),
+                       codes ? (uint2*)codes + row * n16 : nullptr,
+                       scales ? scales + row * (n16 / 16) : nullptr, n16,
+                       1.0f / (float)n.hidden, n.eps);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <int DT>
@@ -262,11 +278,6 @@ auto grad_kernel(int hidden) {
 }
 
 }  // namespace
-
-int norm_threads(int hidden) {
-  const int per_wave = kWave * chunks_per_thread(hidden);
-  return kWave * ((hidden / 8 + per_wave - 1) / per_wave);
-}
 
 // Workgroups that together fill the chip with 1024 threads per CU, a multiple
 // of its 256 CUs; no more than rows.
