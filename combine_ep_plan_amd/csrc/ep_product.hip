@@ -157,11 +157,28 @@ hipError_t run(FwdArgs a, int act, hipStream_t stream) {
 template <int FR, bool FP8, int STAGES, bool ONCE = true>
 using Rows = Shape<2, FR, 4, 4, false, false, FP8, STAGES, ONCE>;
 
+// Tiles of fewer rows and columns, with more steps on their way.
 template <bool FP8>
-hipError_t by_rows(const FwdArgs& a, int act, hipStream_t stream) {
-  const int64_t mean = a.g.most / (a.g.N * a.g.L);
-  if (mean <= 24) return run<Shape<1, 2, 2, 4, false, false, FP8, 4, true>>(a, act, stream);
-  return run<Rows<8, FP8, 2, false>, Rows<2, FP8, 3>, Rows<4, FP8, 3>, Rows<6, FP8, 2>>(a, act, stream);
+using Small = Shape<2, 4, 2, 4, false, false, FP8, 4>;        // 128 x 128
+template <bool FP8>
+using Flat = Shape<1, 2, 2, 4, false, false, FP8, 4, true>;   // 32 x 128
+template <bool FP8>
+using Thin = Shape<1, 2, 1, 4, false, false, FP8, 5, true>;   // 32 x 64
+
+// The tiles that cost least, of equals the smallest. Rows of 7168 values by
+// 4096 columns: 2048 rows take 173 us in the large ones and 138 in 128 x 128; 256
+// rows 178, 71, 52 and 73 in the four; 64 rows 91, 60, 51 and 38. 2048 rows of
+// 2048 values by 7168 columns: 62, 84, 187 and 307.
+template <bool FP8>
+hipError_t by_cost(const FwdArgs& a, int act, hipStream_t stream) {
+  using Large = Rows<8, FP8, 2, false>;
+  const int64_t cols = act == EP_ACT_SWIGLU ? 2 * a.n : a.n;
+  const int64_t large = cost_of(a.g, 256, 64, 256, cols), small = cost_of(a.g, 128, 128, 128, cols),
+                flat = cost_of(a.g, 32, 32, 128, cols), thin = cost_of(a.g, 32, 32, 64, cols);
+  if (thin <= flat && thin <= small && thin <= large) return run<Thin<FP8>>(a, act, stream);
+  if (flat <= small && flat <= large) return run<Flat<FP8>>(a, act, stream);
+  if (small <= large) return run<Small<FP8>>(a, act, stream);
+  return run<Large, Rows<2, FP8, 3>, Rows<4, FP8, 3>, Rows<6, FP8, 2>>(a, act, stream);
 }
 
 }  // namespace
@@ -181,8 +198,8 @@ hipError_t launch_product(const ep_product& p, const Groups& g, const void* cons
   a.in = p.in;
   a.n = p.out;
   a.cols = 0;
-  return p.dtype == EP_DTYPE_E4M3 ? by_rows<true>(a, p.act, stream)
-                                  : by_rows<false>(a, p.act, stream);
+  return p.dtype == EP_DTYPE_E4M3 ? by_cost<true>(a, p.act, stream)
+                                  : by_cost<false>(a, p.act, stream);
 }
 
 }  // namespace ep

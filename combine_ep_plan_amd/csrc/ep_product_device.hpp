@@ -15,6 +15,7 @@
 // compute what nothing stores.
 #pragma once
 
+#include <cmath>
 #include <utility>
 
 #include "ep_device.hpp"
@@ -75,6 +76,7 @@ __device__ __forceinline__ void copy4(const u32x4& from, uint32_t at, uint32_t t
 // then all waves' (barrier).
 template <int N>
 __device__ __forceinline__ void settle() {
+  static_assert(N <= 63, "the wait counts to 63");
   asm volatile("s_waitcnt vmcnt(%0) lgkmcnt(0)\n\ts_barrier" : : "n"(N) : "memory");
 }
 
@@ -699,6 +701,26 @@ struct Line {
     return true;
   }
 };
+
+// What a kernel with tiles of br x bc takes, in units that compare kernels: a
+// CU takes in operands at about 45 GB/s whatever the tile (32 x 64: 36, 32 x
+// 128: 45, 128 x 128: 52, 256 x 256: 41 at 256 to 8192 rows of 7168 values),
+// so the time goes by the rounds of 256 tiles and by the rows and columns that
+// each takes in. The groups are taken to have the mean size, if routed and two
+// standard deviations of a random count (a group that just passes a tile reads
+// its weights twice: 32 rows on average take 3.2 ms in tiles of 32 rows and 2.2
+// in those of 64). rows: of a tile in steps of which the kernel skips rows that
+// are not there.
+inline int64_t cost_of(const Groups& g, int br, int rows, int bc, int64_t cols) {
+  const int64_t experts = (int64_t)g.N * g.L, groups = experts < g.most ? experts : g.most;
+  if (groups == 0) return 0;
+  int64_t mean = (g.most + groups - 1) / groups;
+  if (g.off) mean += (int64_t)(2.0 * std::sqrt((double)mean));
+  const int64_t blocks = (mean + br - 1) / br;
+  const int64_t each = (mean + blocks - 1) / blocks;
+  const int64_t rounds = (groups * blocks * ((cols + bc - 1) / bc) + 255) / 256;
+  return rounds * ((each + rows - 1) / rows * rows + bc);
+}
 
 // Workgroups for a line: one per CU, or as many as there are tiles.
 inline unsigned line_grid(int64_t tiles) { return (unsigned)(tiles < 256 ? tiles : 256); }

@@ -170,14 +170,14 @@ __device__ __forceinline__ void write_tile(const Tile<S>& tile, uint16_t* out, i
 
 template <int FR, bool ONCE>
 using RowsShape = Shape<2, FR, 4, 4, false, true, false, 2, ONCE>;
-using RowsLine = Line<RowsShape<8, false>::BR, RowsShape<8, false>::threads>;
+using RowsSmall = Shape<2, 4, 2, 4, false, true, false, 4>;       // 128 x 128
+using RowsFlat = Shape<1, 2, 2, 4, false, true, false, 4, true>;  // 32 x 128
 
 // dx[r][c] = sum over n of dz[r][n] w[n][c], for tiles of more than MIN and at
 // most S::BR rows, from t on, while the line has such ones. Returns whether t is
 // then a tile of another height.
-template <typename S, int MIN>
-__device__ __forceinline__ bool rows_tiles(const GradArgs& a, RowsLine& line_, Where& t,
-                                           uint32_t lds) {
+template <typename S, int MIN, typename L>
+__device__ __forceinline__ bool rows_tiles(const GradArgs& a, L& line_, Where& t, uint32_t lds) {
   const int line = a.W * 2, w_line = a.in * 2;
   const auto feed_of = [&](const Where& w) {
     Feed p;
@@ -211,20 +211,40 @@ __device__ __forceinline__ bool rows_tiles(const GradArgs& a, RowsLine& line_, W
   }
 }
 
-__global__ __launch_bounds__(512) void rows_grad_kernel(GradArgs a) {
-  using S = RowsShape<8, false>;
-  static_assert(S::threads == 512, "one size for all heights");
+template <typename S>
+__global__ __launch_bounds__(S::threads) void rows_grad_kernel(GradArgs a) {
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S::lds_bytes];
   extern __shared__ int ends[];
-  RowsLine line(a.g, a.cols, ends);
+  Line<S::BR, S::threads> line(a.g, a.cols, ends);
   Where t;
   bool more = line.next(&t);
   while (more) {
-    if (t.rows <= 64) more = rows_tiles<RowsShape<2, true>, 0>(a, line, t, lds_base(lds));
-    else if (t.rows <= 128) more = rows_tiles<RowsShape<4, true>, 64>(a, line, t, lds_base(lds));
-    else if (t.rows <= 192) more = rows_tiles<RowsShape<6, true>, 128>(a, line, t, lds_base(lds));
-    else more = rows_tiles<S, 192>(a, line, t, lds_base(lds));
+    if constexpr (S::BR == 256) {  // in tiles of 64, 128 and 192 rows where they hold the rows
+      if (t.rows <= 64) more = rows_tiles<RowsShape<2, true>, 0>(a, line, t, lds_base(lds));
+      else if (t.rows <= 128) more = rows_tiles<RowsShape<4, true>, 64>(a, line, t, lds_base(lds));
+      else if (t.rows <= 192) more = rows_tiles<RowsShape<6, true>, 128>(a, line, t, lds_base(lds));
+      else more = rows_tiles<S, 192>(a, line, t, lds_base(lds));
+    } else {
+      more = rows_tiles<S, 0>(a, line, t, lds_base(lds));
+    }
   }
+}
+
+template <typename S>
+hipError_t run_rows(GradArgs a, hipStream_t stream) {
+  a.cols = (a.in + S::BC - 1) / S::BC;
+  hipLaunchKernelGGL(rows_grad_kernel<S>, dim3(line_grid(tile_grid(a.g, S::BR, a.cols))),
+                     dim3(S::threads), (size_t)a.g.N * a.g.L * 4, stream, a);
+  return hipGetLastError();
+}
+
+// The tiles that cost least, of equals the smallest, as in the forward pass.
+hipError_t rows_by_cost(const GradArgs& a, hipStream_t stream) {
+  const int64_t large = cost_of(a.g, 256, 64, 256, a.in), small = cost_of(a.g, 128, 128, 128, a.in),
+                flat = cost_of(a.g, 32, 32, 128, a.in);
+  if (flat <= small && flat <= large) return run_rows<RowsFlat>(a, stream);
+  if (small <= large) return run_rows<RowsSmall>(a, stream);
+  return run_rows<RowsShape<8, false>>(a, stream);
 }
 
 // dw[n][c] = sum over the expert's rows r of dz[r][n] x[r][c]. The experts'
@@ -280,7 +300,25 @@ __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   }
 }
 
-using WeightsShape = Shape<2, 8, 4, 4, true, true, false, 2>;
+template <typename S>
+hipError_t run_weights(GradArgs a, hipStream_t stream) {
+  a.rows = (a.W + S::BR - 1) / S::BR;
+  a.cols = (a.in + S::BC - 1) / S::BC;
+  hipLaunchKernelGGL(weights_grad_kernel<S>,
+                     dim3(line_grid(((int64_t)a.g.N * a.g.L * a.rows * a.cols + 7) / 8 * 8)),
+                     dim3(S::threads), 0, stream, a);
+  return hipGetLastError();
+}
+
+// By the same cost; the tiles are of the matrices, E times W x in.
+hipError_t weights_by_cost(const GradArgs& a, hipStream_t stream) {
+  const int64_t experts = (int64_t)a.g.N * a.g.L;
+  const auto cost = [&](int b) {
+    return (experts * ((a.W + b - 1) / b) * ((a.in + b - 1) / b) + 255) / 256 * 2 * b;
+  };
+  if (cost(128) <= cost(256)) return run_weights<Shape<2, 4, 2, 4, true, true, false, 4>>(a, stream);
+  return run_weights<Shape<2, 8, 4, 4, true, true, false, 2>>(a, stream);
+}
 
 int64_t blocks_of(const Groups& g) { return tile_grid(g, kChunkRows, 1); }
 
@@ -307,8 +345,8 @@ bool product_fits(const ep_product& p, const Dims& d) {
   const int64_t rows = d.NTR > d.N * d.cap ? d.NTR : d.N * d.cap;
   const int64_t most = (int64_t)1 << 23, W = weight_rows(p);
   const int64_t tiles = (rows / 32 + d.E + 8) * ((p.out + 63) / 64);
-  const int64_t back = (rows / 256 + d.E + 8) * ((p.in + 255) / 256);
-  const int64_t weights = d.E * ((W + 255) / 256) * ((p.in + 255) / 256);
+  const int64_t back = (rows / 32 + d.E + 8) * ((p.in + 127) / 128);
+  const int64_t weights = d.E * ((W + 127) / 128) * ((p.in + 127) / 128);
   return tiles < most && back < most && weights < most;
 }
 
@@ -359,23 +397,12 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
   a.g = g;
   a.in = p.in;
   a.W = W;
-  a.rows = (W + WeightsShape::BR - 1) / WeightsShape::BR;
+  a.rows = a.cols = 0;
   if (dx && g.most > 0) {
-    using S = RowsShape<8, false>;
-    a.cols = (p.in + S::BC - 1) / S::BC;
-    hipLaunchKernelGGL(rows_grad_kernel, dim3(line_grid(tile_grid(g, S::BR, a.cols))),
-                       dim3(S::threads), (size_t)experts * 4, stream, a);
-    e = hipGetLastError();
+    e = rows_by_cost(a, stream);
     if (e != hipSuccess) return e;
   }
-  if (dw) {
-    a.cols = (p.in + WeightsShape::BC - 1) / WeightsShape::BC;
-    hipLaunchKernelGGL(weights_grad_kernel<WeightsShape>,
-                       dim3(line_grid(((int64_t)experts * a.rows * a.cols + 7) / 8 * 8)),
-                       dim3(WeightsShape::threads), 0,
-                       stream, a);
-    e = hipGetLastError();
-  }
+  if (dw) e = weights_by_cost(a, stream);
   return e;
 }
 
