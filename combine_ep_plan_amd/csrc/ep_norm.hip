@@ -81,10 +81,12 @@ __device__ __forceinline__ void block_sum(float (&v)[N], float (*room)[N]) {
 template <int DT, int V, bool QUANT>
 __global__ __launch_bounds__(1024) void norm_kernel(const u32x4* x, const u32x4* residual,
                                                     const u32x4* weight, u32x4* sum, u32x4* y,
-                                                    uint2* codes, float* scales, int n16,
-                                                    float per, float eps) {
+                                                    uint2* codes, float* scales, int64_t rows,
+                                                    int n16, float per, float eps) {
   __shared__ float room[kMaxWaves][1];
-  const size_t row = (size_t)blockIdx.x * n16;
+  const int64_t number = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  if (number >= rows) return;  // whole waves: with blockDim.y > 1 a row is one wave's
+  const size_t row = (size_t)number * n16;
   u32x4 raw[V], res[V], wt[V];
 #pragma unroll
   for (int i = 0; i < V; ++i) {
@@ -137,18 +139,21 @@ __global__ __launch_bounds__(1024) void norm_kernel(const u32x4* x, const u32x4*
   }
 }
 
-// Rows blockIdx.x, blockIdx.x + gridDim.x, ...; with AHEAD the next row's
-// values are on their way while one is worked on (registers for it are there
-// up to 512 threads). Each workgroup keeps its part of dweight in registers
-// and writes it once: sums in a fixed order, without atomics.
-template <int DT, int V, int THREADS, bool AHEAD>
+// Rows number, number + step, ... of a workgroup, or with SIDE of each of its
+// waves; with AHEAD the next row's values are on their way while one is worked
+// on (registers for it are there up to 512 threads). Each workgroup keeps its
+// part of dweight in registers and writes it once: sums in a fixed order,
+// without atomics.
+template <int DT, int V, int THREADS, bool AHEAD, bool SIDE>
 __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const u32x4* dy, const u32x4* h,
                                                          const u32x4* weight, const u32x4* dsum,
                                                          u32x4* dx, float* parts, int64_t rows,
                                                          int n16, float per, float eps) {
+  const int64_t number = (int64_t)blockIdx.x * blockDim.y + threadIdx.y;
+  const int64_t step = (int64_t)gridDim.x * blockDim.y;
   __shared__ float room[2][kMaxWaves][2];
-  u32x4 hn[V], dn[V], sn[V];
-  float wt[V][8], dw[V][8];
+  u32x4 hn[V], dn[V], sn[V], wt[V];  // packed: a row's unpacked values fill the registers
+  float dw[V][8];
   const auto load = [&](int64_t r) {
 #pragma unroll
     for (int i = 0; i < V; ++i) {
@@ -162,50 +167,74 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const u32x4* dy, con
       }
     }
   };
-  if (AHEAD) load(blockIdx.x);
+  if (AHEAD) load(number);
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
-    unpack<DT>(c < n16 ? weight[c] : u32x4{0, 0, 0, 0}, wt[i]);
+    wt[i] = c < n16 ? weight[c] : u32x4{0, 0, 0, 0};
 #pragma unroll
     for (int j = 0; j < 8; ++j) dw[i][j] = 0.0f;
   }
   int turn = 0;
-  for (int64_t r = blockIdx.x; r < rows; r += gridDim.x, turn ^= 1) {
-    float hv[V][8], dv[V][8], s[2] = {0.0f, 0.0f};
-    u32x4 add[V];
+  for (int64_t r = number; r < rows; r += step, turn ^= 1) {
+    float s[2] = {0.0f, 0.0f};
+    u32x4 h0[V], d0[V], add[V];
     if (!AHEAD) load(r);
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      unpack<DT>(hn[i], hv[i]);
-      unpack<DT>(dn[i], dv[i]);
+      h0[i] = hn[i];
+      d0[i] = dn[i];
       add[i] = sn[i];
     }
-    if (AHEAD) load(r + gridDim.x);
+    if (AHEAD) load(r + step);
 #pragma unroll
-    for (int i = 0; i < V; ++i)
+    for (int i = 0; i < V; ++i) {
+      float hv[8], dv[8], wv[8];
+      unpack<DT>(h0[i], hv);
+      unpack<DT>(d0[i], dv);
+      unpack<DT>(wt[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        s[0] = __builtin_fmaf(hv[i][j], hv[i][j], s[0]);
-        s[1] = __builtin_fmaf(dv[i][j] * wt[i][j], hv[i][j], s[1]);
+        s[0] = __builtin_fmaf(hv[j], hv[j], s[0]);
+        s[1] = __builtin_fmaf(dv[j] * wv[j], hv[j], s[1]);
       }
+    }
     block_sum(s, room[turn]);  // two rooms in turn: one barrier per row is enough
     const float rs = rsqrtf(s[0] * per + eps);
     const float k = rs * rs * s[1] * per;
+    if constexpr (V > 2) {  // unpacked anew, not kept: 107 registers would not fit
+#pragma unroll
+      for (int i = 0; i < V; ++i) asm volatile("" : "+v"(h0[i]), "+v"(d0[i]), "+v"(wt[i]));
+    }
 #pragma unroll
     for (int i = 0; i < V; ++i) {
       const int c = threadIdx.x + i * blockDim.x;
-      float o[8];
+      float o[8], hv[8], dv[8], wv[8];
       unpack<DT>(add[i], o);
+      unpack<DT>(h0[i], hv);
+      unpack<DT>(d0[i], dv);
+      unpack<DT>(wt[i], wv);
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        o[j] += rs * __builtin_fmaf(-hv[i][j], k, dv[i][j] * wt[i][j]);
-        dw[i][j] = __builtin_fmaf(dv[i][j], hv[i][j] * rs, dw[i][j]);
+        o[j] += rs * __builtin_fmaf(-hv[j], k, dv[j] * wv[j]);
+        dw[i][j] = __builtin_fmaf(dv[j], hv[j] * rs, dw[i][j]);
       }
       if (c < n16) store_stream(&dx[(size_t)r * n16 + c], pack<DT>(o));
     }
   }
   if (!parts) return;
+  if constexpr (SIDE) {  // the waves' sums, in order
+    constexpr int waves = THREADS / kWave;
+    __shared__ float sums[waves - 1][V * 8][kWave];
+    if (threadIdx.y > 0)
+#pragma unroll
+      for (int j = 0; j < V * 8; ++j) sums[threadIdx.y - 1][j][threadIdx.x] = dw[j / 8][j % 8];
+    __syncthreads();
+    if (threadIdx.y > 0) return;
+    for (int w = 0; w < waves - 1; ++w)
+#pragma unroll
+      for (int j = 0; j < V * 8; ++j) dw[j / 8][j % 8] += sums[w][j][threadIdx.x];
+  }
 #pragma unroll
   for (int i = 0; i < V; ++i) {
     const int c = threadIdx.x + i * blockDim.x;
@@ -216,21 +245,29 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const u32x4* dy, con
   }
 }
 
-// Column sums of the parts: 64 columns per workgroup, 16 waves that each take
-// every 16th part.
+// Column sums of the parts: 32 columns per workgroup, 32 groups of lanes that
+// each take every 32nd part, eight of them on their way at once.
 __global__ __launch_bounds__(1024) void norm_weight_kernel(const float* parts, float* dweight,
                                                            int n, int hidden) {
-  __shared__ float room[16][kWave];
-  const int lane = lane_id(), wave = threadIdx.x / kWave, col = blockIdx.x * kWave + lane;
+  __shared__ float room[32][33];
+  const int lane = threadIdx.x % 32, group = threadIdx.x / 32, col = blockIdx.x * 32 + lane;
   float s = 0.0f;
-  if (col < hidden)
-    for (int p = wave; p < n; p += 16) s += parts[(size_t)p * hidden + col];
-  room[wave][lane] = s;
+  for (int p0 = group; p0 < n; p0 += 8 * 32) {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const int p = p0 + i * 32;
+      v[i] = p < n && col < hidden ? parts[(size_t)p * hidden + col] : 0.0f;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s += v[i];
+  }
+  room[group][lane] = s;
   __syncthreads();
-  if (wave != 0 || col >= hidden) return;
+  if (group != 0 || col >= hidden) return;
   s = 0.0f;
 #pragma unroll
-  for (int w = 0; w < 16; ++w) s += room[w][lane];
+  for (int g = 0; g < 32; ++g) s += room[g][lane];
   dweight[col] = s;
 }
 
@@ -244,6 +281,10 @@ int norm_threads(int hidden) {
   return kWave * ((hidden / 8 + per_wave - 1) / per_wave);
 }
 
+// Rows of one wave each that share a workgroup: 35,000 rows of 16 values are
+// otherwise as many workgroups.
+int rows_at_once(int hidden) { return norm_threads(hidden) == kWave ? 8 : 1; }
+
 // A launch holds fewer than 2^32 threads, of at most 1024 per row; more rows
 // go in several launches.
 constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
@@ -251,7 +292,7 @@ constexpr int64_t kRowsPerLaunch = (int64_t)1 << 21;
 template <int DT, int V>
 hipError_t run_norm(const ep_norm& n, const void* x, const void* residual, void* sum, void* y,
                     uint8_t* codes, float* scales, hipStream_t stream) {
-  const dim3 block(norm_threads(n.hidden));
+  const dim3 block(norm_threads(n.hidden), rows_at_once(n.hidden));
   const int n16 = n.hidden / 8;
   const auto kernel = codes ? norm_kernel<DT, V, true> : norm_kernel<DT, V, false>;
   const auto from = [&](const void* p, int64_t row) {
@@ -259,10 +300,10 @@ hipError_t run_norm(const ep_norm& n, const void* x, const void* residual, void*
   };
   for (int64_t row = 0; row < n.rows; row += kRowsPerLaunch) {
     const int64_t rows = n.rows - row < kRowsPerLaunch ? n.rows - row : kRowsPerLaunch;
-    hipLaunchKernelGGL(kernel, dim3((unsigned)rows), block, 0, stream, from(x, row),
+    hipLaunchKernelGGL(kernel, dim3((unsigned)((rows + block.y - 1) / block.y)), block, 0, stream, from(x, row),
                        from(residual, row), (const u32x4*)n.weight, from(sum, row), from(y, row),
                        codes ? (uint2*)codes + row * n16 : nullptr,
-                       scales ? scales + row * (n16 / 16) : nullptr, n16,
+                       scales ? scales + row * (n16 / 16) : nullptr, rows, n16,
                        1.0f / (float)n.hidden, n.eps);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -272,18 +313,20 @@ hipError_t run_norm(const ep_norm& n, const void* x, const void* residual, void*
 
 template <int DT>
 auto grad_kernel(int hidden) {
-  if (chunks_per_thread(hidden) == 4) return norm_grad_kernel<DT, 4, 1024, false>;
-  return norm_threads(hidden) > 512 ? norm_grad_kernel<DT, 2, 1024, false>
-                                    : norm_grad_kernel<DT, 2, 512, true>;
+  if (rows_at_once(hidden) > 1) return norm_grad_kernel<DT, 2, 512, true, true>;
+  if (chunks_per_thread(hidden) == 4) return norm_grad_kernel<DT, 4, 1024, false, false>;
+  return norm_threads(hidden) > 512 ? norm_grad_kernel<DT, 2, 1024, false, false>
+                                    : norm_grad_kernel<DT, 2, 512, true, false>;
 }
 
 }  // namespace
 
-// Workgroups that together fill the chip with 1024 threads per CU, a multiple
-// of its 256 CUs; no more than rows.
+// Workgroups that together give each of the chip's 256 CUs 1024 threads, but
+// at most two: every one of them costs a row of parts. No more than rows need.
 int norm_grad_parts(const ep_norm& n) {
-  const int64_t most = 256 * (1024 / norm_threads(n.hidden));
-  return (int)(n.rows < most ? n.rows : most);
+  const int threads = norm_threads(n.hidden), side = rows_at_once(n.hidden);
+  const int64_t most = threads * side > 512 ? 256 : 512, need = (n.rows + side - 1) / side;
+  return (int)(need < most ? need : most);
 }
 
 hipError_t launch_rms_norm(const ep_norm& n, const void* x, const void* residual, void* sum,
@@ -302,7 +345,8 @@ hipError_t launch_rms_norm_grad(const ep_norm& n, const void* dy, const void* h,
   if (blocks > 0) {
     const auto kernel =
         n.dtype == EP_DTYPE_BF16 ? grad_kernel<EP_DTYPE_BF16>(n.hidden) : grad_kernel<EP_DTYPE_F16>(n.hidden);
-    hipLaunchKernelGGL(kernel, dim3(blocks), dim3(norm_threads(n.hidden)), 0, stream,
+    hipLaunchKernelGGL(kernel, dim3(blocks),
+                       dim3(norm_threads(n.hidden), rows_at_once(n.hidden)), 0, stream,
                        (const u32x4*)dy, (const u32x4*)h, (const u32x4*)n.weight,
                        (const u32x4*)dsum, (u32x4*)dx, dweight ? parts : nullptr, n.rows,
                        n.hidden / 8, 1.0f / (float)n.hidden, n.eps);
@@ -310,7 +354,7 @@ hipError_t launch_rms_norm_grad(const ep_norm& n, const void* dy, const void* h,
     if (e != hipSuccess || !dweight) return e;
   }
   if (dweight)
-    hipLaunchKernelGGL(norm_weight_kernel, dim3((n.hidden + kWave - 1) / kWave), dim3(1024), 0,
+    hipLaunchKernelGGL(norm_weight_kernel, dim3((n.hidden + 31) / 32), dim3(1024), 0,
                        stream, parts, dweight, blocks, n.hidden);
   return hipGetLastError();
 }

@@ -13,12 +13,10 @@ struct FwdArgs {
   int in, n, cols;  // cols: column blocks
 };
 
-__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
-
 template <int ACT>
 __device__ __forceinline__ float activate(float z) {
   if constexpr (ACT == EP_ACT_SILU) return z * sigmoid(z);
-  if constexpr (ACT == EP_ACT_GELU) return 0.5f * z * erfcf(z * -0.70710678118654752f);
+  if constexpr (ACT == EP_ACT_GELU) return z * normal_at(z).below;
   return z;
 }
 

@@ -40,6 +40,33 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // nearest ev
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
+__device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
+
+// Density and distribution function of the standard normal distribution at z.
+// The tail beyond |z| is the density times Mills' ratio, which is smooth: a
+// polynomial in u = 1 / (1 + 0.3 |z|) fitted to it (least squares in the
+// relative error, reweighted towards its maximum) is within 2^-20 for all z,
+// also where the tail is far below 1. erfcf() takes 140 instructions and made
+// the 32 values of a thread 9 us of a small backward pass; this takes 20.
+struct Normal {
+  float density, below;
+};
+__device__ __forceinline__ Normal normal_at(float z) {
+  const float u = __builtin_amdgcn_rcpf(__builtin_fmaf(0.3f, fabsf(z), 1.0f));
+  float m = 4.652415588e-02f;
+  m = __builtin_fmaf(m, u, -1.212453768e-01f);
+  m = __builtin_fmaf(m, u, 7.356668357e-03f);
+  m = __builtin_fmaf(m, u, 9.863400459e-02f);
+  m = __builtin_fmaf(m, u, 1.256773323e-01f);
+  m = __builtin_fmaf(m, u, 2.238885313e-01f);
+  m = __builtin_fmaf(m, u, 2.724575102e-01f);
+  m = __builtin_fmaf(m, u, 3.000220060e-01f);
+  m = __builtin_fmaf(m, u, 2.999998331e-01f);
+  const float density = 0.39894228040143268f * __expf(-0.5f * z * z);
+  const float tail = m * u * density;
+  return Normal{density, z < 0.0f ? tail : 1.0f - tail};
+}
+
 // Bytes [base, base + size) as the buffer instructions take them (raw: 32-bit
 // offsets, reads past the end give zeros; no bytes when size is negative).
 __device__ __forceinline__ u32x4 buffer_of(const uint8_t* base, int size) {
