@@ -476,9 +476,9 @@ struct Tile {
         });
       });
     } else {
-      // Scales of 2^0 for both operands of the matrix instruction; the blocks'
-      // own multiply its sum over 128 values of k, in 32 bits, two products
-      // later, when it is there.
+      // The matrix instruction without scales of its own (constants of 0 select
+      // it); the blocks' multiply its sum over 128 values of k, in 32 bits, two
+      // products later, when it is there.
       constexpr int behind = 2;
       f32x4 sum[behind + 1];
       float by[S::FR][2];
@@ -504,7 +504,7 @@ struct Tile {
         each<S::FC>([&](auto column) {
           constexpr int j = column, m = i * S::FC + j;
           sum[m % (behind + 1)] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              f.a8[j], f.b8[i % 2], f32x4{}, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+              f.a8[j], f.b8[i % 2], f32x4{}, 0, 0, 0, 0, 0, 0);
           if constexpr (turned) f.a8[j] = cr.get8(next + S::BR * kStep, j);
           if constexpr (i == 0) {
             spread<S::r_copies - early, S::FC, j>([&](auto q) { copy_r(early + q, last); });
