@@ -14,7 +14,8 @@ constexpr int kActCols = kWave * 4;
 struct ActArgs {
   const uint16_t *dout, *pre;
   uint16_t* dz;   // or null
-  float* parts;   // [row blocks][W], or null
+  float* parts;   // [most][W], or null
+  int64_t most;   // row blocks that parts has room for: all those of a whole plan
   Groups g;
   int n;          // columns of dout
   int cols;
@@ -105,7 +106,7 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   __syncthreads();
   const int block = t.at / kChunkRows + before[0] + before[1] + before[2] + before[3];
   const int col = t.col * kActCols + threadIdx.x;
-  if (col >= a.n) return;
+  if (col >= a.n || block < 0 || block >= a.most) return;
 #pragma unroll
   for (int h = 0; h < (glu ? 2 : 1); ++h)
     a.parts[(int64_t)block * W + h * a.n + col] =
@@ -117,8 +118,8 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
 // groups of COLS lanes that each take every GROUPS-th part, eight of them on
 // their way at once.
 template <int COLS, int GROUPS>
-__global__ __launch_bounds__(COLS * GROUPS) void bias_kernel(const float* parts, Groups g,
-                                                             float* dbias, int W) {
+__global__ __launch_bounds__(COLS * GROUPS) void bias_kernel(const float* parts, int64_t most,
+                                                             Groups g, float* dbias, int W) {
   constexpr int threads = COLS * GROUPS;
   __shared__ int before[threads / kWave];
   __shared__ float room[GROUPS][COLS];
@@ -133,13 +134,14 @@ __global__ __launch_bounds__(COLS * GROUPS) void bias_kernel(const float* parts,
   __syncthreads();
   int64_t first = 0;
   for (int w = 0; w < threads / kWave; ++w) first += before[w];
-  const int n = (group_of(g, e).rows + kChunkRows - 1) / kChunkRows;
+  int64_t n = (group_of(g, e).rows + kChunkRows - 1) / kChunkRows;
+  if (first < 0 || first + n > most) n = 0;  // of a broken plan
   float s = 0.0f;
-  for (int p0 = group; p0 < n; p0 += 8 * GROUPS) {
+  for (int64_t p0 = group; p0 < n; p0 += 8 * GROUPS) {
     float v[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const int p = p0 + i * GROUPS;
+      const int64_t p = p0 + i * GROUPS;
       v[i] = p < n && c < W ? parts[(first + p) * W + c] : 0.0f;
     }
 #pragma unroll
@@ -157,14 +159,15 @@ __global__ __launch_bounds__(COLS * GROUPS) void bias_kernel(const float* parts,
 // Many parts per expert (65,536 rows of one: 2048) need many lanes a column,
 // 50 against 540 us; few (64 experts of 1024 rows: 32) are one batch of loads
 // for four lanes, 11 us against 56.
-hipError_t run_bias(const float* parts, const Groups& g, float* dbias, int W, hipStream_t stream) {
+hipError_t run_bias(const float* parts, int64_t most, const Groups& g, float* dbias, int W,
+                    hipStream_t stream) {
   const int experts = g.N * g.L;
   if (g.most / experts > 64 * kChunkRows)
     hipLaunchKernelGGL((bias_kernel<32, 32>), dim3((W + 31) / 32, experts), dim3(1024), 0, stream,
-                       parts, g, dbias, W);
+                       parts, most, g, dbias, W);
   else
     hipLaunchKernelGGL((bias_kernel<64, 4>), dim3((W + 63) / 64, experts), dim3(256), 0, stream,
-                       parts, g, dbias, W);
+                       parts, most, g, dbias, W);
   return hipGetLastError();
 }
 
@@ -401,6 +404,7 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
   act.dz = none || (!dx && !dw) ? nullptr : (uint16_t*)ws;
   act.parts =
       dbias ? (float*)((char*)ws + (none ? 0 : align256((int64_t)d.N * d.cap * W * 2))) : nullptr;
+  act.most = most_blocks(d);
   act.g = g;
   act.n = p.out;
   act.cols = (p.out + kActCols - 1) / kActCols;
@@ -416,7 +420,7 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
     if (e != hipSuccess) return e;
   }
   if (dbias) {
-    e = run_bias(act.parts, g, dbias, W, stream);
+    e = run_bias(act.parts, act.most, g, dbias, W, stream);
     if (e != hipSuccess) return e;
   }
   GradArgs a;

@@ -189,3 +189,33 @@ def test_product_grad_special_values():
     cols = torch.arange(40) != 5
     assert torch.equal(hw[1][cols], gw[1][cols]) and hw[1][5].isnan().all()
     assert torch.equal(hb[1][cols], gb[1][cols]) and hb[1][5].isnan()
+
+
+def sorted_rows(sizes):
+    idx = torch.cat([torch.full((m,), e, dtype=torch.int32) for e, m in enumerate(sizes)])
+    idx = idx[torch.randperm(len(idx), generator=torch.Generator().manual_seed(1))]
+    return Routed(1, len(idx), len(sizes), 1, idx.view(1, -1, 1))
+
+
+@pytest.mark.parametrize("sizes,k,n,act", [
+    ([256, 0, 257, 64, 65, 1, 128, 129, 192, 193, 512, 30, 250, 3, 700, 31] * 2, 1920, 136, ep.EP_ACT_NONE),
+    ([4113], 4096, 72, ep.EP_ACT_SILU),          # rows in tiles of 256
+    ([100, 0, 260, 64], 2088, 2048, ep.EP_ACT_NONE),   # weights in tiles of 256, several each
+    ([900, 124], 1160, 1032, ep.EP_ACT_SWIGLU),
+    ([20] * 10, 3840, 72, ep.EP_ACT_GELU),
+    ([2100, 40], 64, 72, ep.EP_ACT_SILU),        # more row blocks of one expert than a group of lanes takes at once
+])
+def test_product_grad_large(sizes, k, n, act):
+    note(f"product grad large {sizes[:4]} {k} {n} {act}")
+    Case(sorted_rows(sizes), len(sizes), k, n, act).check()
+
+
+def test_product_grad_of_a_plan_that_was_never_made():
+    """Offsets of any value: nothing outside the rank's rows and the workspace is touched."""
+    note("product grad broken plan")
+    for fill in (0, 127, 255):
+        where = sorted_rows([50, 60, 70])
+        c = Case(where, 3, 72, 40, ep.EP_ACT_SWIGLU)
+        where.plan.fill_(fill)
+        where.owned[:] = True
+        c.run()
