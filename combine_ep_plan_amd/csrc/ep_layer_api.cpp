@@ -142,9 +142,6 @@ int ep_rms_norm(const ep_norm* n, const void* x, const void* residual, void* sum
   for (const Span& s : {sr, ss, sy, sc, sf}) EP_CHECK(check_span(s, scope.device(), true));
   EP_CHECK(check_apart({ss, sy, sc, sf},
                        {sx, Span{unless_same(residual, sum), 2 * elems, "residual"}, sw}));
-  if (residual && residual == sum) {  // in place: the others still apart from it
-    EP_CHECK(check_apart({sy, sc, sf}, {sr}));
-  }
   const hipError_t e = ep::launch_rms_norm(*n, x, residual, sum, y, codes, scales, stream);
   if (e != hipSuccess) return fail_hip(e, "ep_rms_norm");
   return EP_OK;
@@ -231,9 +228,11 @@ int ep_expert_product_grad(const ep_desc* d, const ep_product* p, const uint16_t
   EP_CHECK(check_product(p));
   if (p->dtype != EP_DTYPE_BF16)
     return fail(EP_ERR_UNSUPPORTED, "ep_expert_product_grad takes bf16 products");
-  if ((pre != nullptr) != (p->act != EP_ACT_NONE))
+  const bool empty = dims.N * dims.cap == 0;  // no buffer of rows has an address then
+  if (!empty && (pre != nullptr) != (p->act != EP_ACT_NONE))
     return fail(EP_ERR_INVALID_ARG, "pre must be given with an activation, and only then");
-  if (!dx && !dw && !dbias) return fail(EP_ERR_INVALID_ARG, "dx, dw or dbias must be given");
+  if (!dx && !dw && !dbias)
+    return empty ? EP_OK : fail(EP_ERR_INVALID_ARG, "dx, dw or dbias must be given");
   if (!ep::product_fits(*p, dims))
     return fail(EP_ERR_UNSUPPORTED, "product: too many tiles for one launch");
   DeviceScope scope(stream);
@@ -263,8 +262,8 @@ int ep_combine_grad(const ep_desc* d, const uint16_t* dout, const uint16_t* y,
                     const float* weights, const void* plan_ws, uint16_t* dy, float* dweights,
                     hipStream_t stream) {
   EP_PROLOGUE(d, stream, plan_ws);
-  if (!dy && !dweights) return fail(EP_ERR_INVALID_ARG, "dy or dweights must be given");
   if (dims.NT == 0) return EP_OK;
+  if (!dy && !dweights) return fail(EP_ERR_INVALID_ARG, "dy or dweights must be given");
   const int dev = scope.device();
   const int64_t row = 2 * (int64_t)dims.H, rows = dims.N * dims.cap;
   const Span sd{dout, dims.NT * row, "dout"}, sy{y, rows * row, "y"},

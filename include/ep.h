@@ -709,7 +709,9 @@ typedef struct ep_norm {
  * neither; hidden % 128 == 0) receive the same rows as the planes of a block-fp8 dispatch:
  * codes [rows][hidden] e4m3fn, scales fp32 [rows][hidden / 128], quantised from
  * the 32-bit values (not from the rounded y) by the rules of
- * ep_dispatch_pack_quant. Either y or codes must be given. */
+ * ep_dispatch_pack_quant. Either y or codes must be given. The sum of squares is
+ * a float: a bf16 row whose squares leave its range (values beyond 1e18; with
+ * eps 0 also rows of nothing but values below 1e-19) has no meaningful norm. */
 EP_API int ep_rms_norm(const ep_norm *n, const void *x, const void *residual,
                        void *sum, void *y, uint8_t *codes, float *scales,
                        hipStream_t stream);

@@ -256,3 +256,32 @@ def test_refused_buffers():
     refused(ep.dispatch_grad, where.desc, a, where.plan, None)
     ep.expert_product_grad(where.desc, p, o, None, None, where.plan, ws, dx=torch.empty_like(a))   # x not needed
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("act", [ep.EP_ACT_NONE, ep.EP_ACT_SWIGLU])
+def test_no_tokens(act):
+    """No tokens and no capacity: every operator returns, sums over nothing are zero."""
+    note(f"no tokens {act}")
+    dev = "cuda"
+    where = Routed(2, 0, 4, 2, torch.zeros(2, 0, 2, dtype=torch.int32), hidden=64)
+    assert where.rows == 0
+    none = torch.empty(0, 64, dtype=BF, device=dev)
+    w = torch.ones(64, dtype=BF, device=dev)
+    dweight = torch.full((64,), 7.0, device=dev)
+    ep.rms_norm(none, w, EPS, y=none)
+    ep.rms_norm_grad(none, none, w, EPS, none, dweight, torch.empty(0, dtype=torch.uint8, device=dev))
+    wrows = 80 if act == ep.EP_ACT_SWIGLU else 40
+    m = torch.ones(4, wrows, 64, dtype=BF, device=dev)
+    p = ep.make_product(m, act)
+    out = torch.empty(0, 40, dtype=BF, device=dev)
+    pre = None if act == ep.EP_ACT_NONE else torch.empty(0, wrows, dtype=BF, device=dev)
+    ep.expert_product(where.desc, p, [none], where.plan, out, pre=pre)
+    ws = torch.empty(ep.expert_product_grad_bytes(where.desc, p), dtype=torch.uint8, device=dev)
+    dw, dbias = torch.full_like(m, 7.0), torch.full((4, wrows), 7.0, device=dev)
+    ep.expert_product_grad(where.desc, p, out, none, pre, where.plan, ws, none, dw, dbias)
+    ep.expert_product_grad(where.desc, p, out, none, pre, where.plan, ws, dx=none)
+    d, wt = torch.empty(2, 0, 64, dtype=BF, device=dev), torch.empty(2, 0, 2, device=dev)
+    ep.combine_grad(where.desc, d, none, wt, where.plan, none, wt.clone())
+    ep.dispatch_grad(where.desc, none, where.plan, d)
+    torch.cuda.synchronize()
+    assert (dweight == 0).all() and (dw == 0).all() and (dbias == 0).all()
