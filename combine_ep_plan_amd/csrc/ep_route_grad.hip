@@ -7,6 +7,9 @@
 // whole rows wherever the plan put them.
 //
 // One workgroup per token, V chunks of 8 values (16 bytes) per thread.
+//
+// 8 x 4096 tokens of 7168 values, top-8: 1582 us for combine (7.99 GB, 5.05
+// TB/s), 799 us for dispatch (4.70 GB, 5.9 TB/s). 32 x 128 tokens: 195 and 91 us.
 #include "ep_device.hpp"
 #include "ep_kernels.hpp"
 
@@ -14,7 +17,9 @@ namespace ep {
 namespace {
 
 constexpr int kV = 2;        // 16-byte chunks per thread
-constexpr int kRows = 4;     // expert rows in flight
+// Expert rows in flight. Of 1, 2, 4 and 8: combine takes 1591, 1581, 1585 and
+// 1589 us, dispatch 823, 835, 839 and 799 (8 x 4096 tokens).
+constexpr int kRows = 4, kSumRows = 8;
 constexpr int kMaxWaves = 16;
 
 typedef float f32x2 __attribute__((ext_vector_type(2)));
@@ -125,13 +130,13 @@ __global__ __launch_bounds__(1024) void dispatch_grad_kernel(const u32x4* g, con
         acc[i][2 * j + 1] = bf16_hi(a[j]);
       }
     }
-    for (int k0 = 0; k0 < R; k0 += kRows) {
-      int row[kRows];
-      u32x4 v[kRows][kV];
+    for (int k0 = 0; k0 < R; k0 += kSumRows) {
+      int row[kSumRows];
+      u32x4 v[kSumRows][kV];
 #pragma unroll
-      for (int b = 0; b < kRows; ++b) row[b] = row_of(rows, k0 + b, R, rows_in);
+      for (int b = 0; b < kSumRows; ++b) row[b] = row_of(rows, k0 + b, R, rows_in);
 #pragma unroll
-      for (int b = 0; b < kRows; ++b)
+      for (int b = 0; b < kSumRows; ++b)
 #pragma unroll
         for (int i = 0; i < kV; ++i) {
           const int c = base + threadIdx.x + i * blockDim.x;
@@ -139,7 +144,7 @@ __global__ __launch_bounds__(1024) void dispatch_grad_kernel(const u32x4* g, con
             v[b][i] = load_stream(&g[(size_t)row[b] * n16 + (c < n16 ? c : n16 - 1)]);
         }
 #pragma unroll
-      for (int b = 0; b < kRows; ++b) {
+      for (int b = 0; b < kSumRows; ++b) {
         if (row[b] < 0) continue;
 #pragma unroll
         for (int i = 0; i < kV; ++i)
