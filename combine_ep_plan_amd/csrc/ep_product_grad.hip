@@ -32,7 +32,7 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
 }
 
 // dz of a block of rows and columns, and the columns' sums over the rows: wave
-// w takes rows w, w + 4, ..., all of them on their way at once. HBM bounds it:
+// w takes rows w, w + 4, ... HBM bounds it:
 // 65,536 rows of 2048 + 4096 values to 4096 in 270 us, 5.0 TB/s.
 template <int ACT>
 __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
@@ -46,49 +46,56 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   const int c = t.col * kActCols + lane * 4, W = glu ? 2 * a.n : a.n;
   float s[glu ? 2 : 1][4] = {};
   if (c < a.n) {
-    uint2 d2[steps], z2[steps], u2[steps];
+    // Rows of a wave on their way at once: a sum alone (no activation) reads 65,536
+    // rows in 51 us with all eight and 56 with four; where dz is written, four take
+    // 5 to 8 % less (GELU, with the product behind it: 217 against 235 us).
+    constexpr int some = ACT == EP_ACT_NONE ? steps : 4;
+#pragma unroll 1
+    for (int i0 = 0; i0 < steps; i0 += some) {
+      uint2 d2[some], z2[some], u2[some];
 #pragma unroll
-    for (int i = 0; i < steps; ++i) {
-      const int r = wave + i * waves;
-      const int64_t row = t.first + r;
-      d2[i] = z2[i] = u2[i] = uint2{0, 0};
-      if (r >= t.rows) continue;
-      d2[i] = *(const uint2*)(a.dout + row * a.n + c);
-      if constexpr (ACT != EP_ACT_NONE) z2[i] = *(const uint2*)(a.pre + row * W + c);
-      if constexpr (glu) u2[i] = *(const uint2*)(a.pre + row * W + a.n + c);
-    }
-#pragma unroll
-    for (int i = 0; i < steps; ++i) {
-      const int r = wave + i * waves;
-      if (r >= t.rows) continue;
-      const int64_t row = t.first + r;
-      float d[4], z[4], u[4], o[4];
-      unpack4(d2[i], d);
-      unpack4(z2[i], z);
-      unpack4(u2[i], u);
-#pragma unroll
-      for (int v = 0; v < 4; ++v) {
-        if constexpr (ACT == EP_ACT_NONE) {
-          o[v] = d[v];
-        } else if constexpr (ACT == EP_ACT_GELU) {
-          const Normal n = normal_at(z[v]);
-          o[v] = d[v] * (n.below + z[v] * n.density);
-        } else {
-          const float sg = sigmoid(z[v]);
-          const float slope = sg * (1.0f + z[v] * (1.0f - sg));
-          if constexpr (glu) {
-            o[v] = d[v] * u[v] * slope;
-            u[v] = d[v] * z[v] * sg;
-            s[1][v] += u[v];
-          } else {
-            o[v] = d[v] * slope;
-          }
-        }
-        s[0][v] += o[v];
+      for (int i = 0; i < some; ++i) {
+        const int r = wave + (i0 + i) * waves;
+        const int64_t row = t.first + r;
+        d2[i] = z2[i] = u2[i] = uint2{0, 0};
+        if (r >= t.rows) continue;
+        d2[i] = *(const uint2*)(a.dout + row * a.n + c);
+        if constexpr (ACT != EP_ACT_NONE) z2[i] = *(const uint2*)(a.pre + row * W + c);
+        if constexpr (glu) u2[i] = *(const uint2*)(a.pre + row * W + a.n + c);
       }
-      if (ACT != EP_ACT_NONE && a.dz) {
-        store4(a.dz + row * W + c, o);
-        if constexpr (glu) store4(a.dz + row * W + a.n + c, u);
+#pragma unroll
+      for (int i = 0; i < some; ++i) {
+        const int r = wave + (i0 + i) * waves;
+        if (r >= t.rows) continue;
+        const int64_t row = t.first + r;
+        float d[4], z[4], u[4], o[4];
+        unpack4(d2[i], d);
+        unpack4(z2[i], z);
+        unpack4(u2[i], u);
+#pragma unroll
+        for (int v = 0; v < 4; ++v) {
+          if constexpr (ACT == EP_ACT_NONE) {
+            o[v] = d[v];
+          } else if constexpr (ACT == EP_ACT_GELU) {
+            const Normal n = normal_at(z[v]);
+            o[v] = d[v] * (n.below + z[v] * n.density);
+          } else {
+            const float sg = sigmoid(z[v]);
+            const float slope = sg * (1.0f + z[v] * (1.0f - sg));
+            if constexpr (glu) {
+              o[v] = d[v] * u[v] * slope;
+              u[v] = d[v] * z[v] * sg;
+              s[1][v] += u[v];
+            } else {
+              o[v] = d[v] * slope;
+            }
+          }
+          s[0][v] += o[v];
+        }
+        if (ACT != EP_ACT_NONE && a.dz) {
+          store4(a.dz + row * W + c, o);
+          if constexpr (glu) store4(a.dz + row * W + a.n + c, u);
+        }
       }
     }
   }
