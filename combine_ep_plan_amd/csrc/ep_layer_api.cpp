@@ -109,6 +109,9 @@ int check_groups(const ep::Dims& d, const void* plan_ws, int dev, ep::Groups* g)
   EP_CHECK(check_aligned16(plan_ws, "plan_ws"));
   g->off = ep::plan_ptrs(d, plan_ws).grp_off;
   if (d.NTR < g->most) g->most = d.NTR;
+  // Without tokens no plan need have been made, and no row buffer is checked:
+  // offsets of any value then name no rows.
+  if (g->most == 0) g->cap = 0;
   return EP_OK;
 }
 
