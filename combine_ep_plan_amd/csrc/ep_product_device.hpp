@@ -20,6 +20,7 @@
 
 #include "ep_device.hpp"
 #include "ep_kernels.hpp"
+#include "ep_tiles.hpp"
 
 namespace ep {
 
@@ -565,26 +566,6 @@ __device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
                      pack_bf16(v[6], v[7])};
 }
 
-// Rows [first, first + rows) of the grouped buffers.
-struct Group {
-  int first, rows;
-};
-
-__device__ __forceinline__ Group group_of(const Groups& g, int e) {
-  if (!g.off) return Group{(int)(e * g.cap), (int)g.cap};
-  const int d = e / g.L, j = e - d * g.L;
-  const int32_t* off = g.off + (size_t)d * (g.L + 1) + j;
-  const int64_t lo = off[0] < 0 ? 0 : off[0] < g.cap ? off[0] : g.cap;
-  const int64_t hi = off[1] < lo ? lo : off[1] < g.cap ? off[1] : g.cap;
-  return Group{(int)(d * g.cap + lo), (int)(hi - lo)};
-}
-
-// A tile of a group's rows: `rows` of them from the group's `at`-th on, and
-// the tile's column block.
-struct Where {
-  int expert, first, rows, at, col;
-};
-
 // The tile of this workgroup, among `cols` column blocks per block of BR rows;
 // false: none is left. The tiles of the groups lie on a line that the eight
 // XCDs (workgroup b runs on XCD b % 8) share in equal stretches, so that the
@@ -594,24 +575,26 @@ template <int BR, int THREADS>
 __device__ __forceinline__ bool find_tile(const Groups& g, int cols, Where* out) {
   __shared__ int wave_sum[THREADS / kWave];
   __shared__ Where found;
-  const int experts = g.N * g.L, tid = threadIdx.x, lane = lane_id();
+  const int experts = g.N * g.L, tid = threadIdx.x, lane = lane_id(), room = room_of(g, BR);
   const int per = (experts + THREADS - 1) / THREADS;
   const int e0 = tid * per, e1 = e0 + per < experts ? e0 + per : experts;
   int mine = 0;
-  for (int e = e0; e < e1; ++e) mine += (group_of(g, e).rows + BR - 1) / BR;
-  int sum = mine;
+  for (int e = e0; e < e1; ++e) mine = add_blocks(mine, blocks_of(g, e, BR, room), room);
+  int sum = mine, before = 0;  // before: of the threads before this one
 #pragma unroll
   for (int off = 1; off < kWave; off <<= 1) {
     const int up = __shfl_up(sum, off);
-    if (lane >= off) sum += up;
+    if (lane >= off) sum = add_blocks(sum, up, room);
   }
+  before = __shfl_up(sum, 1);
+  if (lane == 0) before = 0;
   if (lane == kWave - 1) wave_sum[tid / kWave] = sum;
-  if (tid == 0) found = Where{0, 0, 0, 0, 0};  // of a broken plan whose rows pass 32 bits
+  if (tid == 0) found = Where{0, 0, 0, 0, 0};
   __syncthreads();
-  int before = sum - mine, total = 0;
+  int total = 0;
   for (int w = 0; w < THREADS / kWave; ++w) {
-    if (w < tid / kWave) before += wave_sum[w];
-    total += wave_sum[w];
+    if (w < tid / kWave) before = add_blocks(before, wave_sum[w], room);
+    total = add_blocks(total, wave_sum[w], room);
   }
   const int64_t tiles = (int64_t)total * cols;
   const int64_t stretch = (tiles + 7) / 8;
@@ -621,16 +604,13 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int cols, Where* out)
   if (left >= 0 && left < (int64_t)mine * cols) {
     for (int e = e0; e < e1; ++e) {
       const Group gr = group_of(g, e);
-      const int blocks = (gr.rows + BR - 1) / BR;
+      const int blocks = blocks_in(gr.rows, BR);
       if (left >= (int64_t)blocks * cols) {
         left -= (int64_t)blocks * cols;
         continue;
       }
-      const int at = (int)left, stripe = at / (blocks * 8);
-      const int wide = cols - stripe * 8 < 8 ? cols - stripe * 8 : 8;
-      const int in = at - stripe * blocks * 8, rb = in / wide;
-      const int rows = gr.rows - rb * BR < BR ? gr.rows - rb * BR : BR;
-      found = Where{e, gr.first + rb * BR, rows, rb * BR, stripe * 8 + in % wide};
+      const RowCol rc = stripe_of((int)left, blocks, cols);
+      found = where_of(gr, e, BR, rc.row, rc.col);
       break;
     }
   }
@@ -640,43 +620,9 @@ __device__ __forceinline__ bool find_tile(const Groups& g, int cols, Where* out)
   return true;
 }
 
-// Workgroups that hold every tile that find_tile can name, given at most
-// `most` rows in groups of `experts`; a multiple of 8.
+// Workgroups that hold every tile that find_tile can name; a multiple of 8.
 inline int64_t tile_grid(const Groups& g, int br, int64_t cols) {
-  const int64_t experts = (int64_t)g.N * g.L;
-  int64_t blocks;
-  if (!g.off)
-    blocks = g.N * ((g.cap + br - 1) / br);
-  else
-    blocks = g.most / br + (experts < g.most ? experts : g.most);
-  return (blocks * cols + 7) / 8 * 8;
-}
-
-// A workgroup's i-th tile on a line of `all`, or -1: the XCDs take turns with
-// as many neighbouring tiles as they have workgroups, so that what several of
-// them read is still in the memory-side cache, and share what is left at the
-// end evenly.
-__device__ __forceinline__ int64_t tile_of(int i, int64_t all) {
-  const int slots = gridDim.x / 8, xcd = blockIdx.x % 8, slot = blockIdx.x / 8;
-  const int64_t before = (int64_t)i * 8 * slots, left = all - before;
-  if (left >= 8 * slots) return before + xcd * slots + slot;
-  const int each = (int)((left + 7) / 8);
-  return left > 0 && slot < each && xcd * each + slot < left ? before + xcd * each + slot : -1;
-}
-
-// Row block and column block of the at-th tile of blocks x cols: the tiles go by
-// stripes of 16 columns, in those by four rows, in those by 8 columns, so that
-// 32 neighbours, an XCD's at one time, are 4 x 8 and need 12 blocks of operands.
-struct RowCol {
-  int row, col;
-};
-__device__ __forceinline__ RowCol place_of(int at, int blocks, int cols) {
-  const int stripe = at / (blocks * 16), in = at - stripe * blocks * 16;
-  const int wide = cols - stripe * 16 < 16 ? cols - stripe * 16 : 16;
-  const int four = in / (4 * wide), rows = blocks - 4 * four < 4 ? blocks - 4 * four : 4;
-  const int left = wide < 8 ? wide : 8, i = in - four * 4 * wide, j = i - rows * left;
-  return j < 0 ? RowCol{4 * four + i / left, stripe * 16 + i % left}
-               : RowCol{4 * four + j / (wide - left), stripe * 16 + left + j % (wide - left)};
+  return (room_of(g, br) * cols + 7) / 8 * 8;
 }
 
 // The tiles of a workgroup that takes one after the other. The groups' tiles
@@ -692,25 +638,25 @@ struct Line {
   __device__ __forceinline__ Line(const Groups& g, int cols, int* ends)
       : g(g), ends(ends), experts(g.N * g.L), cols(cols), taken(0) {
     __shared__ int wave_sum[THREADS / kWave];
-    const int tid = threadIdx.x, lane = lane_id();
+    const int tid = threadIdx.x, lane = lane_id(), room = room_of(g, BR);
     int total = 0;
     for (int e0 = 0; e0 < experts; e0 += THREADS) {
       const int e = e0 + tid;
-      int sum = e < experts ? (group_of(g, e).rows + BR - 1) / BR : 0;
+      int sum = e < experts ? blocks_of(g, e, BR, room) : 0;
 #pragma unroll
       for (int off = 1; off < kWave; off <<= 1) {
         const int up = __shfl_up(sum, off);
-        if (lane >= off) sum += up;
+        if (lane >= off) sum = add_blocks(sum, up, room);
       }
       if (lane == kWave - 1) wave_sum[tid / kWave] = sum;
       __syncthreads();
       int all = 0;
       for (int w = 0; w < THREADS / kWave; ++w) {
-        if (w < tid / kWave) sum += wave_sum[w];
-        all += wave_sum[w];
+        if (w < tid / kWave) sum = add_blocks(sum, wave_sum[w], room);
+        all = add_blocks(all, wave_sum[w], room);
       }
-      if (e < experts) ends[e] = total + sum;
-      total += all;
+      if (e < experts) ends[e] = add_blocks(total, sum, room);
+      total = add_blocks(total, all, room);
       __syncthreads();
     }
     tiles = (int64_t)wave_uniform(total) * cols;
@@ -718,26 +664,17 @@ struct Line {
 
   // The workgroup's next tile; false: none is left.
   __device__ __forceinline__ bool next(Where* out) {
-    const int64_t want = tile_of(taken, tiles);
+    const int64_t want = tile_of(taken, tiles, gridDim.x, blockIdx.x);
     if (want < 0) return false;
     ++taken;
     const int block = (int)(want / cols);  // row blocks of whole groups lie before it
     int e = 0;
     for (int e0 = 0; e0 < experts; e0 += kWave)
       e += __popcll(ballot(e0 + lane_id() < experts && ends[e0 + lane_id()] <= block));
-    // Offsets of a broken plan may add up to anything, past 32 bits too; each
-    // group alone is inside its rank's rows.
-    e = wave_uniform(e < experts ? e : experts - 1);
-    const Group gr = group_of(g, e);
-    const int blocks = wave_uniform((gr.rows + BR - 1) / BR), first = wave_uniform(gr.first);
-    const int start = wave_uniform(e > 0 ? ends[e - 1] : 0), rows = wave_uniform(gr.rows);
-    const RowCol rc = place_of((int)(want - (int64_t)start * cols), blocks, cols);
-    const int at = rc.row * BR;
-    if (rc.row < 0 || rc.row >= blocks || rc.col < 0 || rc.col >= cols) {
-      *out = Where{e, first, 0, 0, 0};
-      return true;
-    }
-    *out = Where{e, first + at, rows - at < BR ? rows - at : BR, at, rc.col};
+    e = wave_uniform(e);
+    const Where t = tile_at(g, BR, e, wave_uniform(e > 0 ? ends[e - 1] : 0), want, cols);
+    *out = Where{e, wave_uniform(t.first), wave_uniform(t.rows), wave_uniform(t.at),
+                 wave_uniform(t.col)};
     return true;
   }
 };

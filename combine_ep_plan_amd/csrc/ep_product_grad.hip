@@ -102,22 +102,23 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   if (!a.parts) return;
   // The row block's number among all groups' row blocks: those of the experts
   // before, then those of its own.
+  const int limit = room_of(a.g, kChunkRows);
   int mine = 0;
   for (int e = threadIdx.x; e < t.expert; e += kActThreads)
-    mine += (group_of(a.g, e).rows + kChunkRows - 1) / kChunkRows;
+    mine = add_blocks(mine, blocks_of(a.g, e, kChunkRows, limit), limit);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mine += __shfl_xor(mine, off);
+  for (int off = 32; off >= 1; off >>= 1) mine = add_blocks(mine, __shfl_xor(mine, off), limit);
   if (lane == 0) before[wave] = mine;
 #pragma unroll
   for (int h = 0; h < (glu ? 2 : 1); ++h)
     *(float4*)&room[wave][h][lane * 4] = float4{s[h][0], s[h][1], s[h][2], s[h][3]};
   __syncthreads();
-  const int block = t.at / kChunkRows + before[0] + before[1] + before[2] + before[3];
+  const int64_t block = (int64_t)t.at / kChunkRows + before[0] + before[1] + before[2] + before[3];
   const int col = t.col * kActCols + threadIdx.x;
-  if (col >= a.n || block < 0 || block >= a.most) return;
+  if (col >= a.n || block >= a.most) return;  // the latter with a broken plan only
 #pragma unroll
   for (int h = 0; h < (glu ? 2 : 1); ++h)
-    a.parts[(int64_t)block * W + h * a.n + col] =
+    a.parts[block * W + h * a.n + col] =
         room[0][h][threadIdx.x] + room[1][h][threadIdx.x] + room[2][h][threadIdx.x] +
         room[3][h][threadIdx.x];
 }
@@ -133,17 +134,18 @@ __global__ __launch_bounds__(COLS * GROUPS) void bias_kernel(const float* parts,
   __shared__ float room[GROUPS][COLS];
   const int e = blockIdx.y, lane = threadIdx.x % COLS, group = threadIdx.x / COLS;
   const int c = blockIdx.x * COLS + lane;
+  const int limit = room_of(g, kChunkRows);
   int mine = 0;
   for (int i = threadIdx.x; i < e; i += threads)
-    mine += (group_of(g, i).rows + kChunkRows - 1) / kChunkRows;
+    mine = add_blocks(mine, blocks_of(g, i, kChunkRows, limit), limit);
 #pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) mine += __shfl_xor(mine, off);
+  for (int off = 32; off >= 1; off >>= 1) mine = add_blocks(mine, __shfl_xor(mine, off), limit);
   if (lane_id() == 0) before[threadIdx.x / kWave] = mine;
   __syncthreads();
   int64_t first = 0;
   for (int w = 0; w < threads / kWave; ++w) first += before[w];
-  int64_t n = (group_of(g, e).rows + kChunkRows - 1) / kChunkRows;
-  if (first < 0 || first + n > most) n = 0;  // of a broken plan
+  int64_t n = blocks_in(group_of(g, e).rows, kChunkRows);
+  if (first + n > most) n = 0;  // of a broken plan
   float s = 0.0f;
   for (int64_t p0 = group; p0 < n; p0 += 8 * GROUPS) {
     float v[8];
@@ -324,7 +326,7 @@ __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
     p.rs_size = p.cs_size = 0;
     return p;
   };
-  int64_t want = tile_of(0, all);
+  int64_t want = tile_of(0, all, gridDim.x, blockIdx.x);
   if (want < 0) return;
   Tile<S> tile(
       lds_base(lds), line, x_line,
@@ -334,7 +336,7 @@ __global__ __launch_bounds__(S::threads) void weights_grad_kernel(GradArgs a) {
   Feed p = feed_of(t);
   int taken = 1;
   for (bool primed = false;; ++taken) {
-    want = tile_of(taken, all);
+    want = tile_of(taken, all, gridDim.x, blockIdx.x);
     const bool more = want >= 0;
     const At n = more ? at_of((int)want) : t;
     const Feed after = feed_of(n);
@@ -368,8 +370,6 @@ hipError_t weights_by_cost(const GradArgs& a, hipStream_t stream) {
   return run_weights<Shape<2, 8, 4, 4, true, true, false, 2>>(a, stream);
 }
 
-int64_t blocks_of(const Groups& g) { return tile_grid(g, kChunkRows, 1); }
-
 int64_t align256(int64_t n) { return (n + 255) / 256 * 256; }
 
 Groups groups_of(const Dims& d) {
@@ -381,7 +381,7 @@ Groups groups_of(const Dims& d) {
 // Row blocks, at most: dense groups or the plan's.
 int64_t most_blocks(const Dims& d) {
   const Groups g = groups_of(d);
-  const int64_t dense = blocks_of(g), routed = d.NTR / kChunkRows + d.E + 8;
+  const int64_t dense = room_of(g, kChunkRows), routed = d.NTR / kChunkRows + d.E + 8;
   return d.E == d.N && dense > routed ? dense : routed;
 }
 

@@ -40,3 +40,97 @@ def test_no_tokens_and_a_plan_that_was_never_made(act):
         ep.expert_product_grad(d, p, dout, x, pre, plan, ws, dx, dw, db)
         torch.cuda.synchronize()
         assert (out == 7).all() and (dx == 7).all() and (dw == 0).all() and (db == 0).all()
+
+
+def broken(kind, n, local, cap, g):
+    """Group offsets that no plan has, int32 [n, local + 1]; their groups together are far more rows than slots."""
+    j = torch.arange(local + 1)
+    big, small = 2**31 - 1, -2**31
+    one = {
+        "all or nothing": (j % 2) * cap,
+        "descending": cap - cap * j // local,
+        "out of range": torch.where(j % 2 == 1, torch.tensor(big), torch.tensor(small)),
+        "one past another": (j * 37) % (cap + 1),
+        "random": torch.randint(small, big, (local + 1,), generator=g),
+        "random rows": torch.randint(0, cap + 1, (local + 1,), generator=g),
+    }[kind]
+    return one.to(torch.int32).expand(n, -1).contiguous()
+
+
+def guarded(shape, dtype, fill=7.0):
+    """A tensor between two guards of at least 64 KB, and a function that asserts that the guards are whole."""
+    count = 1
+    for s in shape:
+        count *= s
+    size = torch.empty(0, dtype=dtype).element_size()
+    edge = 65536 // size
+    whole = torch.full((count + 2 * edge,), fill, dtype=dtype, device="cuda")
+
+    def check():
+        assert (whole[:edge] == fill).all() and (whole[-edge:] == fill).all()
+    return whole[edge:-edge].view(shape), check
+
+
+KINDS = ["all or nothing", "descending", "out of range", "one past another", "random", "random rows"]
+# ranks, tokens, experts, top-k, capacity, columns in, columns out: so that the forward pass takes tiles of 32 x 64, 32 x 128,
+# 128 x 128, 256 x 256 and 32 x 128 in turn, dx of 32 x 128 (three times), 128 x 128 and 256 x 256, the capacity being far
+# more rows than the slots.
+PLANS = [(1, 20, 6, 2, 400, 128, 128), (2, 40, 16, 2, 300, 256, 1280), (1, 900, 4, 2, 2000, 128, 2048),
+         (1, 4200, 3, 1, 5000, 256, 2048), (1, 4200, 3, 1, 5000, 4096, 128)]
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("fp8", [False, True])
+@pytest.mark.parametrize("n,t,e,r,cap,k,m", PLANS)
+def test_product_of_broken_plans(n, t, e, r, cap, k, m, fp8, kind):
+    note(f"product broken plan {kind} {fp8} {n} {t} {e} {r} {cap} {k} {m}")
+    g = torch.Generator().manual_seed(1)
+    d = ep.make_desc(n, t, 8, e, r, cap_rows=cap)
+    plan, whole = guarded((ep.plan_bytes(d),), torch.uint8, 7)
+    plan.zero_()
+    group_offsets(d, plan).copy_(broken(kind, n, e // n, cap, g))
+    rows = n * cap
+    if fp8:
+        x = [torch.zeros(rows, k, dtype=torch.float8_e4m3fn, device="cuda"), torch.ones(rows, k // 128, device="cuda")]
+        p = ep.make_product(torch.zeros(e, m, k, dtype=torch.float8_e4m3fn, device="cuda"), ep.EP_ACT_SILU,
+                            w_scale=torch.ones(e, m // 128, k // 128, device="cuda"))
+    else:
+        x = [torch.zeros(rows, k, dtype=BF, device="cuda")]
+        p = ep.make_product(torch.zeros(e, m, k, dtype=BF, device="cuda"), ep.EP_ACT_SILU)
+    (out, a), (pre, b) = guarded((rows, m), BF), guarded((rows, m), BF)
+    ep.expert_product(d, p, x, plan, out, pre=pre)
+    torch.cuda.synchronize()
+    for f in (a, b, whole):
+        f()
+    # Every row is some group's product, 0, or was left as it was.
+    for o in (out, pre):
+        assert ((o == 0) | (o == 7)).all()
+
+
+@pytest.mark.parametrize("kind", KINDS)
+@pytest.mark.parametrize("act", [ep.EP_ACT_NONE, ep.EP_ACT_SWIGLU])
+@pytest.mark.parametrize("n,t,e,r,cap,k,m", PLANS)
+def test_product_grad_of_broken_plans(n, t, e, r, cap, k, m, act, kind):
+    note(f"product grad broken plan {kind} {act} {n} {t} {e} {r} {cap} {k} {m}")
+    g = torch.Generator().manual_seed(2)
+    d = ep.make_desc(n, t, 8, e, r, cap_rows=cap)
+    plan, whole = guarded((ep.plan_bytes(d),), torch.uint8, 7)
+    plan.zero_()
+    offsets = broken(kind, n, e // n, cap, g)
+    group_offsets(d, plan).copy_(offsets)
+    rows, wrows = n * cap, 2 * m if act == ep.EP_ACT_SWIGLU else m
+    p = ep.make_product(torch.zeros(e, wrows, k, dtype=BF, device="cuda"), act)
+    x, dout = torch.ones(rows, k, dtype=BF, device="cuda"), torch.ones(rows, m, dtype=BF, device="cuda")
+    pre = torch.zeros(rows, wrows, dtype=BF, device="cuda") if act != ep.EP_ACT_NONE else None
+    (ws, a), (dx, b) = guarded((ep.expert_product_grad_bytes(d, p),), torch.uint8, 9), guarded((rows, k), BF)
+    (dw, c), (db, f) = guarded((e, wrows, k), BF), guarded((e, wrows), torch.float32)
+    ep.expert_product_grad(d, p, dout, x, pre, plan, ws, dx, dw, db)
+    torch.cuda.synchronize()
+    for check in (a, b, c, f, whole):
+        check()
+    assert ((dx == 0) | (dx == 7)).all()
+    if act == ep.EP_ACT_NONE:   # x and dout of ones: dw holds each group's rows, cut to its rank's
+        off = offsets.long().clamp(0, cap)
+        lo, hi = off[:, :-1].flatten(), off[:, 1:].flatten()
+        want = (torch.maximum(hi, lo) - lo).to(BF).cuda()
+        assert (dw == want[:, None, None]).all()
