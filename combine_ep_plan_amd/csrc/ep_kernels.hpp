@@ -177,8 +177,10 @@ struct Groups {
 inline int64_t weight_rows(const ep_product& p) {
   return p.act == EP_ACT_SWIGLU ? 2 * (int64_t)p.out : p.out;
 }
-// Whether every launch of the product's two directions stays inside a grid.
-bool product_fits(const ep_product& p, const Dims& d);
+// Whether the tiles of `cols` output columns on a line of the groups' rows can
+// be numbered, and whether one launch holds the backward pass's elementwise part.
+bool line_fits(const Groups& g, int64_t cols);
+bool act_grad_fits(const Groups& g, int64_t cols);
 hipError_t launch_product(const ep_product& p, const Groups& g, const void* const x[2],
                           const void* residual, void* pre, void* out, hipStream_t stream);
 int64_t product_grad_bytes(const ep_product& p, const Dims& d);

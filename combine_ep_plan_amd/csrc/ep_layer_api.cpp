@@ -98,21 +98,25 @@ int check_product(const ep_product* p) {
 }
 
 // Which rows belong to which expert: the plan's, or all of a rank's.
-int check_groups(const ep::Dims& d, const void* plan_ws, int dev, ep::Groups* g) {
+int groups_of(const ep::Dims& d, const void* plan_ws, ep::Groups* g) {
   *g = ep::Groups{nullptr, d.N, d.L, d.cap, d.N * d.cap};
   if (!plan_ws) {
     if (d.E != d.N)
       return fail(EP_ERR_INVALID_ARG, "without a plan n_experts must be n_ranks");
     return EP_OK;
   }
-  EP_CHECK(check_ptr(plan_ws, dev, "plan_ws", (int64_t)ep::layout_of(d).bytes));
-  EP_CHECK(check_aligned16(plan_ws, "plan_ws"));
   g->off = ep::plan_ptrs(d, plan_ws).grp_off;
   if (d.NTR < g->most) g->most = d.NTR;
   // Without tokens no plan need have been made, and no row buffer is checked:
   // offsets of any value then name no rows.
   if (g->most == 0) g->cap = 0;
   return EP_OK;
+}
+
+int check_plan(const ep::Dims& d, const void* plan_ws, int dev) {
+  if (!plan_ws) return EP_OK;
+  EP_CHECK(check_ptr(plan_ws, dev, "plan_ws", (int64_t)ep::layout_of(d).bytes));
+  return check_aligned16(plan_ws, "plan_ws");
 }
 
 int64_t w_elems(const ep::Dims& d, const ep_product& p) {
@@ -191,13 +195,14 @@ int ep_expert_product(const ep_desc* d, const ep_product* p, const void* const x
   if (!x) return fail(EP_ERR_INVALID_ARG, "null plane array: x");
   const bool fp8 = p->dtype == EP_DTYPE_E4M3;
   if (!fp8 && x[1]) return fail(EP_ERR_INVALID_ARG, "plane 1 must be NULL for bf16: x");
-  if (!ep::product_fits(*p, dims))
-    return fail(EP_ERR_UNSUPPORTED, "product: too many tiles for one launch");
+  ep::Groups g;
+  EP_CHECK(groups_of(dims, plan_ws, &g));
+  if (!ep::line_fits(g, p->out))
+    return fail(EP_ERR_UNSUPPORTED, "product: too many tiles of rows by out");
   DeviceScope scope(stream);
   if (scope.error() != hipSuccess) return fail_hip(scope.error(), "device");
   const int dev = scope.device();
-  ep::Groups g;
-  EP_CHECK(check_groups(dims, plan_ws, dev, &g));
+  EP_CHECK(check_plan(dims, plan_ws, dev));
   if (g.most == 0) return EP_OK;
   const int64_t rows = dims.N * dims.cap, W = ep::weight_rows(*p), we = w_elems(dims, *p);
   const Span s0{x[0], rows * p->in * (fp8 ? 1 : 2), "x"}, s1{x[1], rows * (p->in / 32), "x scales"},
@@ -236,13 +241,16 @@ int ep_expert_product_grad(const ep_desc* d, const ep_product* p, const uint16_t
     return fail(EP_ERR_INVALID_ARG, "pre must be given with an activation, and only then");
   if (!dx && !dw && !dbias)
     return empty ? EP_OK : fail(EP_ERR_INVALID_ARG, "dx, dw or dbias must be given");
-  if (!ep::product_fits(*p, dims))
-    return fail(EP_ERR_UNSUPPORTED, "product: too many tiles for one launch");
+  ep::Groups g;
+  EP_CHECK(groups_of(dims, plan_ws, &g));
+  if (dx && !ep::line_fits(g, p->in))
+    return fail(EP_ERR_UNSUPPORTED, "product: too many tiles of rows by in");
+  if ((dbias || p->act != EP_ACT_NONE) && !ep::act_grad_fits(g, p->out))
+    return fail(EP_ERR_UNSUPPORTED, "product: too many blocks of rows by out for one launch");
   DeviceScope scope(stream);
   if (scope.error() != hipSuccess) return fail_hip(scope.error(), "device");
   const int dev = scope.device();
-  ep::Groups g;
-  EP_CHECK(check_groups(dims, plan_ws, dev, &g));
+  EP_CHECK(check_plan(dims, plan_ws, dev));
   const int64_t rows = g.most == 0 ? 0 : dims.N * dims.cap, W = ep::weight_rows(*p);
   const Span sd{dout, 2 * rows * p->out, "dout"}, sx{x, 2 * rows * p->in, "x"},
       sp{pre, 2 * rows * W, "pre"}, sw{p->w, 2 * w_elems(dims, *p), "w"},

@@ -387,15 +387,17 @@ int64_t most_blocks(const Dims& d) {
 
 }  // namespace
 
-bool product_fits(const ep_product& p, const Dims& d) {
-  // The smallest tiles are 32 x 64 (columns of a SwiGLU tile), 32 x 256 in the
-  // elementwise part; no workgroup has more than 512 threads.
-  const int64_t rows = d.NTR > d.N * d.cap ? d.NTR : d.N * d.cap;
-  const int64_t most = (int64_t)1 << 23, W = weight_rows(p);
-  const int64_t tiles = (rows / 32 + d.E + 8) * ((p.out + 63) / 64);
-  const int64_t back = (rows / 32 + d.E + 8) * ((p.in + 127) / 128);
-  const int64_t weights = d.E * ((W + 127) / 128) * ((p.in + 127) / 128);
-  return tiles < most && back < most && weights < most;
+// A line's tiles are given to as many workgroups as there are; their numbers,
+// of 32 x 32 tiles at least, are 32-bit ones. 2^26 blocks of 32 x 64 are outputs
+// of 275 GB.
+bool line_fits(const Groups& g, int64_t cols) {
+  return room_of(g, 32) * ((cols + 63) / 64) < (int64_t)1 << 26;
+}
+
+// One workgroup per 32 rows by 256 columns, in a grid of fewer than 2^32 threads.
+bool act_grad_fits(const Groups& g, int64_t cols) {
+  return tile_grid(g, kChunkRows, (cols + kActCols - 1) / kActCols) * kActThreads <
+         (int64_t)1 << 32;
 }
 
 int64_t product_grad_bytes(const ep_product& p, const Dims& d) {

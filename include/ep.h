@@ -734,7 +734,12 @@ EP_API int ep_rms_norm_grad(const ep_norm *n, const void *dy, const void *h,
 #define EP_ACT_SWIGLU 3 /* y[j] = silu(z[j]) z[out + j]: gate rows of w, then up rows */
 
 /* The experts' matrices. W = out, or 2 out for EP_ACT_SWIGLU. `in` and `out`
- * are multiples of 8 (e4m3: of 128), in * W < 2^30, both below 2^20. */
+ * are multiples of 8 (e4m3: of 128), in * W < 2^30, both below 2^20.
+ * With B the blocks of 32 rows that the experts can have, B = min(N T topk,
+ * N cap) / 32 + E (N cap / 32 without a plan): B out / 64 < 2^26, for dx
+ * B in / 64 < 2^26, and in a backward pass with an activation or dbias
+ * B out / 256 < 2^24; else EP_ERR_UNSUPPORTED. Capacity beyond the slots costs
+ * memory only. */
 typedef struct ep_product {
   const void *w;        /* [E][W][in] */
   const float *w_scale; /* e4m3: fp32 [E][W / 128][in / 128]; else NULL */

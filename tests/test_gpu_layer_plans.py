@@ -134,3 +134,43 @@ def test_product_grad_of_broken_plans(n, t, e, r, cap, k, m, act, kind):
         lo, hi = off[:, :-1].flatten(), off[:, 1:].flatten()
         want = (torch.maximum(hi, lo) - lo).to(BF).cuda()
         assert (dw == want[:, None, None]).all()
+
+
+def test_default_capacity_far_beyond_the_slots():
+    """2,048 slots, a capacity for any routing of them: 2^21 rows, of which the experts have one or so each."""
+    note("product of a large default capacity")
+    n, t, e, r, k, m = 32, 32, 2048, 2, 64, 8192
+    d = ep.make_desc(n, t, 8, e, r)
+    cap = ep.capacity(d)
+    assert n * cap == 1 << 21
+    g = torch.Generator(device="cuda").manual_seed(3)
+    idx = torch.rand((n * t, e), generator=g, device="cuda").argsort(1)[:, :r].to(torch.int32).view(n, t, r)
+    plan = torch.zeros(ep.plan_bytes(d), dtype=torch.uint8, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    ep.plan(d, idx, plan, status)
+    off = group_offsets(d, plan).long()
+    assert int(off[:, -1].sum()) == n * t * r and int(status) == 0
+    w = torch.empty((e, m, k), dtype=BF, device="cuda").normal_(generator=g)
+    x = torch.zeros((n * cap, k), dtype=BF, device="cuda").normal_(generator=g)
+    out, dx = torch.empty((n * cap, m), dtype=BF, device="cuda"), torch.empty((n * cap, k), dtype=BF, device="cuda")
+    p = ep.make_product(w)
+    ep.expert_product(d, p, [x], plan, out)
+    # The outputs are the backward pass's dout: 34 GB of it are enough on the card.
+    dw, db = torch.empty_like(w), torch.empty((e, m), device="cuda")
+    ws = torch.empty(ep.expert_product_grad_bytes(d, p), dtype=torch.uint8, device="cuda")
+    ep.expert_product_grad(d, p, out, x, None, plan, ws, dx, dw, db)
+    torch.cuda.synchronize()
+    had = 0
+    for j in list(range(0, e, 97)) + [e - 1]:
+        a, b = (int(off[j // (e // n), j % (e // n) + i]) + j // (e // n) * cap for i in (0, 1))
+        had += b - a
+        x64, w64 = x[a:b].double(), w[j].double()
+        z, terms = x64 @ w64.T, x64.abs() @ w64.abs().T
+        # Sums of k products in 32 bits, (k + 8) 2^-23 of their terms, then half a step of bf16.
+        assert ((out[a:b].double() - z).abs() <= terms * (k + 8) * 2.0**-23 + z.abs() * 2.0**-7.99).all()
+        do = out[a:b].double()
+        for got, want, terms, count in ((dx[a:b], do @ w64, do.abs() @ w64.abs(), m),
+                                        (dw[j], do.T @ x64, do.abs().T @ x64.abs(), b - a)):
+            assert ((got.double() - want).abs() <= terms * (count + 8) * 2.0**-23 + want.abs() * 2.0**-7.99).all()
+        assert ((db[j].double() - do.sum(0)).abs() <= do.abs().sum(0) * (b - a + 8) * 2.0**-24).all()
+    assert had > 10
