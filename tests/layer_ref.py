@@ -103,3 +103,17 @@ def check(got, want, tol, what):
     assert not bad.any(), (what, int(bad.sum()), bad.nonzero()[:4].tolist(),
                            [(float(got[tuple(i)]), float(want[tuple(i)]), float(tol[tuple(i)]))
                             for i in bad.nonzero()[:4].tolist()])
+
+
+def guarded(shape, dtype, fill=7.0):
+    """A tensor between two guards of at least 64 KB, and a function that asserts that the guards are whole."""
+    count = 1
+    for s in shape:
+        count *= s
+    size = torch.empty(0, dtype=dtype).element_size()
+    edge = 65536 // size
+    whole = torch.full((count + 2 * edge,), fill, dtype=dtype, device="cuda")
+
+    def check():
+        assert (whole[:edge] == fill).all() and (whole[-edge:] == fill).all()
+    return whole[edge:-edge].view(shape), check

@@ -5,7 +5,7 @@ import torch
 
 import combine_ep_plan_amd as ep
 from gpu_util import note
-from layer_ref import BF
+from layer_ref import BF, guarded
 
 pytestmark = pytest.mark.gpu
 
@@ -55,20 +55,6 @@ def broken(kind, n, local, cap, g):
         "random rows": torch.randint(0, cap + 1, (local + 1,), generator=g),
     }[kind]
     return one.to(torch.int32).expand(n, -1).contiguous()
-
-
-def guarded(shape, dtype, fill=7.0):
-    """A tensor between two guards of at least 64 KB, and a function that asserts that the guards are whole."""
-    count = 1
-    for s in shape:
-        count *= s
-    size = torch.empty(0, dtype=dtype).element_size()
-    edge = 65536 // size
-    whole = torch.full((count + 2 * edge,), fill, dtype=dtype, device="cuda")
-
-    def check():
-        assert (whole[:edge] == fill).all() and (whole[-edge:] == fill).all()
-    return whole[edge:-edge].view(shape), check
 
 
 KINDS = ["all or nothing", "descending", "out of range", "one past another", "random", "random rows"]
