@@ -41,14 +41,19 @@ __device__ __forceinline__ uint32_t pack_bf16(float a, float b) {  // nearest ev
   return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{a, b}, bf16x2));
 }
 
+// Where exp(-z) passes the floats' range (z < -88.7) this is 0; the true value
+// times z is under 2^-120 there.
 __device__ __forceinline__ float sigmoid(float z) { return 1.0f / (1.0f + __expf(-z)); }
 
 // Density and distribution function of the standard normal distribution at z.
 // The tail beyond |z| is the density times Mills' ratio, which is smooth: a
 // polynomial in u = 1 / (1 + 0.3 |z|) fitted to it (least squares in the
-// relative error, reweighted towards its maximum) is within 2^-20 for all z,
-// also where the tail is far below 1. erfcf() takes 140 instructions and made
-// the 32 values of a thread 9 us of a small backward pass; this takes 20.
+// relative error, reweighted towards its maximum) is within 2^-20 of the ratio
+// for all z. The exponent a = z^2 / 2 adds its roundings, 2.3 a 2^-24 relative
+// in density and tail: of all bf16 z, GELU's slope is within 2^-20 of its terms
+// up to |z| = 5 and within 2^-18 up to 13, behind which the density is below
+// 2^-120. erfcf() takes 140 instructions and made the 32 values of a thread 9
+// us of a small backward pass; this takes 20.
 struct Normal {
   float density, below;
 };

@@ -728,6 +728,8 @@ EP_API int ep_rms_norm_grad(const ep_norm *n, const void *dy, const void *h,
                             const void *dsum, void *dx, float *dweight,
                             void *ws, hipStream_t stream);
 
+/* Activations are evaluated in 32 bits, within 2^-16 relative; one (or a slope)
+ * below 2^-120 may come out as 0. */
 #define EP_ACT_NONE 0   /* y = z */
 #define EP_ACT_SILU 1   /* y = z / (1 + exp(-z)) */
 #define EP_ACT_GELU 2   /* y = z (1 + erf(z / sqrt(2))) / 2 */
