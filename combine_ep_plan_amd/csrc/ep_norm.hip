@@ -12,8 +12,10 @@
 // thread; the 16 lanes of a DPP row hold one 128-value block of the codes.
 //
 // 32768 rows of 7168 bf16 values: forward with residual and codes 365 us (2.12
-// GB, 5.8 TB/s), backward 311 + 5 us (1.88 GB, 6.0 TB/s); a copy of 4 GiB runs
-// at 4.5 to 4.9 TB/s. One row: 3.6 us, a launch.
+// GB, 5.8 TB/s), backward 311 to 318 + 5 us (1.88 GB, 5.9 to 6.0 TB/s); a copy
+// of 4 GiB runs at 4.5 to 4.9 TB/s. One row: 3.5 us, a launch. 4096 rows of 16384
+// and of 32768 values: forward 100 and 218 us (6.0 and 5.5 TB/s), backward 100
+// and 258 us (5.4 and 4.2: see the four chunks of the backward pass).
 #include "ep_device.hpp"
 #include "ep_kernels.hpp"
 #include "ep_quant_device.hpp"
@@ -206,7 +208,10 @@ __global__ __launch_bounds__(THREADS) void norm_grad_kernel(const u32x4* dy, con
     block_sum(s, room[turn]);  // two rooms in turn: one barrier per row is enough
     const float rs = rsqrtf(s[0] * per + eps);
     const float k = rs * rs * s[1] * per;
-    if constexpr (V > 2) {  // unpacked anew, not kept: 107 registers would not fit
+    // Unpacked anew, not kept: of 1024 threads each has 128 registers, and 107 more
+    // do not fit. The packed row and dweight of four chunks pass them all the same:
+    // 31 to 33 registers, 80 bytes a lane, are spilled.
+    if constexpr (V > 2) {
 #pragma unroll
       for (int i = 0; i < V; ++i) asm volatile("" : "+v"(h0[i]), "+v"(d0[i]), "+v"(wt[i]));
     }

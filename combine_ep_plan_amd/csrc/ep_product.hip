@@ -2,11 +2,16 @@
 // epilogue applied to the 32-bit sums in registers.
 //
 // Few rows an expert: the weights' way from HBM bounds it. 256 experts of 128
-// rows (7168 values to 2048 by SwiGLU): 3.1 ms, 15.6 GB at 5.0 TB/s. Many rows:
-// the matrix units are busy half of the time, and wait for operands from L2 and
-// behind it the other half; 256 experts of 1024 rows 1.29 PFLOP/s in bf16, 1.8
-// in e4m3, where the 32-bit sums of 128 products are scaled on the vector units
-// as well. One dense product of 16,384 rows: 1.36 PFLOP/s.
+// rows (7168 values to 2048 by SwiGLU): 3.1 ms, 15.6 GB at 5.0 TB/s; e4m3 1.7 ms.
+// Many rows: the matrix units are busy 62 % (e4m3 50 %) of the time, and wait for
+// operands from L2 and behind it in the rest. 256 experts of about 1024 rows take 13.6
+// ms in bf16 (1.13 PFLOP/s) and 8.1 to 8.4 in e4m3 (1.8 to 1.9); of exactly 1024
+// each 11.9 (1.29) and 7.3 (2.1), and read 23 and 11 GB where random sizes read
+// 43 and 29: likely neighbouring tiles of different heights leave step over 56 or
+// 112 steps of k and no longer find each other's operands in L2. e4m3's scaling, 128
+// FMAs beside 32 matrix instructions a step, is about half the matrix work. One
+// dense product of 16,384 rows of 7168 to 8192: 1.41 to 1.50 ms, 1.28 to 1.37
+// PFLOP/s.
 #include "ep_product_device.hpp"
 
 namespace ep {
@@ -163,7 +168,11 @@ hipError_t run(FwdArgs a, int act, hipStream_t stream) {
 template <int FR, bool FP8, int STAGES, bool ONCE = true>
 using Rows = Shape<2, FR, 4, 4, false, false, FP8, STAGES, ONCE>;
 
-// Tiles of fewer rows and columns, with more steps on their way.
+// Tiles of fewer rows and columns, with more steps on their way. In e4m3 the
+// compiler has the matrix instruction write accumulator registers here (one
+// wave a SIMD leaves it those), and every sum is moved out for its scaling: 64
+// moves beside 64 FMAs in a step of 128 x 128, 32 beside 32 in the others. 1 to
+// 128 rows of 7168 values by 4096 columns: 32 us, bf16 38 to 40.
 template <bool FP8>
 using Small = Shape<2, 4, 2, 4, false, false, FP8, 4>;        // 128 x 128
 template <bool FP8>
@@ -172,9 +181,9 @@ template <bool FP8>
 using Thin = Shape<1, 2, 1, 4, false, false, FP8, 5, true>;   // 32 x 64
 
 // The tiles that cost least, of equals the smallest. Rows of 7168 values by
-// 4096 columns: 2048 rows take 173 us in the large ones and 138 in 128 x 128; 256
-// rows 178, 71, 52 and 73 in the four; 64 rows 91, 60, 51 and 38. 2048 rows of
-// 2048 values by 7168 columns: 62, 84, 187 and 307.
+// 4096 columns: 2048 rows take 150 us in the large ones and 125 in 128 x 128; 256
+// rows 126, 53, 50 and 74 in the four; 64 rows 89, 46, 49 and 38. 2048 rows of
+// 2048 values by 7168 columns: 54, 69, 189 and 315.
 template <bool FP8>
 hipError_t by_cost(const FwdArgs& a, int act, hipStream_t stream) {
   using Large = Rows<8, FP8, 2, false>;

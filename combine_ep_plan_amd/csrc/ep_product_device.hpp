@@ -685,14 +685,14 @@ struct Line {
 };
 
 // What a kernel with tiles of br x bc takes, in units that compare kernels: a
-// CU takes in operands at about 45 GB/s whatever the tile (32 x 64: 36, 32 x
-// 128: 45, 128 x 128: 52, 256 x 256: 41 at 256 to 8192 rows of 7168 values),
-// so the time goes by the rounds of 256 tiles and by the rows and columns that
-// each takes in. The groups are taken to have the mean size, if routed and two
-// standard deviations of a random count (a group that just passes a tile reads
-// its weights twice: 32 rows on average take 3.2 ms in tiles of 32 rows and 2.2
-// in those of 64). rows: of a tile in steps of which the kernel skips rows that
-// are not there.
+// CU takes in operands at about 45 GB/s whatever the tile (7168 values by 4096
+// columns, 32 x 64 with 64 rows: 36, 32 x 128 with 256: 46, 128 x 128 with 2048:
+// 58, 256 x 256 with 2048 and 8192: 49 and 37), so the time goes by the rounds of
+// 256 tiles and by the rows and columns that each takes in. The groups are taken
+// to have the mean size, if routed and two standard deviations of a random count
+// (a group that just passes a tile reads its weights twice: 32 rows on average
+// take 3.2 ms in tiles of 32 x 128 and 2.2 to 2.4 in those of 64 x 256). rows: of
+// a tile in steps of which the kernel skips rows that are not there.
 inline int64_t cost_of(const Groups& g, int br, int rows, int bc, int64_t cols) {
   const int64_t experts = (int64_t)g.N * g.L, groups = experts < g.most ? experts : g.most;
   if (groups == 0) return 0;

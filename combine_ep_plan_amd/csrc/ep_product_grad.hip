@@ -32,8 +32,10 @@ __device__ __forceinline__ void store4(uint16_t* p, const float (&v)[4]) {
 }
 
 // dz of a block of rows and columns, and the columns' sums over the rows: wave
-// w takes rows w, w + 4, ... HBM bounds it:
-// 65,536 rows of 2048 + 4096 values to 4096 in 263 us, 5.1 TB/s.
+// w takes rows w, w + 4, ... HBM bounds it: 65,536 rows of 2048 + 4096 values to
+// 4096 in 262 us, 5.1 TB/s. A small layer (333 tokens of 6 experts, 264 columns)
+// takes 11 us, a chain: the offsets, their sum, two batches of loads, the offsets
+// again for the parts' place.
 template <int ACT>
 __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   constexpr bool glu = ACT == EP_ACT_SWIGLU;
@@ -47,8 +49,8 @@ __global__ __launch_bounds__(kActThreads) void act_grad_kernel(ActArgs a) {
   float s[glu ? 2 : 1][4] = {};
   if (c < a.n) {
     // Rows of a wave on their way at once: a sum alone (no activation) reads 65,536
-    // rows in 51 us with all eight and 56 with four; where dz is written, four take
-    // 5 to 8 % less (GELU, with the product behind it: 217 against 235 us).
+    // rows of 2048 in 54 us with all eight and 55 with four; where dz is written,
+    // four take 5 to 9 % less (GELU 173 against 190 us, SwiGLU 249 against 261).
     constexpr int some = ACT == EP_ACT_NONE ? steps : 4;
 #pragma unroll 1
     for (int i0 = 0; i0 < steps; i0 += some) {
@@ -166,9 +168,9 @@ __global__ __launch_bounds__(COLS * GROUPS) void bias_kernel(const float* parts,
   dbias[(int64_t)e * W + c] = s;
 }
 
-// Many parts per expert (65,536 rows of one: 2048) need many lanes a column,
-// 50 against 540 us; few (64 experts of 1024 rows: 32) are one batch of loads
-// for four lanes, 11 us against 56.
+// Many parts per expert (65,536 rows of one: 2048, of 4096 columns) need many
+// lanes a column, 11 against 43 us; few (64 experts of 1024 rows: 32) are one
+// batch of loads for four lanes, 11 us against 74.
 hipError_t run_bias(const float* parts, int64_t most, const Groups& g, float* dbias, int W,
                     hipStream_t stream) {
   const int experts = g.N * g.L;
@@ -219,9 +221,11 @@ using RowsShape = Shape<2, FR, 4, 4, false, true, false, 2, ONCE>;
 using RowsSmall = Shape<2, 4, 2, 4, false, true, false, 4>;       // 128 x 128
 using RowsFlat = Shape<1, 2, 2, 4, false, true, false, 4, true>;  // 32 x 128
 
-// 64 experts of 1024 rows, W 4096, in 7168: dx 3.37 ms, dw 3.56 ms, 1.14 and
-// 1.08 PFLOP/s; the matrix units are busy 60 and 56 % of the time. As in the
-// forward pass a CU's intake of operands is what the steps wait for.
+// 64 experts of about 1024 rows, W 4096, in 7168: dx 3.42 ms, dw 3.58 ms, 1.12
+// and 1.07 PFLOP/s; the matrix units are busy 60 and 56 % of the time. As in the
+// forward pass a CU's intake of operands is what the steps wait for, and groups of
+// exactly 1024 rows (dx 3.17 against 3.54 ms) read 9 GB where random sizes read
+// 18. The 256-row kernel spills 13 registers, outside its steps.
 //
 // dx[r][c] = sum over n of dz[r][n] w[n][c], for tiles of more than MIN and at
 // most S::BR rows, from t on, while the line has such ones. Returns whether t is
@@ -410,7 +414,7 @@ hipError_t launch_product_grad(const ep_product& p, const Dims& d, const Groups&
                                const uint16_t* dout, const uint16_t* x, const uint16_t* pre,
                                void* ws, uint16_t* dx, uint16_t* dw, float* dbias,
                                hipStream_t stream) {
-  const int W = (int)weight_rows(p), experts = d.E;
+  const int W = (int)weight_rows(p);
   const bool none = p.act == EP_ACT_NONE;
   ActArgs act;
   act.dout = dout;

@@ -2,9 +2,9 @@
 //
 // With out = sum_k w_k y_k over a token's slots k, the gradients are
 // dy_k = w_k dout and dw_k = dout . y_k. With grouped row = x of its token,
-// dx = sum_k dgrouped_k. HBM bounds both: a token's dout is read once and
-// stays in registers for its R expert rows, each of which is read once, in
-// whole rows wherever the plan put them.
+// dx = sum_k dgrouped_k. HBM bounds both: each expert row is read once, in whole
+// rows wherever the plan put them, and a token's dout comes from HBM once (the
+// combine kernel reads it anew for every four slots, then from the caches).
 //
 // One workgroup per token, V chunks of 8 values (16 bytes) per thread.
 //

@@ -755,8 +755,9 @@ typedef struct ep_product {
 /* Grouped product ("Dispatch and combine": the grouped GEMM between dispatch
  * and combine): for every delivered row i of expert e,
  *   z = x[i] w[e]^T + bias[e], out[i] = act(z) + residual[i].
- * Of the descriptor only N, E and cap matter: rows have the product's own
- * widths. x: bf16 [N][cap][in] in x[0]; or e4m3 codes in x[0] and their scales
+ * With a plan the descriptor is the plan's (N, E, T and topk place its
+ * offsets), without one only N, E and cap matter; rows have the product's own
+ * widths, whatever its hidden and payload. x: bf16 [N][cap][in] in x[0]; or e4m3 codes in x[0] and their scales
  * [N][cap][in / 128] in x[1], as a block-fp8 dispatch delivers them (a value is
  * code * scale, and w's the same by blocks of 128 x 128; products of 128 codes
  * are summed first, then scaled. The matrix unit adds 8 neighbouring products
